@@ -82,6 +82,7 @@ extern "C" {
 #define PAGED_ATTN_ERR_SCALE (-8)      /* scale is not finite */
 #define PAGED_ATTN_ERR_STATIC_SCRATCH (-9) /* sizes exceed paged_attn_decode_static's scratch */
 #define PAGED_ATTN_ERR_FLAGS (-10)     /* unknown bits in paged_attn_set_launch_flags */
+#define PAGED_ATTN_ERR_MODS (-11)      /* softcap negative or not finite, or window negative */
 
 /* Launch flags (paged_attn_set_launch_flags). */
 #define PAGED_ATTN_FLAG_EARLY_PROLOGUE 1
@@ -420,6 +421,136 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
                                                 const int32_t* seq_lens, int num_seqs, int H_q,
                                                 int H_kv, int head_dim, int max_blocks_per_seq,
                                                 int block_size, float scale, void* stream);
+
+/*
+ * Decode with score options, for the layers whose scores are not the plain
+ * scaled products.  The query of sequence s stands at position pos = L - 1 (L
+ * = seq_lens[s], clamped as in paged_attn_decode) and
+ *
+ *   x(h, t) = scale * q[s, h, :] . K_t
+ *   x       = softcap * tanh(x / softcap)            softcap > 0 (0: off)
+ *   x       = x - alibi_slopes[h] * |pos - t|        alibi_slopes non-null
+ *   out[s, h, :] = sum_t softmax_t(x) V_t over the tokens t < L that it sees:
+ *       t < prefix_lens[s]   or
+ *       t >= doc_starts[s]  and  (window == 0 or t > pos - window)
+ *
+ *   alibi_slopes  [H_q]       float32  (read; null: no distance bias)
+ *   window        tokens the query sees at most, itself included (0: all)
+ *   prefix_lens   [num_seqs]  int32    (read; null: 0) a prefix that every query
+ *                 sees whatever the window and the documents (an attention sink,
+ *                 a prefix language model's prefix)
+ *   doc_starts    [num_seqs]  int32    (read; null: 0) the first token of the
+ *                 document the query is in, in a sequence that packs several
+ *
+ * prefix_lens and doc_starts are clamped to [0, L].  A query that sees no token
+ * gets a zero row.  Pages that hold no token the query sees are not read (their
+ * table entries neither), and unseen rows of the pages that are may hold
+ * anything, NaN included.  The arrays are 4-byte aligned device (or pinned
+ * host) memory.  The cap is computed in float32 to about 1e-6 of the score, the
+ * bias as one float32 multiply-add on top of it; everything else is
+ * paged_attn_decode's.
+ *
+ * workspace: at least paged_attn_mods_workspace_bytes(...) bytes, 256-byte
+ * aligned, zero-filled before its first use, not shared by calls that may
+ * overlap; or null, for a workspace the library owns, as paged_attn_decode's
+ * (its own one, so calls of the two kinds may overlap).  A stream that is
+ * being captured must pass one: with a null workspace the call returns
+ * PAGED_ATTN_ERR_WORKSPACE there.  Launch flags do not apply.
+ */
+PAGED_ATTN_API int paged_attn_decode_mods(const void* q, const void* k_cache,
+                                          const void* v_cache, void* out,
+                                          const int32_t* block_tables, const int32_t* seq_lens,
+                                          int num_seqs, int H_q, int H_kv, int head_dim,
+                                          int max_blocks_per_seq, int block_size, float scale,
+                                          float softcap, const float* alibi_slopes, int window,
+                                          const int32_t* prefix_lens, const int32_t* doc_starts,
+                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same over FP8 caches (paged_attn_decode_fp8: head_dim 128 or 256). */
+PAGED_ATTN_API int paged_attn_decode_fp8_mods(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, void* out, const int32_t* block_tables, const int32_t* seq_lens,
+    int num_seqs, int H_q, int H_kv, int head_dim, int max_blocks_per_seq, int block_size,
+    float scale, float softcap, const float* alibi_slopes, int window,
+    const int32_t* prefix_lens, const int32_t* doc_starts, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace paged_attn_decode_mods and paged_attn_decode_fp8_mods need for
+ * these sizes on the CURRENT device; 0 for unsupported sizes. */
+PAGED_ATTN_API size_t paged_attn_mods_workspace_bytes(int num_seqs, int H_q, int H_kv,
+                                                      int head_dim, int max_blocks_per_seq,
+                                                      int block_size);
+
+/*
+ * Block tables, query offsets and the slot map of a serving step, built on the
+ * GPU from request lengths.  Sequence s holds seq_lens[s] tokens and new_lens[s]
+ * arrive, as the rows qo_indptr[s] .. qo_indptr[s+1] - 1 of the step's packed
+ * batch (qo_indptr: the running sum of new_lens, row 0 first).  The pages its
+ * new tokens begin take blocks from the top of the free stack, in the order of
+ * the sequences and of their pages:
+ *
+ *   need[s]  = ceil((seq_lens[s] + new_lens[s]) / block_size) - ceil(seq_lens[s] / block_size)
+ *   block k of the call = free_blocks[free_count - 1 - k]
+ *   slot_map[qo_indptr[s] + i] = block * block_size + t % block_size,  t = seq_lens[s] + i
+ *
+ *   seq_lens, new_lens  [num_seqs]  int32  (read)
+ *   block_tables   [num_seqs, max_blocks_per_seq]  int32: the entries of the fresh
+ *                  pages are written, the others are left (and the last page's
+ *                  read, when tokens join it)
+ *   free_blocks    [free_capacity]  int32  (read), free_count [1] int32 (read;
+ *                  clamped to [0, free_capacity])
+ *   seq_lens_out   [num_seqs]  int32: seq_lens + new_lens; may be seq_lens itself
+ *   qo_indptr      [num_seqs + 1]  int32 (written)
+ *   slot_map       [max_new]  int64 (written whole: -1 past the last row)
+ *   free_count_out [1] int32: what is left; may be free_count itself
+ *   refused        [1] int32, or null: how many sequences were refused
+ *
+ * A sequence is refused when its blocks and those of the sequences before it do
+ * not all fit in the free stack, when its tokens do not fit its table row or
+ * its rows do not fit in max_new, or when a length is negative (its rows count
+ * as 0 then).  It takes no block, keeps its length (seq_lens_out) and its table
+ * row, and its rows get slots of -1; sequences that need no block are served
+ * whatever is free.  Other outputs must not overlap inputs.
+ *
+ * max_new bounds the sum of new_lens, so that a captured step serves any batch
+ * of up to that many rows.  Any number of sequences; max_blocks_per_seq and
+ * block_size as paged_attn_decode.  The tensors are 16-byte aligned, the
+ * one-element ones 4-byte.  With paged_attn_set_checks on, a block id outside the
+ * pool sets bit 0 and an invalid length bit 1 of the status word (such an id is
+ * still assigned).  One launch; no workspace; asynchronous on `stream`.
+ */
+PAGED_ATTN_API int paged_kv_assign(const int32_t* seq_lens, const int32_t* new_lens,
+                                   int32_t* block_tables, const int32_t* free_blocks,
+                                   const int32_t* free_count, int32_t* seq_lens_out,
+                                   int32_t* qo_indptr, int64_t* slot_map,
+                                   int32_t* free_count_out, int32_t* refused, int num_seqs,
+                                   int max_blocks_per_seq, int block_size, int free_capacity,
+                                   int max_new, void* stream);
+
+/*
+ * Cache append by slot: row r of the new tokens goes to slot_map[r] = block *
+ * block_size + place, for every KV head g
+ *
+ *   k_cache[block, g, place, :] = k_new[r, g, :]      (v alike)
+ *
+ * so that it needs neither tables nor lengths (paged_kv_assign makes the map).
+ *
+ *   k_new, v_new  row r begins k_stride (v_stride) elements after row r - 1 and
+ *                 holds [H_kv, head_dim] bf16: slices of one fused projection
+ *                 need no copy; strides are multiples of 8, at least H_kv * head_dim
+ *   slot_map      [rows]  int64 (read).  A slot outside [0, num_blocks * block_size)
+ *                 writes nothing (-1: a padding row); with paged_attn_set_checks on, one
+ *                 past the pool sets bit 0 of the status word.
+ *
+ * The slots of a call must be distinct: of two rows with the same slot either
+ * may remain, in pieces of 16 bytes.  num_blocks is the pool's size, in [1, 2^31).
+ * Sizes and errors as paged_kv_append.  Asynchronous; allocates nothing.
+ */
+PAGED_ATTN_API int paged_kv_append_slots(const void* k_new, const void* v_new,
+                                         long long k_stride, long long v_stride, void* k_cache,
+                                         void* v_cache, const int64_t* slot_map, int rows,
+                                         int H_kv, int head_dim, int block_size,
+                                         long long num_blocks, void* stream);
 
 /* Human-readable text for a PAGED_ATTN_* code (static storage). */
 PAGED_ATTN_API const char* paged_attn_status_string(int status);

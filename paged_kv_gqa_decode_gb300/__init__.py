@@ -30,6 +30,11 @@ __all__ = [
     "paged_attn_append_decode_multi",
     "paged_kv_append_fp8",
     "paged_attn_append_decode_fp8",
+    "paged_attn_decode_mods",
+    "paged_attn_decode_fp8_mods",
+    "paged_attn_mods_workspace_bytes",
+    "paged_kv_assign",
+    "paged_kv_append_slots",
     "paged_attn_workspace_bytes",
     "paged_attn_status_string",
     "paged_attn_set_launch_flags",
@@ -59,6 +64,11 @@ EXPORTED_SYMBOLS = (
     "paged_attn_append_decode_multi",
     "paged_kv_append_fp8",
     "paged_attn_append_decode_fp8",
+    "paged_attn_decode_mods",
+    "paged_attn_decode_fp8_mods",
+    "paged_attn_mods_workspace_bytes",
+    "paged_kv_assign",
+    "paged_kv_append_slots",
     "paged_attn_status_string",
     "paged_attn_set_launch_flags",
     "paged_attn_set_checks",
@@ -129,6 +139,17 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.paged_attn_append_decode_fp8.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, I, I,
                                                      I, F, P]
         lib.paged_attn_append_decode_fp8.restype = I
+        mods = [F, P, I, P, P, P, SZ, P]  # softcap .. doc_starts, workspace, stream
+        lib.paged_attn_decode_mods.argtypes = common + mods
+        lib.paged_attn_decode_mods.restype = I
+        lib.paged_attn_decode_fp8_mods.argtypes = [P, P] + common + mods
+        lib.paged_attn_decode_fp8_mods.restype = I
+        lib.paged_attn_mods_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        lib.paged_attn_mods_workspace_bytes.restype = SZ
+        lib.paged_kv_assign.argtypes = [P] * 10 + [I, I, I, I, I, P]
+        lib.paged_kv_assign.restype = I
+        lib.paged_kv_append_slots.argtypes = [P, P, LL, LL, P, P, P, I, I, I, I, LL, P]
+        lib.paged_kv_append_slots.restype = I
         lib.paged_attn_set_checks.argtypes = [LL, P]
         lib.paged_attn_set_checks.restype = I
         lib.paged_attn_reset_workspace.argtypes = [P]
@@ -479,3 +500,199 @@ def paged_attn_append_decode_fp8(q, k_new, v_new, k8, v8, k_scale, v_scale, bloc
                                                _ptr(k_scale), _ptr(v_scale), a[3], *a[4:],
                                                _stream(stream)))
     return out
+
+
+def _same_device(tensors) -> None:
+    """CUDA tensors must lie on the current device (whose stream the call uses);
+    a host tensor must be pinned."""
+    import torch
+
+    current = -1
+    for t in tensors:
+        if t is None:
+            continue
+        if t.is_cuda:
+            if current < 0:
+                current = torch.cuda.current_device()
+            if t.get_device() != current:
+                raise ValueError("every tensor must be on the current CUDA device")
+        elif not t.is_pinned():
+            raise ValueError("host tensors must be pinned")
+
+
+def _need(name, t, dtype, shape) -> None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _mods_problem(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
+                  doc_starts, workspace, cache_dtype, rows=None):
+    """Checks the tensors of a decode call with score options; returns the sizes and out."""
+    import torch
+
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
+        raise ValueError("q must be [rows, H_q, D], the caches [num_blocks, H_kv, block_size, D], "
+                         "block_tables [num_seqs, max_blocks] and seq_lens [num_seqs]")
+    n, H_q, D = q.shape
+    nb, H_kv, BS, Dk = k_cache.shape
+    num_seqs = seq_lens.shape[0]
+    if Dk != D:
+        raise ValueError("q and the caches disagree on head_dim")
+    if rows is None and n != num_seqs:
+        raise ValueError("q must have one row per sequence")
+    maxb = block_tables.shape[1]
+    _need("q", q, torch.bfloat16, (n, H_q, D))
+    _need("k_cache", k_cache, cache_dtype, (nb, H_kv, BS, D))
+    _need("v_cache", v_cache, cache_dtype, (nb, H_kv, BS, D))
+    _need("block_tables", block_tables, torch.int32, (num_seqs, maxb))
+    _need("seq_lens", seq_lens, torch.int32, (num_seqs,))
+    if alibi_slopes is not None:
+        _need("alibi_slopes", alibi_slopes, torch.float32, (H_q,))
+    if prefix_lens is not None:
+        _need("prefix_lens", prefix_lens, torch.int32, (num_seqs,))
+    if doc_starts is not None:
+        _need("doc_starts", doc_starts, torch.int32, (n,))
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need("out", out, torch.bfloat16, (n, H_q, D))
+    _same_device((q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
+                  doc_starts, workspace))
+    return n, num_seqs, H_q, H_kv, D, maxb, BS, out
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def paged_attn_decode_mods(q, k_cache, v_cache, block_tables, seq_lens, scale: float, *,
+                           softcap: float = 0.0, alibi_slopes=None, window: int = 0,
+                           prefix_lens=None, doc_starts=None, out=None, workspace=None,
+                           stream=None):
+    """Decode with capped scores, a distance bias, a window, a prefix and documents (see
+    paged_attn.h): a query at position L - 1 sees token t when t < prefix_lens[s], or
+    when t >= doc_starts[s] and t > L - 1 - window (window 0: none), with the score
+    softcap * tanh(scale * q.k / softcap) - alibi_slopes[h] * (L - 1 - t).
+    ``workspace``: a zero-initialised uint8 tensor of paged_attn_mods_workspace_bytes,
+    needed while a stream is being captured."""
+    import torch
+
+    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+        q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
+        workspace, torch.bfloat16)
+    _check(load().paged_attn_decode_mods(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
+        float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens), _ptr(doc_starts),
+        _ptr(workspace), _bytes(workspace), _stream(stream)))
+    return out
+
+
+def paged_attn_decode_fp8_mods(q, k8, v8, k_scale, v_scale, block_tables, seq_lens,
+                               scale: float, *, softcap: float = 0.0, alibi_slopes=None,
+                               window: int = 0, prefix_lens=None, doc_starts=None, out=None,
+                               workspace=None, stream=None):
+    """paged_attn_decode_mods over FP8 caches (as paged_attn_decode_fp8; head_dim 128 or 256)."""
+    import torch
+
+    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+        q, k8, v8, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts, workspace,
+        torch.uint8)
+    _need("k_scale", k_scale, torch.float32, k8.shape[:3])
+    _need("v_scale", v_scale, torch.float32, k8.shape[:3])
+    _same_device((k_scale, v_scale))
+    _check(load().paged_attn_decode_fp8_mods(
+        q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS,
+        float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
+        _ptr(doc_starts), _ptr(workspace), _bytes(workspace), _stream(stream)))
+    return out
+
+
+def paged_attn_mods_workspace_bytes(num_seqs: int, H_q: int, H_kv: int, head_dim: int,
+                                    max_blocks_per_seq: int, block_size: int) -> int:
+    return int(load().paged_attn_mods_workspace_bytes(num_seqs, H_q, H_kv, head_dim,
+                                                      max_blocks_per_seq, block_size))
+
+
+def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, block_size: int,
+                    max_new: int, *, seq_lens_out=None, qo_indptr=None, slot_map=None,
+                    free_count_out=None, refused=None, stream=None):
+    """Block tables, query offsets and the slot map of a serving step from request
+    lengths (see paged_attn.h).  seq_lens, new_lens: int32 [num_seqs]; block_tables:
+    int32 [num_seqs, max_blocks], whose entries of fresh pages are written;
+    free_blocks: int32, a stack whose top is at free_count[0] - 1; max_new: rows of
+    the slot map, at least the sum of new_lens.  Returns (seq_lens_out, qo_indptr,
+    slot_map, free_count_out), made here unless passed; seq_lens_out may be seq_lens
+    and free_count_out free_count, to update them in place.  ``refused``: an int32
+    tensor of one element that receives the number of sequences refused."""
+    import torch
+
+    n = seq_lens.shape[0]
+    i32 = torch.int32
+    _need("seq_lens", seq_lens, i32, (n,))
+    _need("new_lens", new_lens, i32, (n,))
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    _need("block_tables", block_tables, i32, (n, block_tables.shape[1]))
+    _need("free_blocks", free_blocks, i32, (free_blocks.numel(),))
+    _need("free_count", free_count, i32, (1,))
+    dev = seq_lens.device
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens)
+    else:
+        _need("seq_lens_out", seq_lens_out, i32, (n,))
+    if qo_indptr is None:
+        qo_indptr = torch.empty(n + 1, dtype=i32, device=dev)
+    else:
+        _need("qo_indptr", qo_indptr, i32, (n + 1,))
+    if slot_map is None:
+        slot_map = torch.empty(max_new, dtype=torch.int64, device=dev)
+    else:
+        _need("slot_map", slot_map, torch.int64, (max_new,))
+    if free_count_out is None:
+        free_count_out = torch.empty_like(free_count)
+    else:
+        _need("free_count_out", free_count_out, i32, (1,))
+    if refused is not None:
+        _need("refused", refused, i32, (1,))
+    _same_device((seq_lens, new_lens, block_tables, free_blocks, free_count, seq_lens_out,
+                  qo_indptr, slot_map, free_count_out, refused))
+    _check(load().paged_kv_assign(
+        seq_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
+        free_blocks.data_ptr(), free_count.data_ptr(), seq_lens_out.data_ptr(),
+        qo_indptr.data_ptr(), slot_map.data_ptr(), free_count_out.data_ptr(), _ptr(refused), n,
+        block_tables.shape[1], int(block_size), free_blocks.numel(), int(max_new),
+        _stream(stream)))
+    return seq_lens_out, qo_indptr, slot_map, free_count_out
+
+
+def paged_kv_append_slots(k_new, v_new, k_cache, v_cache, slot_map, stream=None):
+    """Write new K and V rows into the paged caches by slot (see paged_attn.h).
+    k_new, v_new: bf16 [rows, H_kv, head_dim], each row contiguous, the rows at any
+    stride that is a multiple of 8 (slices of a fused projection need no copy);
+    slot_map: int64 [rows], block * block_size + place, or -1 to skip the row."""
+    import torch
+
+    if k_cache.dim() != 4 or k_new.dim() != 3:
+        raise ValueError("k_new must be [rows, H_kv, D], the caches [num_blocks, H_kv, "
+                         "block_size, D]")
+    nb, H_kv, BS, D = k_cache.shape
+    rows = k_new.shape[0]
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, H_kv, D):
+            raise ValueError(f"{name} must be bfloat16 [rows, H_kv, head_dim]")
+        if rows and (t.stride(2) != 1 or (H_kv > 1 and t.stride(1) != D)):
+            raise ValueError(f"the rows of {name} must be contiguous [H_kv, head_dim]")
+    _need("k_cache", k_cache, torch.bfloat16, (nb, H_kv, BS, D))
+    _need("v_cache", v_cache, torch.bfloat16, (nb, H_kv, BS, D))
+    _need("slot_map", slot_map, torch.int64, (rows,))
+    _same_device((k_new, v_new, k_cache, v_cache, slot_map))
+    row = H_kv * D
+    _check(load().paged_kv_append_slots(
+        k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0) if rows > 1 else row,
+        v_new.stride(0) if rows > 1 else row, k_cache.data_ptr(), v_cache.data_ptr(),
+        slot_map.data_ptr(), rows, H_kv, D, BS, nb, _stream(stream)))

@@ -21,10 +21,12 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB_NAME = "libpaged_kv_gqa_decode.so"
 LIB_PATH = os.path.join(LIB_DIR, LIB_NAME)
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["paged_attn_api.cu", "append.cu", "decode_d64.cu", "decode_d128.cu",
+SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d64.cu", "decode_d128.cu",
            "decode_d256.cu", "decode_fp8_d128.cu", "decode_fp8_d256.cu", "decode_xp_d64.cu",
            "decode_xp_d128.cu", "decode_xp_d256.cu", "decode_multi_d64.cu",
-           "decode_multi_d128.cu", "decode_multi_d256.cu"]
+           "decode_multi_d128.cu", "decode_multi_d256.cu", "decode_mod_d64.cu",
+           "decode_mod_d128.cu", "decode_mod_d256.cu", "decode_fp8_mod_d128.cu",
+           "decode_fp8_mod_d256.cu"]
 
 
 def nvcc() -> str:
@@ -99,7 +101,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
 # a wait run out (a ring slot left without its copy, a combiner waiting for one
 # more published part than exists).  Never loaded by the product path.
 WAIT_TEST_LIB = os.path.join(LIB_DIR, "libpaged_kv_gqa_decode_waittest.so")
-WAIT_TEST_SOURCES = ["paged_attn_api.cu", "append.cu", "decode_d128.cu"]
+WAIT_TEST_SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d128.cu"]
 WAIT_TEST_DEFINES = ["-DPAGED_ATTN_WAIT_TEST", "-DPAGED_ATTN_MBAR_SLEEPS=(1u<<14)",
                      "-DPAGED_ATTN_PUBLISH_POLLS=(1u<<15)"]
 

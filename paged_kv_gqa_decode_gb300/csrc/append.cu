@@ -135,6 +135,50 @@ __global__ void __launch_bounds__(256) paged_kv_append_fp8_kernel(const AppendPa
   }
 }
 
+// Rows by slot: one thread moves kSlotUnroll 16-byte chunks, each chunk a whole
+// grid apart from the next, so neighbouring threads read and write neighbouring
+// chunks and every thread keeps that many loads in flight.
+constexpr int kSlotUnroll = 4;
+
+__global__ void __launch_bounds__(256) paged_kv_append_slots_kernel(const AppendSlotsParams a) {
+  const int chunks_per_row = a.D / 8;
+  const int half = a.H_kv * chunks_per_row;  // 16-byte chunks of one new K (or V) row
+  const long long total = (long long)a.rows * 2 * half;
+  const long long grid = (long long)gridDim.x * blockDim.x;
+  const long long slots = a.num_blocks * a.BS;
+  const int shift = a.BS == 32 ? 5 : 4;
+  for (long long c0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; c0 < total;
+       c0 += grid * kSlotUnroll) {
+    uint4 x[kSlotUnroll];
+    uint4* dst[kSlotUnroll];
+#pragma unroll
+    for (int u = 0; u < kSlotUnroll; ++u) {
+      const long long c = c0 + u * grid;
+      dst[u] = nullptr;
+      if (c >= total) continue;
+      // (32-bit division where it fits: the 64-bit one is a long sequence)
+      const int r = total <= 0xffffffffLL ? (int)((uint32_t)c / (uint32_t)(2 * half))
+                                          : (int)(c / (2 * half));
+      const int rem = (int)(c - (long long)r * (2 * half));
+      const bool is_v = rem >= half;
+      const int at = is_v ? rem - half : rem;    // chunk of the row's [H_kv, D]
+      const long long slot = __ldg(reinterpret_cast<const long long*>(a.slot_map) + r);
+      if (slot < 0 || slot >= slots) {
+        if (slot >= slots && a.status != nullptr) atomicOr(a.status, 1);
+        continue;
+      }
+      const int g = at / chunks_per_row, ch = at - g * chunks_per_row;
+      const long long row = ((slot >> shift) * a.H_kv + g) * a.BS + (slot & (a.BS - 1));
+      const __nv_bfloat16* src = is_v ? a.v_new + r * a.v_stride : a.k_new + r * a.k_stride;
+      x[u] = __ldg(reinterpret_cast<const uint4*>(src) + at);
+      dst[u] = reinterpret_cast<uint4*>((is_v ? a.v_cache : a.k_cache) + row * a.D) + ch;
+    }
+#pragma unroll
+    for (int u = 0; u < kSlotUnroll; ++u)
+      if (dst[u] != nullptr) *dst[u] = x[u];
+  }
+}
+
 int grid_for(long long work_items, int per_block, int sms) {
   const long long want = (work_items + per_block - 1) / per_block;
   return (int)(want < (long long)sms * 8 ? want : (long long)sms * 8);
@@ -161,6 +205,13 @@ cudaError_t launch_append_fp8(const AppendParams& a, int sms, cudaStream_t strea
     paged_kv_append_fp8_kernel<8><<<grid, 256, 0, stream>>>(a);
   else
     return cudaErrorInvalidValue;
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append_slots(const AppendSlotsParams& a, int sms, cudaStream_t stream) {
+  const long long chunks = (long long)a.rows * 2 * a.H_kv * (a.D / 8);
+  if (chunks == 0) return cudaSuccess;
+  paged_kv_append_slots_kernel<<<grid_for(chunks, 256, sms), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

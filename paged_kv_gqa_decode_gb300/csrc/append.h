@@ -28,4 +28,19 @@ cudaError_t launch_append(const AppendParams& a, int sms, cudaStream_t stream);
 // FP8 caches: each new row is quantized to e4m3 with its own dequant float.
 cudaError_t launch_append_fp8(const AppendParams& a, int sms, cudaStream_t stream);
 
+// Rows placed by slot (block * BS + place in the block), from strided new rows.
+struct AppendSlotsParams {
+  const __nv_bfloat16* k_new;   // row r at r * k_stride: [H_kv, D]
+  const __nv_bfloat16* v_new;
+  long long k_stride, v_stride; // elements between rows (multiples of 8)
+  __nv_bfloat16* k_cache;       // [num_blocks, H_kv, BS, D]
+  __nv_bfloat16* v_cache;
+  const int64_t* slot_map;      // [rows]; outside [0, num_blocks * BS): the row is skipped
+  int rows, H_kv, D, BS;
+  long long num_blocks;
+  int32_t* status;              // null, or: bit 0 set for a slot past the pool
+};
+
+cudaError_t launch_append_slots(const AppendSlotsParams& a, int sms, cudaStream_t stream);
+
 }  // namespace pagedattn

@@ -172,6 +172,19 @@ struct DecodeParams {
   // only ones to read q or the new rows, or to write out or the workspace)
   // still wait for it.
   int early;
+  // Score options (MOD instantiations).  A score x becomes cap tanh(x / cap)
+  // (cap_log2 = cap log2(e), cap_in = scale / cap; cap_log2 0: off), then loses
+  // slopes[h] |pos - t| (null: none), pos = seq_len - 1.  A token t is seen when t
+  // < prefix_lens[s] (null: 0) or t >= max(seq_len - window (window 0: none),
+  // doc_starts[s] (null: 0)); pages that hold no seen token are not walked.
+  float cap_log2, cap_in;
+  const float* slopes;         // [H_q]
+  int window;
+  const int32_t* prefix_lens;  // [num_seqs]
+  const int32_t* doc_starts;   // [num_seqs]
+  // MOD: write each row's softmax state [M, L, -, -, o[0..D)] (fp32, M in the log2
+  // domain) here instead of the bf16 output (null: off).
+  float* state;                // [num_seqs * H_q][D + 4]
 #ifdef PAGED_ATTN_WAIT_TEST
   // Test build only: CTA 0 arms the ring slot of its unit `test_skip_unit` but
   // issues no copy into it, so the consumer's bounded wait for that page runs
@@ -343,7 +356,15 @@ __device__ __noinline__ void fp8_patch_row(const uint8_t* rows, uint8_t* st, int
 //
 // MULTI: multi-token decode (DecodeParams::qo_indptr); compiled separately so
 // the single-token decode carries none of its row mapping or causal masking.
-template <int D, int BS, bool G16, int KV = kKvBf16, bool MULTI = false>
+//
+// MOD: single-token decode with capped and biased scores, a window, a prefix
+// and document starts, or with the softmax states as its output
+// (DecodeParams::cap_log2 .. state).  Every query row of a sequence sees the same
+// tokens, [0, prefix) and [lo, len), so the mask is a page skip (the walk goes
+// over the pages of those two intervals only) and, in the few pages an interval
+// ends in, a selection of the scores and a zeroing of the unseen V rows, which
+// may hold anything.  Compiled separately: the plain decode carries none of it.
+template <int D, int BS, bool G16, int KV = kKvBf16, bool MULTI = false, bool MOD = false>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8))
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
@@ -371,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr bool multi = MULTI;
-  const L lay{p.stages, multi ? p.rows : p.G, p.num_seqs, multi ? p.num_seqs + 1 : 0,
+  const L lay{p.stages, multi ? p.rows : p.G, p.num_seqs, multi ? p.num_seqs + 1 : MOD ? 2 * p.num_seqs : 0,
               multi ? p.chunks : 1};
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + lay.bars());
   uint64_t* empty_bar = full_bar + p.stages;
@@ -386,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   int* sm_wprefix = reinterpret_cast<int*>(smem + lay.wprefix());
   int* sm_len = reinterpret_cast<int*>(smem + lay.lens());
   int* sm_qo = reinterpret_cast<int*>(smem + lay.qo());  // multi: qo_indptr[0..N]
+  static_assert(!MOD || (!MULTI && !XP), "score options: single-token bf16 and FP8 decode");
+  int* sm_lo = sm_qo;                  // MOD: first token of the window and document
+  int* sm_pre = sm_qo + p.num_seqs;    // MOD: length of the prefix every query sees
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -407,6 +431,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
                                                              : PAGED_ATTN_PIECE_WEIGHT_FP8)
                  : MULTI && (R > 8 || QC > 1) ? PAGED_ATTN_PIECE_WEIGHT_MULTI
                                               : PAGED_ATTN_PIECE_WEIGHT_BF16;
+  // MOD: pages of sequence s ahead of its skipped ones, and how many are skipped:
+  // the walk's page w is the sequence's page w, or w + skip from `head` on.
+  auto skip_of = [&](int s, int& head) -> int {
+    const int n_all = (sm_len[s] + BS - 1) / BS;
+    const int first = sm_lo[s] >= sm_len[s] ? n_all : sm_lo[s] / BS;
+    head = (sm_pre[s] + BS - 1) / BS;
+    return max(0, first - head);
+  };
+  // Pages the walk takes for sequence s.
+  auto walk_pages = [&](int s) -> int {
+    int n = (sm_len[s] + BS - 1) / BS;
+    if constexpr (MOD) {
+      int head;
+      n -= skip_of(s, head);
+    }
+    return n;
+  };
+  // The sequence's page that the walk's page w is.
+  auto page_of = [&](int s, int w) -> int {
+    if constexpr (MOD) {
+      int head;
+      const int skip = skip_of(s, head);
+      return w < head ? w : w + skip;
+    }
+    return w;
+  };
   // Status bits are written only after the work ahead in the stream has
   // completed: with the early prologue the producer runs before that point,
   // and a caller that zero-fills the status word in that work must not erase
@@ -456,7 +506,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
         len = min(max(len, 0), cap);
       }
       sm_len[s] = len;
-      const int pages = (len + BS - 1) / BS;
+      if constexpr (MOD) {
+        int lo = p.window > 0 ? len - p.window : 0;
+        if (p.doc_starts != nullptr) lo = max(lo, __ldg(p.doc_starts + s));
+        sm_lo[s] = min(max(lo, 0), len);
+        sm_pre[s] = p.prefix_lens != nullptr ? min(max(__ldg(p.prefix_lens + s), 0), len) : 0;
+      }
+      const int pages = walk_pages(s);
       local += pages;
       wlocal += pages + (pages > 0 ? kWgt : 0);
     }
@@ -485,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     for (int s = s0; s < s1; ++s) {
       sm_prefix[s] = run;
       sm_wprefix[s] = wrun;
-      const int pages = (sm_len[s] + BS - 1) / BS;
+      const int pages = walk_pages(s);
       run += pages;
       wrun += pages + (pages > 0 ? kWgt : 0);
     }
@@ -525,7 +581,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   // threads t0, t0 + nt, ... of it
   auto zero_empty = [&](long long ctas, int t0, int nt) {
     for (long long s = blockIdx.x; s < N; s += ctas) {
-      if (sm_len[s] != 0) continue;
+      if (MOD ? sm_prefix[s + 1] != sm_prefix[s] : sm_len[s] != 0) continue;
+      if constexpr (MOD) {
+        if (p.state != nullptr) {  // an empty state: M = -inf, L = 0 (its o is never read)
+          for (int h = t0; h < p.H_q; h += nt)
+            *reinterpret_cast<float2*>(p.state + ((size_t)s * p.H_q + h) * kPartialRow) =
+                make_float2(-INFINITY, 0.f);
+          continue;
+        }
+      }
       const int r0 = multi ? min(max(sm_qo[s], 0), p.total_q) : (int)s;
       const int nr = multi ? max(0, min(min(sm_qo[s + 1] - sm_qo[s], R * QC / G), p.total_q - r0))
                            : 1;
@@ -590,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       // physical block and KV head of this lane's unit (block -1 past the range)
       if (u >= u1) return make_int2(-1, 0);
       const int sq = multi && QC > 1 ? wk.s % N : wk.s;  // the walked sequence's sequence
-      int pb = __ldg(p.block_tables + (size_t)sq * p.maxb + wk.p);
+      int pb = __ldg(p.block_tables + (size_t)sq * p.maxb + page_of(sq, wk.p));
       if (p.num_blocks > 0 && (pb < 0 || (long long)pb >= p.num_blocks))
         report(kStatusBadBlock);  // the TMA bounds check reads it as zeros
       return make_int2(pb, wk.g);
@@ -760,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
                           : static_cast<const void*>(p.q),
                   qr >= 0 ? 16 : 0);
     }
-    if (!multi && !XP && (!FP8 || kFp8FusedAppend) && p.k_new != nullptr) {
+    if (!multi && !XP && !MOD && (!FP8 || kFp8FusedAppend) && p.k_new != nullptr) {
       const size_t row = ((size_t)s * H_kv + g) * D;
       for (int i = ctid; i < D / 4; i += kConsumerThreads) {  // K then V, 16 bytes each
         const bool is_v = i >= D / 8;
@@ -819,6 +883,53 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
         m_run[nh][e] = -INFINITY;
         l_run[nh][e] = 0.f;
       }
+  };
+
+  // MOD: the piece's interval ends and the slopes of this lane's query columns
+  // (log2 domain).
+  int mod_lo = 0, mod_pre = 0, mod_pos = 0;
+  float mod_slope[kNH][2] = {};
+  auto set_mods = [&](int s, int gv) {
+    if constexpr (MOD) {
+      mod_lo = sm_lo[s];
+      mod_pre = sm_pre[s];
+      mod_pos = sm_len[s] - 1;
+#pragma unroll
+      for (int nh = 0; nh < kNH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * nh + 2 * quad + e;
+          mod_slope[nh][e] = p.slopes != nullptr && h < G
+                                 ? __ldg(p.slopes + (size_t)gv * G + h) * 1.4426950408889634f
+                                 : 0.f;
+        }
+    }
+  };
+  // Token t of the sequence lies in one of the seen intervals (its end aside).
+  auto in_sight = [&](int t) -> bool { return !MOD || t >= mod_lo || t < mod_pre; };
+  // A page of `valid` tokens from tb on that holds an unseen token or row.
+  auto is_ragged = [&](int valid, int tb) -> bool {
+    return valid < BS || (MOD && tb < mod_lo && tb + BS > mod_pre);
+  };
+  // Score of token t (log2 domain) from the dot product, for slope `slope`.  The
+  // cap: the series where every score of the warp is small next to the cap,
+  // which is the ordinary case and costs no MUFU operation.
+  auto mod_score = [&](float dot, float factor, int t, float slope) -> float {
+    float x;
+    if (p.cap_log2 > 0.f) {
+      const float y = dot * (factor * p.cap_in);
+      float th = tanh_series(y);
+      const bool big = !(fabsf(y) < kTanhSeries);
+      if (__any_sync(0xffffffffu, big)) {
+        const float te = tanh_exp(y);
+        th = big ? te : th;
+      }
+      x = p.cap_log2 * th;
+    } else {
+      x = dot * (factor * p.scale_log2);
+    }
+    if (p.slopes != nullptr) x = fmaf(-slope, (float)abs(mod_pos - t), x);
+    return x;
   };
 
   // One page: S^T = K Q^T, online softmax, O^T += V^T P^T.
@@ -891,9 +1002,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = 16 * tg + row + ((e >> 1) << 3);
-          const float x = tok < valid && (!MULTI || tb + tok <= lim[nh][e & 1])
-                              ? s_acc[tg][nh][e] * p.scale_log2
-                              : -INFINITY;
+          float x;
+          if constexpr (MOD) {
+            x = mod_score(s_acc[tg][nh][e], 1.f, tb + tok, mod_slope[nh][e & 1]);
+            if (!(tok < valid && in_sight(tb + tok))) x = -INFINITY;
+          } else {
+            x = tok < valid && (!MULTI || tb + tok <= lim[nh][e & 1])
+                    ? s_acc[tg][nh][e] * p.scale_log2
+                    : -INFINITY;
+          }
           s_acc[tg][nh][e] = x;
           mx[nh][e & 1] = fmaxf(mx[nh][e & 1], x);
         }
@@ -920,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
           const float m_new = fmaxf(m_run[nh][e], v);
           // a column that has seen no token yet (all masked) keeps -inf; subtract 0
           // then, so its weights are exp2(-inf) = 0 instead of NaN
-          m_sub[nh][e] = MULTI && m_new == -INFINITY ? 0.f : m_new;
+          m_sub[nh][e] = (MULTI || MOD) && m_new == -INFINITY ? 0.f : m_new;
           alpha[nh][e] = fast_exp2(m_run[nh][e] - m_sub[nh][e]);
           m_run[nh][e] = m_new;
         }
@@ -929,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m_sub[nh][e] = MULTI && m_run[nh][e] == -INFINITY ? 0.f : m_run[nh][e];
+          m_sub[nh][e] = (MULTI || MOD) && m_run[nh][e] == -INFINITY ? 0.f : m_run[nh][e];
           alpha[nh][e] = 1.f;
         }
     }
@@ -966,14 +1083,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     }
 
     // ---- O^T += V^T P^T: A operand = 16 columns x 16 tokens via transposing ldmatrix
-    const bool tail = valid < BS;
+    const bool tail = is_ragged(valid, tb);
 #pragma unroll
     for (int tg = 0; tg < kTG; ++tg) {
       uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
       if (tail) {  // rows past the sequence may hold anything: zero them in the fragment
         const int t0 = 16 * tg + 2 * quad;
-        mlo = (t0 < valid ? 0x0000ffffu : 0u) | (t0 + 1 < valid ? 0xffff0000u : 0u);
-        mhi = (t0 + 8 < valid ? 0x0000ffffu : 0u) | (t0 + 9 < valid ? 0xffff0000u : 0u);
+        auto keep = [&](int t) { return t < valid && in_sight(tb + t); };
+        mlo = (keep(t0) ? 0x0000ffffu : 0u) | (keep(t0 + 1) ? 0xffff0000u : 0u);
+        mhi = (keep(t0 + 8) ? 0x0000ffffu : 0u) | (keep(t0 + 9) ? 0xffff0000u : 0u);
       }
       const int tok = 16 * tg + (lane & 7) + ((li >> 1) << 3);
 #pragma unroll
@@ -1023,6 +1141,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     uint32_t k, v;        // shared-memory address of the tile's first K / V row
     uint32_t ks, vs;      // shared-memory address of its 16 K / V row floats
     int valid;            // tokens of the tile inside the sequence (0..16)
+    int tb;               // the tile's first token
   };
   auto process_fp8 = [&](auto nt, const Tile8* tl, uint32_t q16) {
     constexpr int NT = decltype(nt)::value;
@@ -1073,15 +1192,23 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
 #pragma unroll
     for (int tg = 0; tg < NT; ++tg) {
       const int valid = tl[tg].valid;
-      const float k_lo = p.scale_log2 * lds_f32(tl[tg].ks + 4 * row);
-      const float k_hi = p.scale_log2 * lds_f32(tl[tg].ks + 4 * (row + 8));
+      // (MOD scales inside mod_score)
+      const float k_lo = (MOD ? 1.f : p.scale_log2) * lds_f32(tl[tg].ks + 4 * row);
+      const float k_hi = (MOD ? 1.f : p.scale_log2) * lds_f32(tl[tg].ks + 4 * (row + 8));
 #pragma unroll
       for (int nh = 0; nh < kNH; ++nh)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tok = row + ((e >> 1) << 3);
           const float sum = s_acc[tg][nh][e] + s_odd[tg][nh][e];
-          const float x = tok < valid ? sum * ((e >> 1) ? k_hi : k_lo) : -INFINITY;
+          float x;
+          if constexpr (MOD) {
+            const int t = tl[tg].tb + tok;
+            x = mod_score(sum, (e >> 1) ? k_hi : k_lo, t, mod_slope[nh][e & 1]);
+            if (!(tok < valid && in_sight(t))) x = -INFINITY;
+          } else {
+            x = tok < valid ? sum * ((e >> 1) ? k_hi : k_lo) : -INFINITY;
+          }
           s_acc[tg][nh][e] = x;
           mx[nh][e & 1] = fmaxf(mx[nh][e & 1], x);
         }
@@ -1103,7 +1230,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
           v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
           const float m_new = fmaxf(m_run[nh][e], v);
-          alpha[nh][e] = fast_exp2(m_run[nh][e] - m_new);
+          // (MOD: a tile whose tokens are all unseen leaves the max at -inf)
+          alpha[nh][e] = MOD && m_new == -INFINITY ? 1.f : fast_exp2(m_run[nh][e] - m_new);
           m_run[nh][e] = m_new;
         }
     } else {
@@ -1120,14 +1248,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     for (int tg = 0; tg < NT; ++tg) {
       const int valid = tl[tg].valid;
       // masked rows may hold NaN floats
-      const float v_lo = row < valid ? lds_f32(tl[tg].vs + 4 * row) : 0.f;
-      const float v_hi = row + 8 < valid ? lds_f32(tl[tg].vs + 4 * (row + 8)) : 0.f;
+      const bool see_lo = row < valid && in_sight(tl[tg].tb + row);
+      const bool see_hi = row + 8 < valid && in_sight(tl[tg].tb + row + 8);
+      const float v_lo = see_lo ? lds_f32(tl[tg].vs + 4 * row) : 0.f;
+      const float v_hi = see_hi ? lds_f32(tl[tg].vs + 4 * (row + 8)) : 0.f;
 #pragma unroll
       for (int nh = 0; nh < kNH; ++nh) {
-        const float e0 = fast_exp2(s_acc[tg][nh][0] - m_run[nh][0]);
-        const float e1 = fast_exp2(s_acc[tg][nh][1] - m_run[nh][1]);
-        const float e2 = fast_exp2(s_acc[tg][nh][2] - m_run[nh][0]);
-        const float e3 = fast_exp2(s_acc[tg][nh][3] - m_run[nh][1]);
+        const float m0 = MOD && m_run[nh][0] == -INFINITY ? 0.f : m_run[nh][0];
+        const float m1 = MOD && m_run[nh][1] == -INFINITY ? 0.f : m_run[nh][1];
+        const float e0 = fast_exp2(s_acc[tg][nh][0] - m0);
+        const float e1 = fast_exp2(s_acc[tg][nh][1] - m1);
+        const float e2 = fast_exp2(s_acc[tg][nh][2] - m0);
+        const float e3 = fast_exp2(s_acc[tg][nh][3] - m1);
         psum[nh][0] += e0 + e2;
         psum[nh][1] += e1 + e3;
         pb0[tg][nh] = movmatrix_trans(pack_f16x2(e0 * v_lo, e1 * v_lo));
@@ -1243,7 +1375,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       m_acc[k] = m_new;
     }
   };
-  auto store_rows = [&](const Split& x, const float4 (&acc)[kSlots], const float (&l_acc)[kSlots]) {
+  auto store_rows = [&](const Split& x, const float4 (&acc)[kSlots], const float (&m_acc)[kSlots],
+                        const float (&l_acc)[kSlots]) {
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) {
       const int v = ctid + k * kConsumerThreads;
@@ -1251,6 +1384,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       const int r = v / (D / 4), d4 = v - r * (D / 4);
       const long long qr = qrow(x.s, x.g, r);
       if (qr < 0) continue;
+      if constexpr (MOD) {
+        if (p.state != nullptr) {
+          float* st = p.state + (size_t)qr * kPartialRow;
+          *reinterpret_cast<float4*>(st + 4 + 4 * d4) = acc[k];
+          if (d4 == 0) *reinterpret_cast<float2*>(st) = make_float2(m_acc[k], l_acc[k]);
+          continue;
+        }
+      }
       const float inv = l_acc[k] > 0.f ? 1.f / l_acc[k] : 0.f;  // a row that saw no token: 0
       uint2 packed;
       packed.x = pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
@@ -1311,7 +1452,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
              l_acc);
         t += cnt;
         if (t == job_end) {
-          store_rows(t == n0 ? x0 : x1, acc, l_acc);
+          store_rows(t == n0 ? x0 : x1, acc, m_acc, l_acc);
           reset_acc();
         }
       }
@@ -1392,6 +1533,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       if (dst == nullptr) {
         const long long qr = qrow(s, g, r);
         if (qr < 0) continue;
+        if constexpr (MOD) {
+          if (p.state != nullptr) {
+            float* st = p.state + (size_t)qr * kPartialRow;
+            *reinterpret_cast<float4*>(st + 4 + d) = acc;
+            if (d == 0) *reinterpret_cast<float2*>(st) = make_float2(M, lsum);
+            continue;
+          }
+        }
         const float inv = lsum > 0.f ? 1.f / lsum : 0.f;  // a row that saw no token: 0
         uint2 packed;
         packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
@@ -1475,6 +1624,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   }
   reset();
   set_limits(wk.s, wk.g);
+  set_mods(wk.s, wk.g);
   // Ring ownership: unit i of the range (i = u - u0) sits in slot i % stages,
   // and slot r belongs to consumer warp r % 4, so each warp waits on its
   // slots' phases strictly in order (a parity wait cannot tell phase k from
@@ -1503,7 +1653,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     const int len = sm_len[sq];  // read once per piece (the page waits below clobber memory)
     const long long ib = min(n_units, ia + (n - p0));  // one past its last unit here
     while (own_i < ib) {
-      const int pg = p0 + (int)(own_i - ia);  // page of the sequence
+      const int pg = page_of(sq, p0 + (int)(own_i - ia));  // page of the sequence
       if constexpr (FP8) {
         if (!abort) {
           const bool ready = __all_sync(0xffffffffu, mbar_wait(&full_bar[own_slot], own_phase));
@@ -1515,11 +1665,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
             uint8_t* st = smem + own_slot * kStageBytes;
             // Only the piece's last page can end early: zero its V rows past
             // the sequence (they may hold anything) so the V operand needs no mask.
-            const bool tail = valid < BS;
+            // (MOD: its unseen rows, which the page an interval begins or ends in has)
+            const bool tail = is_ragged(valid, pg * BS);
             if (tail) {
-              const int chunks = (BS - valid) * L::kHalves * 8;  // 16-byte chunks
+              const int z0 = MOD ? 0 : valid;
+              const int chunks = (BS - z0) * L::kHalves * 8;  // 16-byte chunks
               for (int c = lane; c < chunks; c += 32) {
-                const int r = valid + c / (L::kHalves * 8);
+                const int r = z0 + c / (L::kHalves * 8);
+                if (MOD && r < valid && in_sight(pg * BS + r)) continue;
                 const int h = (c / 8) % L::kHalves;
                 *reinterpret_cast<uint4*>(st + kPageBytes + h * kTileBytes + r * 128 +
                                           (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -1534,7 +1687,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
             // memory, and stored to the cache after the page is processed.
             // (head_dim 128 only: at 256 the code would cost the page loop a spill,
             // and the library runs the append as its own launch instead)
-            const bool patch = kFp8FusedAppend && !multi && p.k_new != nullptr && pg == n - 1;
+            const bool patch =
+                kFp8FusedAppend && !multi && !MOD && p.k_new != nullptr && pg == n - 1;
             constexpr int kE = D / 32;  // values of a row per lane
             const uint8_t* extra = sm_q + qbuf * kQSlotBytes + kAppendOff;  // k row, v row, block
             // byte lane * kE of row `slot`: 16-byte chunk c (128-byte half c / 8,
@@ -1554,12 +1708,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
             const uint32_t q16 = smem_addr(sm_q + qbuf * kQSlotBytes + kQTileBytes);
             const uint32_t k0 = smem_addr(st), v0 = smem_addr(st + kPageBytes);
             if constexpr (BS == 16) {
-              const Tile8 t[1] = {{k0, v0, sc, sc + 4 * BS, valid}};
+              const Tile8 t[1] = {{k0, v0, sc, sc + 4 * BS, valid, pg * BS}};
               process_fp8(std::integral_constant<int, 1>(), t, q16);
             } else {  // the two 16-token halves of a 32-token page
-              const Tile8 t[2] = {{k0, v0, sc, sc + 4 * BS, min(16, valid)},
+              const Tile8 t[2] = {{k0, v0, sc, sc + 4 * BS, min(16, valid), pg * BS},
                                   {k0 + 16 * 128, v0 + 16 * 128, sc + 4 * 16, sc + 4 * (BS + 16),
-                                   max(0, valid - 16)}};
+                                   max(0, valid - 16), pg * BS + 16}};
               process_fp8(std::integral_constant<int, 2>(), t, q16);
             }
             // the zeroing's and the patch's generic writes precede the next tensor
@@ -1601,7 +1755,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
           // patched into the page in shared memory once the page has landed
           // (the tensor copy brought whatever the cache held) and stored to the
           // cache for later calls.  This page is read by this CTA alone.
-          const bool patch = !XP && !multi && p.k_new != nullptr && pg == n - 1;
+          const bool patch = !XP && !multi && !MOD && p.k_new != nullptr && pg == n - 1;
           // Lanes poll the barrier independently; the vote both reconverges
           // the warp before the warp-collective ldmatrix / movmatrix / mma and
           // makes the outcome uniform.
@@ -1675,6 +1829,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       qbuf = qnext;
       reset();
       set_limits(wk.s, wk.g);
+      set_mods(wk.s, wk.g);
       continue;
     }
     // ---- the range's last piece.  When it is split, thread 0 arrives as soon

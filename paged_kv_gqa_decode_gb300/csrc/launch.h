@@ -51,17 +51,34 @@ cudaError_t launch_decode_fp8_d256(int block_size, bool g16, const CUtensorMap& 
                                    const CUtensorMap& tv, const DecodeParams& p, int grid,
                                    size_t smem, cudaStream_t stream);
 
+// Decode with score options (bf16 caches; FP8 caches with head_dim 128 or 256).
+cudaError_t launch_decode_mod_d64(int block_size, bool g16, const CUtensorMap& tk,
+                                  const CUtensorMap& tv, const DecodeParams& p, int grid,
+                                  size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_mod_d128(int block_size, bool g16, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const DecodeParams& p, int grid,
+                                   size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_mod_d256(int block_size, bool g16, const CUtensorMap& tk,
+                                   const CUtensorMap& tv, const DecodeParams& p, int grid,
+                                   size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_fp8_mod_d128(int block_size, bool g16, const CUtensorMap& tk,
+                                       const CUtensorMap& tv, const DecodeParams& p, int grid,
+                                       size_t smem, cudaStream_t stream);
+cudaError_t launch_decode_fp8_mod_d256(int block_size, bool g16, const CUtensorMap& tk,
+                                       const CUtensorMap& tv, const DecodeParams& p, int grid,
+                                       size_t smem, cudaStream_t stream);
+
 // Launches one instantiation, first raising its dynamic shared-memory limit on
 // the current device when this launch needs more than was set before (the
 // record is per instantiation and per device).
-template <int D, int BS, bool G16, int KV, bool MULTI = false>
+template <int D, int BS, bool G16, int KV, bool MULTI = false, bool MOD = false>
 cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
                        int grid, size_t smem, cudaStream_t stream) {
   // The first launch of this instantiation on a device raises its dynamic
   // shared-memory limit to all the device allows next to its static shared
   // memory; host threads may race here, and every racer sets the same value.
   static std::atomic<bool> limit_raised[64];
-  auto kernel = paged_decode_kernel<D, BS, G16, KV, MULTI>;
+  auto kernel = paged_decode_kernel<D, BS, G16, KV, MULTI, MOD>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -93,14 +110,14 @@ cudaError_t launch_one(const CUtensorMap& tk, const CUtensorMap& tv, const Decod
   return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
 }
 
-template <int D, int KV = kKvBf16, bool MULTI = false>
+template <int D, int KV = kKvBf16, bool MULTI = false, bool MOD = false>
 cudaError_t launch_for_dim(int block_size, bool g16, const CUtensorMap& tk, const CUtensorMap& tv,
                            const DecodeParams& p, int grid, size_t smem, cudaStream_t stream) {
   if (block_size == 16)
-    return g16 ? launch_one<D, 16, true, KV, MULTI>(tk, tv, p, grid, smem, stream)
-               : launch_one<D, 16, false, KV, MULTI>(tk, tv, p, grid, smem, stream);
-  return g16 ? launch_one<D, 32, true, KV, MULTI>(tk, tv, p, grid, smem, stream)
-             : launch_one<D, 32, false, KV, MULTI>(tk, tv, p, grid, smem, stream);
+    return g16 ? launch_one<D, 16, true, KV, MULTI, MOD>(tk, tv, p, grid, smem, stream)
+               : launch_one<D, 16, false, KV, MULTI, MOD>(tk, tv, p, grid, smem, stream);
+  return g16 ? launch_one<D, 32, true, KV, MULTI, MOD>(tk, tv, p, grid, smem, stream)
+             : launch_one<D, 32, false, KV, MULTI, MOD>(tk, tv, p, grid, smem, stream);
 }
 
 }  // namespace pagedattn

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "append.h"
+#include "assign.h"
 #include "launch.h"
 #include "paged_attn.h"
 
@@ -118,6 +119,7 @@ struct Plan {
   bool g16;
   bool fp8;     // FP8 caches
   bool xp;      // x-packed K / D-major V caches (bf16)
+  bool mod;     // score options (or a state output)
   int rows;     // query rows of one piece: G, or a multi-token chunk (8 or 16)
   int qchunks;  // multi-token decode: pieces per (sequence, KV head); 0: single token
   int chunk;    // sequences per launch
@@ -129,11 +131,12 @@ struct Plan {
 
 // G: query rows of one piece; qchunks > 0: multi-token decode (room for chunk + 1
 // row offsets and the page prefixes of qchunks passes).
+// qchunks < 0: decode with score options (room for two values per sequence).
 template <int D, int BS, bool FP8>
 bool plan_smem(int G, int chunk, int max_smem, long long ring_cap, int qchunks, int* stages,
                size_t* smem) {
   using L = SmemLayout<D, BS, FP8>;
-  const int qo_entries = qchunks > 0 ? chunk + 1 : 0;
+  const int qo_entries = qchunks > 0 ? chunk + 1 : qchunks < 0 ? 2 * chunk : 0;
   const int walks = qchunks > 0 ? qchunks : 1;
   const L none{0, G, chunk, qo_entries, walks};
   const long long fixed = none.total() + 2048;  // + alignment slack and static shared memory
@@ -172,12 +175,13 @@ bool plan_smem_any(int D, int BS, bool fp8, int G, int chunk, int max_smem, long
 }
 
 // rows > 0: multi-token decode with `rows` query rows per piece and `qchunks`
-// pieces per (sequence, KV head).
+// pieces per (sequence, KV head).  mod: decode with score options.
 int make_plan(int num_seqs, int H_q, int H_kv, int D, int BS, const DeviceInfo& di, Plan* pl,
-              bool fp8 = false, int rows = 0, int qchunks = 0) {
+              bool fp8 = false, int rows = 0, int qchunks = 0, bool mod = false) {
   pl->D = D;
   pl->fp8 = fp8;
   pl->xp = false;
+  pl->mod = mod;
   pl->BS = BS;
   pl->G = H_q / H_kv;
   pl->rows = rows > 0 ? rows : pl->G;
@@ -208,7 +212,7 @@ int make_plan(int num_seqs, int H_q, int H_kv, int D, int BS, const DeviceInfo& 
            : pieces >= 2LL * di.sms * occ ? kRingBytesPerSmManyPieces
                                           : kRingBytesPerSm) /
           occ;
-      if (plan_smem_any(D, BS, fp8, pl->rows, chunk, budget, ring_cap, pl->qchunks,
+      if (plan_smem_any(D, BS, fp8, pl->rows, chunk, budget, ring_cap, mod ? -1 : pl->qchunks,
                         &pl->stages, &pl->smem) &&
           (pl->stages >= 4 || chunk <= 64)) {
         ok = true;
@@ -237,7 +241,7 @@ int make_plan(int num_seqs, int H_q, int H_kv, int D, int BS, const DeviceInfo& 
 // make_plan through a small per-thread cache: the plan depends only on the
 // sizes, the variant and the device, so a decode loop plans once.
 int cached_plan(int num_seqs, int H_q, int H_kv, int D, int BS, int dev, const DeviceInfo& di,
-                Plan* pl, bool fp8 = false, int rows = 0, int qchunks = 0) {
+                Plan* pl, bool fp8 = false, int rows = 0, int qchunks = 0, bool mod = false) {
   struct Entry {
     int key[9];
     Plan plan;
@@ -245,7 +249,8 @@ int cached_plan(int num_seqs, int H_q, int H_kv, int D, int BS, int dev, const D
   };
   constexpr int kEntries = 16;
   thread_local Entry tl_plans[kEntries] = {};
-  const int key[9] = {num_seqs, H_q, H_kv, D, BS, fp8 ? 1 : 0, rows, qchunks, dev};
+  const int key[9] = {num_seqs, H_q, H_kv, D, BS, (fp8 ? 1 : 0) + (mod ? 2 : 0), rows,
+                      qchunks, dev};
   uint32_t h = 2166136261u;
   for (int k : key) h = (h ^ (uint32_t)k) * 16777619u;
   Entry& e = tl_plans[h % kEntries];
@@ -253,7 +258,7 @@ int cached_plan(int num_seqs, int H_q, int H_kv, int D, int BS, int dev, const D
     *pl = e.plan;
     return PAGED_ATTN_OK;
   }
-  int rc = make_plan(num_seqs, H_q, H_kv, D, BS, di, pl, fp8, rows, qchunks);
+  int rc = make_plan(num_seqs, H_q, H_kv, D, BS, di, pl, fp8, rows, qchunks, mod);
   if (rc != PAGED_ATTN_OK) return rc;
   std::memcpy(e.key, key, sizeof key);
   e.plan = *pl;
@@ -349,14 +354,22 @@ int encode_xpacked_maps(const void* v, int D, int BS, int H_kv, long long num_bl
   return PAGED_ATTN_OK;
 }
 
-cudaError_t launch_dim(int D, int BS, bool g16, bool fp8, bool xp, const CUtensorMap& tk,
-                       const CUtensorMap& tv, const DecodeParams& p, int grid, size_t smem,
-                       cudaStream_t st) {
+cudaError_t launch_dim(int D, int BS, bool g16, bool fp8, bool xp, bool mod,
+                       const CUtensorMap& tk, const CUtensorMap& tv, const DecodeParams& p,
+                       int grid, size_t smem, cudaStream_t st) {
 #ifdef PAGED_ATTN_WAIT_TEST
   // the test build carries the single-token bf16 head_dim-128 kernels only
-  if (p.qo_indptr != nullptr || xp || fp8 || D != 128) return cudaErrorNotSupported;
+  if (p.qo_indptr != nullptr || xp || fp8 || mod || D != 128) return cudaErrorNotSupported;
   return launch_decode_d128(BS, g16, tk, tv, p, grid, smem, st);
-#endif
+#else
+  if (mod && fp8)
+    return D == 128 ? launch_decode_fp8_mod_d128(BS, g16, tk, tv, p, grid, smem, st)
+                    : launch_decode_fp8_mod_d256(BS, g16, tk, tv, p, grid, smem, st);
+  if (mod) {
+    if (D == 64) return launch_decode_mod_d64(BS, g16, tk, tv, p, grid, smem, st);
+    if (D == 128) return launch_decode_mod_d128(BS, g16, tk, tv, p, grid, smem, st);
+    return launch_decode_mod_d256(BS, g16, tk, tv, p, grid, smem, st);
+  }
   if (p.qo_indptr != nullptr) {
     if (D == 64) return launch_decode_multi_d64(BS, g16, tk, tv, p, grid, smem, st);
     if (D == 128) return launch_decode_multi_d128(BS, g16, tk, tv, p, grid, smem, st);
@@ -373,6 +386,7 @@ cudaError_t launch_dim(int D, int BS, bool g16, bool fp8, bool xp, const CUtenso
   if (D == 64) return launch_decode_d64(BS, g16, tk, tv, p, grid, smem, st);
   if (D == 128) return launch_decode_d128(BS, g16, tk, tv, p, grid, smem, st);
   return launch_decode_d256(BS, g16, tk, tv, p, grid, smem, st);
+#endif
 }
 
 int check_pointers(const void* q, const void* k, const void* v, const void* out,
@@ -451,6 +465,13 @@ struct Operands {
   const int32_t* qo_indptr = nullptr;  // multi-token decode
   int total_q = 0;
   int causal = 1;
+  // score options
+  float softcap = 0.f;
+  const float* slopes = nullptr;
+  int window = 0;
+  const int32_t* prefix_lens = nullptr;
+  const int32_t* doc_starts = nullptr;
+  float* state = nullptr;  // softmax states [num_seqs * H_q][D + 4] instead of the output
 };
 
 // The calling thread's device-side checks (paged_attn_set_checks), if any.
@@ -508,6 +529,13 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
     p.partials = reinterpret_cast<float*>(wsb + pl.off_partials);
     p.num_blocks = o.num_blocks;
     p.early = o.early ? 1 : 0;
+    p.cap_log2 = o.softcap * 1.4426950408889634f;
+    p.cap_in = o.softcap > 0.f ? o.scale / o.softcap : 0.f;
+    p.slopes = o.slopes;
+    p.window = o.window;
+    p.prefix_lens = o.prefix_lens ? o.prefix_lens + s0 : nullptr;
+    p.doc_starts = o.doc_starts ? o.doc_starts + s0 : nullptr;
+    p.state = o.state ? o.state + (size_t)s0 * o.H_q * (pl.D + 4) : nullptr;
     p.k_new = o.k_new ? static_cast<const __nv_bfloat16*>(o.k_new) + (size_t)s0 * o.H_kv * pl.D
                       : nullptr;
     p.v_new = o.v_new ? static_cast<const __nv_bfloat16*>(o.v_new) + (size_t)s0 * o.H_kv * pl.D
@@ -521,7 +549,8 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
     p.test_skip_publish = g_test_skip_publish;
 #endif
     cudaError_t e =
-        launch_dim(pl.D, pl.BS, pl.g16, pl.fp8, pl.xp, tk, tv, p, pl.grid, pl.smem, stream);
+        launch_dim(pl.D, pl.BS, pl.g16, pl.fp8, pl.xp, pl.mod, tk, tv, p, pl.grid, pl.smem,
+                   stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return PAGED_ATTN_OK;
@@ -553,6 +582,49 @@ int owned_workspace(size_t bytes, cudaStream_t stream, void** out) {
     }
     w.ptr = p;
     w.bytes = bytes;
+  }
+  *out = w.ptr;
+  return PAGED_ATTN_OK;
+}
+
+// The workspace of a call that takes an optional one: the caller's, or the
+// library's own for these entry points (kept apart from owned_workspace, whose
+// buffer captured graphs of the other entry points may hold).  A stream being
+// captured must bring its own: a graph must not keep a buffer that a later,
+// larger call releases.
+OwnedWorkspace g_opt_ws[kMaxDevices];  // guarded by g_mu
+
+int optional_workspace(void* workspace, size_t workspace_bytes, size_t need, cudaStream_t stream,
+                       void** out) {
+  if (workspace != nullptr) {
+    if ((reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0 || workspace_bytes < need)
+      return PAGED_ATTN_ERR_WORKSPACE;
+    *out = workspace;
+    return PAGED_ATTN_OK;
+  }
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (cap != cudaStreamCaptureStatusNone) return PAGED_ATTN_ERR_WORKSPACE;
+  int dev = 0;
+  int rc = current_device(&dev);
+  if (rc != PAGED_ATTN_OK) return rc;
+  std::lock_guard<std::mutex> lk(g_mu);
+  OwnedWorkspace& w = g_opt_ws[dev];
+  if (w.bytes < need) {
+    if (w.ptr) {
+      if ((e = cudaFreeAsync(w.ptr, stream)) != cudaSuccess) return cuda_fail(e);
+      w.ptr = nullptr;
+      w.bytes = 0;
+    }
+    void* p = nullptr;
+    if ((e = cudaMallocAsync(&p, need, stream)) != cudaSuccess) return cuda_fail(e);
+    if ((e = cudaMemsetAsync(p, 0, need, stream)) != cudaSuccess) {
+      cudaFreeAsync(p, stream);
+      return cuda_fail(e);
+    }
+    w.ptr = p;
+    w.bytes = need;
   }
   *out = w.ptr;
   return PAGED_ATTN_OK;
@@ -627,6 +699,34 @@ int plan_and_run(Operands& o, int head_dim, int block_size, bool fp8, bool xp, i
   pl.xp = xp;  // same shared-memory plan as the bf16 layout
   if (o.ws == nullptr && (rc = owned_workspace(pl.ws_bytes, st, &o.ws)) != PAGED_ATTN_OK)
     return rc;
+  return run(pl, o, st);
+}
+
+// Score options as the entry points take them (arrays 4-byte aligned or null).
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+int mods_checks(float softcap, const float* slopes, int window, const int32_t* prefix_lens,
+                const int32_t* doc_starts) {
+  if (!std::isfinite(softcap) || softcap < 0.f) return PAGED_ATTN_ERR_MODS;
+  if (window < 0) return PAGED_ATTN_ERR_MODS;
+  if (!aligned4(slopes) || !aligned4(prefix_lens) || !aligned4(doc_starts))
+    return PAGED_ATTN_ERR_POINTER;
+  return PAGED_ATTN_OK;
+}
+
+// A decode call with score options, its arguments checked.
+int decode_mods_impl(Operands& o, int head_dim, int block_size, bool fp8, void* workspace,
+                     size_t workspace_bytes, cudaStream_t st) {
+  apply_checks(&o);
+  int dev = 0;
+  DeviceInfo di;
+  int rc = device_info(&di, &dev);
+  if (rc != PAGED_ATTN_OK) return rc;
+  Plan pl;
+  rc = cached_plan(o.num_seqs, o.H_q, o.H_kv, head_dim, block_size, dev, di, &pl, fp8, 0, 0, true);
+  if (rc != PAGED_ATTN_OK) return rc;
+  rc = optional_workspace(workspace, workspace_bytes, pl.ws_bytes, st, &o.ws);
+  if (rc != PAGED_ATTN_OK) return rc;
   return run(pl, o, st);
 }
 
@@ -973,6 +1073,144 @@ int paged_attn_append_decode_fp8(const void* q, const void* k_new, const void* v
   return run(pl, o, st);
 }
 
+int paged_attn_decode_mods(const void* q, const void* k_cache, const void* v_cache, void* out,
+                           const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                           int H_q, int H_kv, int head_dim, int max_blocks_per_seq,
+                           int block_size, float scale, float softcap,
+                           const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                           const int32_t* doc_starts, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  int rc = common_checks(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
+                         head_dim, max_blocks_per_seq, block_size, scale);
+  if (rc == PAGED_ATTN_OK) rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
+  Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
+                        max_blocks_per_seq, scale);
+  o.softcap = softcap;
+  o.slopes = alibi_slopes;
+  o.window = window;
+  o.prefix_lens = prefix_lens;
+  o.doc_starts = doc_starts;
+  return decode_mods_impl(o, head_dim, block_size, false, workspace, workspace_bytes,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int paged_attn_decode_fp8_mods(const void* q, const void* k_cache, const void* v_cache,
+                               const float* k_scale, const float* v_scale, void* out,
+                               const int32_t* block_tables, const int32_t* seq_lens,
+                               int num_seqs, int H_q, int H_kv, int head_dim,
+                               int max_blocks_per_seq, int block_size, float scale, float softcap,
+                               const float* alibi_slopes, int window, const int32_t* prefix_lens,
+                               const int32_t* doc_starts, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  int rc = fp8_checks(q, k_cache, v_cache, k_scale, v_scale, out, block_tables, seq_lens,
+                      num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size, scale);
+  if (rc == PAGED_ATTN_OK) rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
+  Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
+                        max_blocks_per_seq, scale);
+  o.k_scale = k_scale;
+  o.v_scale = v_scale;
+  o.softcap = softcap;
+  o.slopes = alibi_slopes;
+  o.window = window;
+  o.prefix_lens = prefix_lens;
+  o.doc_starts = doc_starts;
+  return decode_mods_impl(o, head_dim, block_size, true, workspace, workspace_bytes,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t paged_attn_mods_workspace_bytes(int num_seqs, int H_q, int H_kv, int head_dim,
+                                       int max_blocks_per_seq, int block_size) {
+  if (validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size) !=
+      PAGED_ATTN_OK)
+    return 0;
+  int dev = 0;
+  DeviceInfo di;
+  if (device_info(&di, &dev) != PAGED_ATTN_OK) return 0;
+  size_t bytes = 0;
+  for (int fp8 = 0; fp8 <= (head_dim == 64 ? 0 : 1); ++fp8) {
+    Plan pl;
+    if (cached_plan(num_seqs, H_q, H_kv, head_dim, block_size, dev, di, &pl, fp8 != 0, 0, 0,
+                    true) != PAGED_ATTN_OK)
+      return 0;
+    if (pl.ws_bytes > bytes) bytes = pl.ws_bytes;
+  }
+  return bytes;
+}
+
+int paged_kv_assign(const int32_t* seq_lens, const int32_t* new_lens, int32_t* block_tables,
+                    const int32_t* free_blocks, const int32_t* free_count, int32_t* seq_lens_out,
+                    int32_t* qo_indptr, int64_t* slot_map, int32_t* free_count_out,
+                    int32_t* refused, int num_seqs, int max_blocks_per_seq, int block_size,
+                    int free_capacity, int max_new, void* stream) {
+  int rc = validate_sizes(num_seqs, 1, 1, 64, max_blocks_per_seq, block_size);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (free_capacity < 0 || max_new < 0) return PAGED_ATTN_ERR_SIZES;
+  if (num_seqs == 0) return PAGED_ATTN_OK;
+  // what a launch without new rows or free blocks never touches may be null
+  if (!aligned16(seq_lens) || !aligned16(new_lens) || !aligned16(block_tables) ||
+      !aligned16(seq_lens_out) || !aligned16(qo_indptr) || free_count == nullptr ||
+      !aligned4(free_count) || free_count_out == nullptr || !aligned4(free_count_out) ||
+      !aligned4(refused) || (max_new > 0 && !aligned16(slot_map)) ||
+      (free_capacity > 0 && !aligned16(free_blocks)))
+    return PAGED_ATTN_ERR_POINTER;
+  AssignParams a;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.block_tables = block_tables;
+  a.free_blocks = free_blocks;
+  a.free_count = free_count;
+  a.seq_lens_out = seq_lens_out;
+  a.qo_indptr = qo_indptr;
+  a.slot_map = slot_map;
+  a.free_count_out = free_count_out;
+  a.refused = refused;
+  a.num_seqs = num_seqs;
+  a.maxb = max_blocks_per_seq;
+  a.BS = block_size;
+  a.free_capacity = free_capacity;
+  a.max_new = max_new;
+  a.num_blocks = g_check_blocks;
+  a.status = g_check_blocks > 0 ? g_check_status : nullptr;
+  cudaError_t e = launch_assign(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+}
+
+int paged_kv_append_slots(const void* k_new, const void* v_new, long long k_stride,
+                          long long v_stride, void* k_cache, void* v_cache,
+                          const int64_t* slot_map, int rows, int H_kv, int head_dim,
+                          int block_size, long long num_blocks, void* stream) {
+  int rc = validate_sizes(0, H_kv, H_kv, head_dim, 1, block_size);
+  if (rc != PAGED_ATTN_OK) return rc;
+  const long long row = (long long)H_kv * head_dim;
+  if (rows < 0 || num_blocks < 1 || num_blocks > 0x7fffffffLL || k_stride < row ||
+      v_stride < row || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return PAGED_ATTN_ERR_SIZES;
+  if (rows == 0) return PAGED_ATTN_OK;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned16(slot_map))
+    return PAGED_ATTN_ERR_POINTER;
+  int sms = 0;
+  if ((rc = sms_of_device(&sms)) != PAGED_ATTN_OK) return rc;
+  AppendSlotsParams a;
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  a.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  a.slot_map = slot_map;
+  a.rows = rows;
+  a.H_kv = H_kv;
+  a.D = head_dim;
+  a.BS = block_size;
+  a.num_blocks = num_blocks;
+  a.status = g_check_blocks > 0 ? g_check_status : nullptr;
+  cudaError_t e = launch_append_slots(a, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+}
+
 size_t paged_attn_workspace_bytes(int num_seqs, int H_q, int H_kv, int head_dim,
                                   int max_blocks_per_seq, int block_size) {
   if (validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size) !=
@@ -1078,6 +1316,7 @@ const char* paged_attn_status_string(int status) {
     case PAGED_ATTN_ERR_STATIC_SCRATCH:
       return "sizes need more scratch than paged_attn_decode_static's fixed 4 MiB array";
     case PAGED_ATTN_ERR_FLAGS: return "unknown launch flag bits";
+    case PAGED_ATTN_ERR_MODS: return "softcap must be finite and >= 0, window >= 0";
     default: return "unknown status";
   }
 }
@@ -1115,7 +1354,7 @@ int paged_attn_reset_workspace(void* stream) {
 
 int paged_attn_last_cuda_error(void) { return g_last_cuda_error; }
 
-int paged_attn_version(void) { return 200; }
+int paged_attn_version(void) { return 300; }
 
 #ifdef PAGED_ATTN_WAIT_TEST
 // Test build only (not in include/paged_attn.h): the next decode launches of

@@ -311,6 +311,30 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// 1 / x with the hardware approximation (relative error below 2^-23); 1 / inf = 0.
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// tanh(y) for |y| < kTanhSeries from its Taylor series, y (1 - y^2/3 + 2 y^4/15 -
+// 17 y^6/315): the first dropped term is below 3.4e-7 of the result there.
+constexpr float kTanhSeries = 0.25f;
+__device__ __forceinline__ float tanh_series(float y) {
+  const float z = y * y;
+  float t = fmaf(z, -17.f / 315.f, 2.f / 15.f);
+  t = fmaf(z, t, -1.f / 3.f);
+  return fmaf(y * z, t, y);
+}
+
+// tanh(y) = 1 - 2 / (1 + e^(2y)): about 2e-7 absolute, so it serves where |y| is
+// not small (at 0.25 that is 1e-6 of the result); exact limits +-1 at +-inf.
+__device__ __forceinline__ float tanh_exp(float y) {
+  const float e = fast_exp2(y * 2.8853900817779268f);
+  return fmaf(-2.f, fast_rcp(1.f + e), 1.f);
+}
+
 // Two fp32 values -> packed bf16x2 (round to nearest even), `lo` in bits 0..15.
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;

@@ -37,7 +37,8 @@ struct SmemLayout {
   static constexpr int kQ16Stride = 2 * D + 32;       // FP8: padded f16 query row
 
   int stages, G, num_seqs;  // G: query rows of one piece (the group size, or a chunk)
-  int qo_entries = 0;       // multi-token decode: num_seqs + 1 query-row offsets
+  int qo_entries = 0;       // multi-token decode: num_seqs + 1 query-row offsets; decode with
+                            // score options: 2 num_seqs (first token and prefix of each)
   int walks = 1;            // multi-token decode: passes over the sequences (row chunks)
   // [0, bars): the ring of `stages` K/V pages (at the end of a range it holds the
   // partial states being combined); then the mbarriers full[stages],
