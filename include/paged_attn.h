@@ -452,7 +452,8 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
  *
  * workspace: at least paged_attn_mods_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use, not shared by calls that may
- * overlap; or null, for a workspace the library owns, as paged_attn_decode's
+ * overlap (one workspace serves any calls of the _mods and _shared entry points
+ * on a device, in any order); or null, for a workspace the library owns, as paged_attn_decode's
  * (its own one, so calls of the two kinds may overlap).  A stream that is
  * being captured must pass one: with a null workspace the call returns
  * PAGED_ATTN_ERR_WORKSPACE there.  Launch flags do not apply.
@@ -480,6 +481,83 @@ PAGED_ATTN_API int paged_attn_decode_fp8_mods(
 PAGED_ATTN_API size_t paged_attn_mods_workspace_bytes(int num_seqs, int H_q, int H_kv,
                                                       int head_dim, int max_blocks_per_seq,
                                                       int block_size);
+
+/*
+ * Attention of several query tokens per sequence with score options: the
+ * verification of drafted tokens, a chunk of a prompt, a whole prompt.  Any
+ * number of query rows per sequence (paged_attn_decode_multi takes up to 256 per
+ * KV head).  Sequence s owns the rows t = qo_indptr[s] + i, its last q_len =
+ * qo_indptr[s+1] - qo_indptr[s] tokens, which are already in the cache; row i
+ * stands at position pos = seq_lens[s] - q_len + i and sees the tokens t' < L with
+ *
+ *       t' < prefix_lens[s]   or
+ *       t' >= doc_starts[t]  and  (window == 0 or t' > pos - window)
+ *                            and  (is_causal == 0 or t' <= pos)
+ *
+ * with the scores of paged_attn_decode_mods, |pos - t'| the distance of the
+ * bias.  q, out, qo_indptr and total_q as paged_attn_decode_multi, except that
+ * doc_starts is [total_q] (one per row) and there is no max_q_len.  Rows that
+ * see no token are zero; rows of q no sequence owns are not written.  Tiles of
+ * 128 tokens (64 for head_dim 256) that no row of a 256-row (128-row) piece
+ * sees are not read, and cache rows that no query of the sequence sees may
+ * hold anything, NaN included; a cache row that only some of a sequence's
+ * queries see must be finite for the others' sake.
+ *
+ * The products run on the 5th-generation tensor cores (bf16 operands, the
+ * weights rounded to bf16, fp32 accumulation).  workspace: as
+ * paged_attn_decode_mods, paged_attn_multi_mods_workspace_bytes(...) bytes.
+ */
+PAGED_ATTN_API int paged_attn_decode_multi_mods(
+    const void* q, const void* k_cache, const void* v_cache, void* out,
+    const int32_t* qo_indptr, const int32_t* block_tables, const int32_t* seq_lens,
+    int num_seqs, int total_q, int H_q, int H_kv, int head_dim, int max_blocks_per_seq,
+    int block_size, float scale, int is_causal, float softcap, const float* alibi_slopes,
+    int window, const int32_t* prefix_lens, const int32_t* doc_starts, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int total_q, int H_q,
+                                                            int H_kv, int head_dim,
+                                                            int max_blocks_per_seq,
+                                                            int block_size);
+
+/*
+ * Decode of a batch whose sequences share long prefixes (system prompts, a
+ * document that many questions are about), each prefix read once for all its
+ * sequences.  Sequences group_indptr[g] .. group_indptr[g+1] - 1 form group g
+ * and begin with the prefix_lens[g] tokens that prefix_tables[g] leads to; their
+ * own tokens follow, seq_lens[s] of them, in their own blocks:
+ *
+ *   x(h, t) over the prefix's tokens (positions 0 .. P - 1) and then the
+ *   sequence's own (positions P .. P + seq_lens[s] - 1), P = prefix_lens[g]
+ *   out[s, h, :] = softmax_t(x) . V_t
+ *
+ * with the scaled products, the cap and the distance bias of
+ * paged_attn_decode_mods (the query stands at P + seq_lens[s] - 1).
+ *
+ *   group_indptr  [num_groups + 1]  int32, non-decreasing; a sequence in no group
+ *                 has no prefix
+ *   prefix_tables [num_groups, prefix_max_blocks]  int32 (read)
+ *   prefix_lens   [num_groups]  int32 (read), clamped to [0, prefix_max_blocks *
+ *                 block_size]: any length, not only whole blocks
+ *   seq_lens      [num_seqs]  a sequence's own tokens, without the prefix (0 allowed)
+ *
+ * Everything else as paged_attn_decode; rows past a prefix's or a sequence's end
+ * may hold anything.  A sequence without any token gets zero rows.  Three
+ * launches: the prefixes, the own tokens, the merge.  num_groups = 0 is
+ * paged_attn_decode_mods.  workspace: as there,
+ * paged_attn_shared_workspace_bytes(...) bytes.
+ */
+PAGED_ATTN_API int paged_attn_decode_shared(
+    const void* q, const void* k_cache, const void* v_cache, void* out,
+    const int32_t* group_indptr, const int32_t* prefix_tables, const int32_t* prefix_lens,
+    int num_groups, int prefix_max_blocks, const int32_t* block_tables, const int32_t* seq_lens,
+    int num_seqs, int H_q, int H_kv, int head_dim, int max_blocks_per_seq, int block_size,
+    float scale, float softcap, const float* alibi_slopes, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+PAGED_ATTN_API size_t paged_attn_shared_workspace_bytes(int num_seqs, int num_groups, int H_q,
+                                                        int H_kv, int head_dim,
+                                                        int max_blocks_per_seq, int block_size);
 
 /*
  * Block tables, query offsets and the slot map of a serving step, built on the

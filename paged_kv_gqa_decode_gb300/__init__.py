@@ -33,6 +33,10 @@ __all__ = [
     "paged_attn_decode_mods",
     "paged_attn_decode_fp8_mods",
     "paged_attn_mods_workspace_bytes",
+    "paged_attn_decode_multi_mods",
+    "paged_attn_multi_mods_workspace_bytes",
+    "paged_attn_decode_shared",
+    "paged_attn_shared_workspace_bytes",
     "paged_kv_assign",
     "paged_kv_append_slots",
     "paged_attn_workspace_bytes",
@@ -67,6 +71,10 @@ EXPORTED_SYMBOLS = (
     "paged_attn_decode_mods",
     "paged_attn_decode_fp8_mods",
     "paged_attn_mods_workspace_bytes",
+    "paged_attn_decode_multi_mods",
+    "paged_attn_multi_mods_workspace_bytes",
+    "paged_attn_decode_shared",
+    "paged_attn_shared_workspace_bytes",
     "paged_kv_assign",
     "paged_kv_append_slots",
     "paged_attn_status_string",
@@ -146,6 +154,15 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.paged_attn_decode_fp8_mods.restype = I
         lib.paged_attn_mods_workspace_bytes.argtypes = [I, I, I, I, I, I]
         lib.paged_attn_mods_workspace_bytes.restype = SZ
+        lib.paged_attn_decode_multi_mods.argtypes = [P] * 7 + [I] * 7 + [F, I] + mods
+        lib.paged_attn_decode_multi_mods.restype = I
+        lib.paged_attn_multi_mods_workspace_bytes.argtypes = [I] * 7
+        lib.paged_attn_multi_mods_workspace_bytes.restype = SZ
+        lib.paged_attn_decode_shared.argtypes = ([P] * 7 + [I, I, P, P] + [I] * 6 +
+                                                 [F, F, P, P, SZ, P])
+        lib.paged_attn_decode_shared.restype = I
+        lib.paged_attn_shared_workspace_bytes.argtypes = [I] * 7
+        lib.paged_attn_shared_workspace_bytes.restype = SZ
         lib.paged_kv_assign.argtypes = [P] * 10 + [I, I, I, I, I, P]
         lib.paged_kv_assign.restype = I
         lib.paged_kv_append_slots.argtypes = [P, P, LL, LL, P, P, P, I, I, I, I, LL, P]
@@ -616,6 +633,72 @@ def paged_attn_mods_workspace_bytes(num_seqs: int, H_q: int, H_kv: int, head_dim
                                     max_blocks_per_seq: int, block_size: int) -> int:
     return int(load().paged_attn_mods_workspace_bytes(num_seqs, H_q, H_kv, head_dim,
                                                       max_blocks_per_seq, block_size))
+
+
+def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, seq_lens,
+                                 scale: float, *, causal: bool = True, softcap: float = 0.0,
+                                 alibi_slopes=None, window: int = 0, prefix_lens=None,
+                                 doc_starts=None, out=None, workspace=None, stream=None):
+    """Attention of any number of query tokens per sequence with score options (see
+    paged_attn.h): q [total_q, H_q, D], sequence s owning rows qo_indptr[s] ..
+    qo_indptr[s+1] - 1 (its last tokens, already in the cache); doc_starts is
+    [total_q], one per query row; the other options as paged_attn_decode_mods."""
+    import torch
+
+    total_q, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+        q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
+        workspace, torch.bfloat16, rows="many")
+    _need("qo_indptr", qo_indptr, torch.int32, (n + 1,))
+    _same_device((qo_indptr,))
+    _check(load().paged_attn_decode_multi_mods(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        qo_indptr.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, total_q, H_q, H_kv,
+        D, maxb, BS, float(scale), 1 if causal else 0, float(softcap), _ptr(alibi_slopes),
+        int(window), _ptr(prefix_lens), _ptr(doc_starts), _ptr(workspace), _bytes(workspace),
+        _stream(stream)))
+    return out
+
+
+def paged_attn_multi_mods_workspace_bytes(num_seqs: int, total_q: int, H_q: int, H_kv: int,
+                                          head_dim: int, max_blocks_per_seq: int,
+                                          block_size: int) -> int:
+    return int(load().paged_attn_multi_mods_workspace_bytes(num_seqs, total_q, H_q, H_kv,
+                                                            head_dim, max_blocks_per_seq,
+                                                            block_size))
+
+
+def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, prefix_lens,
+                             block_tables, seq_lens, scale: float, *, softcap: float = 0.0,
+                             alibi_slopes=None, out=None, workspace=None, stream=None):
+    """Decode of sequences that share prefixes, each prefix read once (see paged_attn.h):
+    sequences group_indptr[g] .. group_indptr[g+1] - 1 begin with the prefix_lens[g]
+    tokens of prefix_tables[g] (int32 [num_groups, prefix_max_blocks]); block_tables and
+    seq_lens are those of the sequences' own tokens."""
+    import torch
+
+    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+        q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, None, None, workspace,
+        torch.bfloat16)
+    if prefix_tables.dim() != 2:
+        raise ValueError("prefix_tables must be [num_groups, prefix_max_blocks]")
+    groups, pmax = prefix_tables.shape
+    _need("prefix_tables", prefix_tables, torch.int32, (groups, pmax))
+    _need("prefix_lens", prefix_lens, torch.int32, (groups,))
+    _need("group_indptr", group_indptr, torch.int32, (groups + 1,))
+    _same_device((prefix_tables, prefix_lens, group_indptr))
+    _check(load().paged_attn_decode_shared(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
+        group_indptr.data_ptr(), prefix_tables.data_ptr(), prefix_lens.data_ptr(), groups, pmax,
+        block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
+        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace), _stream(stream)))
+    return out
+
+
+def paged_attn_shared_workspace_bytes(num_seqs: int, num_groups: int, H_q: int, H_kv: int,
+                                      head_dim: int, max_blocks_per_seq: int,
+                                      block_size: int) -> int:
+    return int(load().paged_attn_shared_workspace_bytes(num_seqs, num_groups, H_q, H_kv, head_dim,
+                                                        max_blocks_per_seq, block_size))
 
 
 def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, block_size: int,

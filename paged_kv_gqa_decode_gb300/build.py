@@ -26,7 +26,7 @@ SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d64.cu", "deco
            "decode_xp_d128.cu", "decode_xp_d256.cu", "decode_multi_d64.cu",
            "decode_multi_d128.cu", "decode_multi_d256.cu", "decode_mod_d64.cu",
            "decode_mod_d128.cu", "decode_mod_d256.cu", "decode_fp8_mod_d128.cu",
-           "decode_fp8_mod_d256.cu"]
+           "decode_fp8_mod_d256.cu", "tile_d64.cu", "tile_d128.cu", "tile_d256.cu", "merge.cu"]
 
 
 def nvcc() -> str:

@@ -14,6 +14,7 @@
 #include "assign.h"
 #include "launch.h"
 #include "paged_attn.h"
+#include "tile.h"
 
 namespace pagedattn {
 namespace {
@@ -111,6 +112,12 @@ int device_info(DeviceInfo* out, int* dev_out = nullptr) {
   g_info[dev] = tl_info[dev] = di;
   *out = di;
   return PAGED_ATTN_OK;
+}
+
+// The end of a workspace's status word and combine counters, which must be zero
+// between calls: whatever else a call puts into a workspace begins here.
+size_t counters_end(const DeviceInfo& di) {
+  return kWsAlign + round_up((size_t)di.sms * kMaxCtasPerSm * 4, kWsAlign);
 }
 
 // Everything a launch needs that depends only on sizes and the device.
@@ -232,7 +239,7 @@ int make_plan(int num_seqs, int H_q, int H_kv, int D, int BS, const DeviceInfo& 
   // which is one CTA per SM for some shapes), so a workspace reused by calls of
   // any size always finds it zero: partials never land on it.
   pl->off_counters = kWsAlign;
-  pl->off_partials = pl->off_counters + round_up((size_t)di.sms * kMaxCtasPerSm * 4, kWsAlign);
+  pl->off_partials = counters_end(di);
   pl->ws_bytes = pl->off_partials +
                  round_up((size_t)pl->grid * 2 * pl->rows * (size_t)(D + 4) * 4, kWsAlign);
   return PAGED_ATTN_OK;
@@ -324,6 +331,31 @@ int encode_cache_map(const void* base, int D, int BS, int H_kv, long long num_bl
   return PAGED_ATTN_OK;
 }
 
+// The same view with a box of one 128-byte column half of a page, {64, BS, 1, 1}:
+// the row-tile kernel stacks the halves of several pages.
+int encode_half_map(const void* base, int D, int BS, int H_kv, long long num_blocks,
+                    CUtensorMap* map) {
+  EncodeTiledFn enc = nullptr;
+  int rc = get_encoder(&enc);
+  if (rc != PAGED_ATTN_OK) return rc;
+  const cuuint64_t row_bytes = (cuuint64_t)D * 2;
+  const cuuint64_t block_bytes = row_bytes * (cuuint64_t)H_kv * BS;
+  cuuint64_t nb = (cuuint64_t)num_blocks;
+  if (num_blocks <= 0) {
+    nb = ((cuuint64_t)1 << 40) / block_bytes;
+    if (nb > 0x7fffffffULL) nb = 0x7fffffffULL;
+  }
+  const cuuint64_t dims[4] = {64, (cuuint64_t)H_kv * BS, (cuuint64_t)D / 64, nb};
+  const cuuint64_t strides[3] = {row_bytes, 128, block_bytes};
+  const cuuint32_t box[4] = {64, (cuuint32_t)BS, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
+                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cuda_fail((int)r);
+  return PAGED_ATTN_OK;
+}
+
 // x-packed caches.  A page of one KV head is contiguous in both (K [num_blocks,
 // H_kv, D / 8, BS, 8], V [num_blocks, H_kv, D, BS]) and the kernel bulk-copies
 // it, except V pages of 32 tokens, read through the 4-D view (BS, D, H_kv,
@@ -400,7 +432,7 @@ int check_pointers(const void* q, const void* k, const void* v, const void* out,
 // The tensor maps of a call through a per-thread direct-mapped cache: a map
 // depends only on the base address and the sizes it describes, so a decode
 // loop over the same caches encodes each once.
-enum MapKind { kMapBf16 = 0, kMapFp8 = 1, kMapXpackedV = 2 };
+enum MapKind { kMapBf16 = 0, kMapFp8 = 1, kMapXpackedV = 2, kMapHalf = 3 };
 
 int cached_map(const void* base, int D, int BS, int H_kv, long long num_blocks, MapKind kind,
                CUtensorMap* out) {
@@ -428,6 +460,8 @@ int cached_map(const void* base, int D, int BS, int H_kv, long long num_blocks, 
   if (kind == kMapXpackedV) {
     CUtensorMap unused;
     rc = encode_xpacked_maps(base, D, BS, H_kv, num_blocks, &unused, &m);
+  } else if (kind == kMapHalf) {
+    rc = encode_half_map(base, D, BS, H_kv, num_blocks, &m);
   } else {
     rc = encode_cache_map(base, D, BS, H_kv, num_blocks, &m, kind == kMapFp8);
   }
@@ -728,6 +762,90 @@ int decode_mods_impl(Operands& o, int head_dim, int block_size, bool fp8, void* 
   rc = optional_workspace(workspace, workspace_bytes, pl.ws_bytes, st, &o.ws);
   if (rc != PAGED_ATTN_OK) return rc;
   return run(pl, o, st);
+}
+
+// Row-tile attention (multi-token decode with score options, shared prefixes).
+constexpr int kMaxSplits = 32;  // the merge gives one lane to each part
+
+// Parts of each piece's token range: as many as fill the SMs once when the
+// pieces do not.  The part count bounds what the kernel uses (it never makes
+// parts of fewer than two tiles).
+int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms) {
+  const long long tiles = (long long)total_q * (H_q / H_kv) / tile_rows(D) + num_seqs;
+  const long long s = sms / (tiles * H_kv);
+  return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+}
+
+// Workspace of the partial states: (m, l) of every part and row, then their o.
+size_t tile_part_bytes(int D, int total_q, int H_q, int splits) {
+  const size_t rows = (size_t)splits * total_q * H_q;
+  return round_up(rows * 8, kWsAlign) + round_up(rows * D * 4, kWsAlign);
+}
+
+// Validates what the row-tile kernel's index arithmetic needs.
+bool tile_sizes_ok(int total_q, int num_seqs, int H_q, int H_kv, int D) {
+  const long long tiles = (long long)total_q * (H_q / H_kv) / tile_rows(D) + num_seqs;
+  return (long long)total_q * (H_q / H_kv) < 0x7ffffff0LL && tiles * H_kv < 0x7fffffffLL &&
+         (long long)total_q * H_q * D < (1LL << 40);
+}
+
+int launch_tiles(int D, const TileParams& p, const void* k_cache, const void* v_cache,
+                 cudaStream_t st) {
+  CUtensorMap tk, tv;
+  int rc = cached_map(k_cache, D, p.BS, p.H_kv, p.num_blocks, kMapHalf, &tk);
+  if (rc != PAGED_ATTN_OK) return rc;
+  rc = cached_map(v_cache, D, p.BS, p.H_kv, p.num_blocks, kMapHalf, &tv);
+  if (rc != PAGED_ATTN_OK) return rc;
+#ifdef PAGED_ATTN_WAIT_TEST
+  (void)st;
+  return cuda_fail(cudaErrorNotSupported);  // not in the test build
+#else
+  const cudaError_t e = D == 64    ? launch_tile_d64(tk, tv, p, st)
+                        : D == 128 ? launch_tile_d128(tk, tv, p, st)
+                                   : launch_tile_d256(tk, tv, p, st);
+  return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+#endif
+}
+
+int launch_merge_parts(const MergeParams& p, cudaStream_t st) {
+#ifdef PAGED_ATTN_WAIT_TEST
+  (void)p, (void)st;
+  return cuda_fail(cudaErrorNotSupported);
+#else
+  const cudaError_t e = launch_merge(p, st);
+  return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+#endif
+}
+
+// The parameters common to both uses.
+TileParams tile_params(const void* q, void* out, const int32_t* bt, const int32_t* lens,
+                       const int32_t* qo, int num_seqs, int total_q, int H_q, int H_kv, int maxb,
+                       int BS, float scale, float softcap, const float* slopes) {
+  TileParams t = {};
+  t.q = static_cast<const __nv_bfloat16*>(q);
+  t.out = static_cast<__nv_bfloat16*>(out);
+  t.block_tables = bt;
+  t.seq_lens = lens;
+  t.qo_indptr = qo;
+  t.num_seqs = num_seqs;
+  t.total_q = total_q;
+  t.H_q = H_q;
+  t.H_kv = H_kv;
+  t.G = H_q / H_kv;
+  t.maxb = maxb;
+  t.BS = BS;
+  t.scale_log2 = scale * 1.4426950408889634f;
+  t.cap_log2 = softcap * 1.4426950408889634f;
+  t.cap_in = softcap > 0.f ? scale / softcap : 0.f;
+  t.slopes = slopes;
+  t.num_blocks = g_check_blocks;
+  return t;
+}
+
+void set_parts(TileParams* t, uint8_t* base) {
+  const size_t rows = (size_t)t->splits * t->total_q * t->H_q;
+  t->part_ml = reinterpret_cast<float2*>(base);
+  t->part_o = reinterpret_cast<float*>(base + round_up(rows * 8, kWsAlign));
 }
 
 AppendParams append_params(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
@@ -1118,6 +1236,179 @@ int paged_attn_decode_fp8_mods(const void* q, const void* k_cache, const void* v
   o.doc_starts = doc_starts;
   return decode_mods_impl(o, head_dim, block_size, true, workspace, workspace_bytes,
                           static_cast<cudaStream_t>(stream));
+}
+
+size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int total_q, int H_q, int H_kv,
+                                             int head_dim, int max_blocks_per_seq,
+                                             int block_size) {
+  if (validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size) !=
+          PAGED_ATTN_OK ||
+      total_q < 0 || !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
+    return 0;
+  DeviceInfo di;
+  if (device_info(&di) != PAGED_ATTN_OK) return 0;
+  if (num_seqs == 0 || total_q == 0) return counters_end(di);
+  const int splits = tile_splits(head_dim, total_q, num_seqs, H_q, H_kv, di.sms);
+  return counters_end(di) + (splits > 1 ? tile_part_bytes(head_dim, total_q, H_q, splits) : 0);
+}
+
+int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void* v_cache,
+                                 void* out, const int32_t* qo_indptr,
+                                 const int32_t* block_tables, const int32_t* seq_lens,
+                                 int num_seqs, int total_q, int H_q, int H_kv, int head_dim,
+                                 int max_blocks_per_seq, int block_size, float scale,
+                                 int is_causal, float softcap, const float* alibi_slopes,
+                                 int window, const int32_t* prefix_lens,
+                                 const int32_t* doc_starts, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  int rc = validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (!std::isfinite(scale)) return PAGED_ATTN_ERR_SCALE;
+  if (total_q < 0 || !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
+    return PAGED_ATTN_ERR_SIZES;
+  rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  if (rc != PAGED_ATTN_OK || num_seqs == 0 || total_q == 0) return rc;
+  rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (!aligned16(qo_indptr)) return PAGED_ATTN_ERR_POINTER;
+  DeviceInfo di;
+  if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  TileParams t = tile_params(q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
+                             H_kv, max_blocks_per_seq, block_size, scale, softcap, alibi_slopes);
+  t.causal = is_causal ? 1 : 0;
+  t.window = window;
+  t.prefix_lens = prefix_lens;
+  t.doc_starts = doc_starts;
+  t.splits = tile_splits(head_dim, total_q, num_seqs, H_q, H_kv, di.sms);
+  t.single = t.splits == 1 ? 1 : 0;
+  const size_t parts = t.single ? 0 : tile_part_bytes(head_dim, total_q, H_q, t.splits);
+  void* ws = nullptr;
+  rc = optional_workspace(workspace, workspace_bytes, counters_end(di) + parts, st, &ws);
+  if (rc != PAGED_ATTN_OK) return rc;
+  t.status = g_check_blocks > 0 ? g_check_status : static_cast<int32_t*>(ws);
+  if (!t.single) set_parts(&t, static_cast<uint8_t*>(ws) + counters_end(di));
+  if ((rc = launch_tiles(head_dim, t, k_cache, v_cache, st)) != PAGED_ATTN_OK) return rc;
+  if (t.single) return PAGED_ATTN_OK;
+  MergeParams m = {};
+  m.part_o = t.part_o;
+  m.part_ml = t.part_ml;
+  m.splits = t.splits;
+  m.qo_indptr = qo_indptr;
+  m.num_seqs = num_seqs;
+  m.total_q = total_q;
+  m.H_q = H_q;
+  m.D = head_dim;
+  m.out = t.out;
+  return launch_merge_parts(m, st);
+}
+
+// Shared prefixes: the rows of a group's members over its prefix (row tiles),
+// every sequence's own tokens (the decode kernel, its states as the output), then
+// the merge of both.
+namespace {
+struct SharedPlan {
+  Plan own;          // the decode over the sequences' own tokens
+  int splits;        // parts of a prefix
+  size_t off_state, off_parts, bytes;
+};
+
+int shared_plan(int num_seqs, int num_groups, int H_q, int H_kv, int head_dim, int block_size,
+                SharedPlan* sp) {
+  int dev = 0;
+  DeviceInfo di;
+  int rc = device_info(&di, &dev);
+  if (rc != PAGED_ATTN_OK) return rc;
+  rc = cached_plan(num_seqs, H_q, H_kv, head_dim, block_size, dev, di, &sp->own, false, 0, 0,
+                   true);
+  if (rc != PAGED_ATTN_OK) return rc;
+  sp->splits = tile_splits(head_dim, num_seqs, num_groups, H_q, H_kv, di.sms);
+  sp->off_state = round_up(sp->own.ws_bytes, kWsAlign);
+  sp->off_parts =
+      sp->off_state + round_up((size_t)num_seqs * H_q * (head_dim + 4) * 4, kWsAlign);
+  sp->bytes = sp->off_parts + tile_part_bytes(head_dim, num_seqs, H_q, sp->splits);
+  return PAGED_ATTN_OK;
+}
+
+int shared_sizes(int num_seqs, int num_groups, int H_q, int H_kv, int head_dim,
+                 int max_blocks_per_seq, int prefix_max_blocks, int block_size) {
+  int rc = validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size);
+  if (rc == PAGED_ATTN_OK)
+    rc = validate_sizes(num_groups, H_q, H_kv, head_dim, prefix_max_blocks, block_size);
+  if (rc == PAGED_ATTN_OK && !tile_sizes_ok(num_seqs, num_groups, H_q, H_kv, head_dim))
+    rc = PAGED_ATTN_ERR_SIZES;
+  return rc;
+}
+}  // namespace
+
+size_t paged_attn_shared_workspace_bytes(int num_seqs, int num_groups, int H_q, int H_kv,
+                                         int head_dim, int max_blocks_per_seq, int block_size) {
+  if (shared_sizes(num_seqs, num_groups, H_q, H_kv, head_dim, max_blocks_per_seq, 1,
+                   block_size) != PAGED_ATTN_OK)
+    return 0;
+  SharedPlan sp;
+  return shared_plan(num_seqs, num_groups, H_q, H_kv, head_dim, block_size, &sp) == PAGED_ATTN_OK
+             ? sp.bytes
+             : 0;
+}
+
+int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_cache, void* out,
+                             const int32_t* group_indptr, const int32_t* prefix_tables,
+                             const int32_t* prefix_lens, int num_groups, int prefix_max_blocks,
+                             const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                             int H_q, int H_kv, int head_dim, int max_blocks_per_seq,
+                             int block_size, float scale, float softcap,
+                             const float* alibi_slopes, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  int rc = shared_sizes(num_seqs, num_groups, H_q, H_kv, head_dim, max_blocks_per_seq,
+                        prefix_max_blocks, block_size);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (!std::isfinite(scale)) return PAGED_ATTN_ERR_SCALE;
+  rc = mods_checks(softcap, alibi_slopes, 0, nullptr, nullptr);
+  if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
+  rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (num_groups > 0 &&
+      (!aligned16(group_indptr) || !aligned16(prefix_tables) || !aligned16(prefix_lens)))
+    return PAGED_ATTN_ERR_POINTER;
+  Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
+                        max_blocks_per_seq, scale);
+  o.softcap = softcap;
+  o.slopes = alibi_slopes;
+  if (num_groups == 0)
+    return decode_mods_impl(o, head_dim, block_size, false, workspace, workspace_bytes,
+                            static_cast<cudaStream_t>(stream));
+  SharedPlan sp;
+  rc = shared_plan(num_seqs, num_groups, H_q, H_kv, head_dim, block_size, &sp);
+  if (rc != PAGED_ATTN_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = optional_workspace(workspace, workspace_bytes, sp.bytes, st, &o.ws);
+  if (rc != PAGED_ATTN_OK) return rc;
+  apply_checks(&o);
+  uint8_t* base = static_cast<uint8_t*>(o.ws);
+  TileParams t = tile_params(q, out, prefix_tables, prefix_lens, group_indptr, num_groups,
+                             num_seqs, H_q, H_kv, prefix_max_blocks, block_size, scale, softcap,
+                             alibi_slopes);
+  t.tail_lens = seq_lens;
+  t.tail_cap = max_blocks_per_seq * block_size;
+  t.splits = sp.splits;
+  t.status = o.status ? o.status : static_cast<int32_t*>(o.ws);
+  set_parts(&t, base + sp.off_parts);
+  if ((rc = launch_tiles(head_dim, t, k_cache, v_cache, st)) != PAGED_ATTN_OK) return rc;
+  o.state = reinterpret_cast<float*>(base + sp.off_state);
+  if ((rc = run(sp.own, o, st)) != PAGED_ATTN_OK) return rc;
+  MergeParams m = {};
+  m.part_o = t.part_o;
+  m.part_ml = t.part_ml;
+  m.splits = t.splits;
+  m.qo_indptr = group_indptr;
+  m.num_seqs = num_groups;
+  m.total_q = num_seqs;
+  m.H_q = H_q;
+  m.D = head_dim;
+  m.state = o.state;
+  m.out = t.out;
+  return launch_merge_parts(m, st);
 }
 
 size_t paged_attn_mods_workspace_bytes(int num_seqs, int H_q, int H_kv, int head_dim,

@@ -1,0 +1,62 @@
+// Row-tile attention over the paged cache (tile_kernel.cuh) and the merge of its
+// partial states: the interface between the C-ABI layer and the kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace pagedattn {
+
+// Query rows of one CTA: two tiles of 128 for head_dim 64 and 128, one for 256
+// (whose accumulators fill the tensor memory).
+constexpr int tile_rows(int D) { return D == 256 ? 128 : 256; }
+// Tokens of one K/V tile.
+constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
+
+struct TileParams {
+  const __nv_bfloat16* q;       // [total_q, H_q, D]
+  __nv_bfloat16* out;           // [total_q, H_q, D]
+  const int32_t* block_tables;  // [num_seqs, maxb]
+  const int32_t* seq_lens;      // [num_seqs] cached tokens
+  const int32_t* qo_indptr;     // [num_seqs + 1] rows of q
+  int num_seqs, total_q, H_q, H_kv, G, maxb, BS, causal;
+  float scale_log2;             // scale * log2(e)
+  float cap_log2, cap_in;       // softcap * log2(e) (0: off), scale / softcap
+  const float* slopes;          // [H_q] or null
+  int window;
+  const int32_t* prefix_lens;   // [num_seqs] or null
+  const int32_t* doc_starts;    // [total_q] or null
+  // Shared prefix: query row t stands tail_lens[t] tokens past the sequence's
+  // (the prefix's) last one (null: the rows are the sequence's last tokens).
+  const int32_t* tail_lens;     // [total_q] or null
+  int tail_cap;                 // largest value tail_lens is clamped to
+  int splits;                   // parts of each piece's token range
+  int single;                   // 1: splits is 1 and the kernel writes the output itself
+  float* part_o;                // [splits][total_q * H_q][D]
+  float2* part_ml;              // [splits][total_q * H_q] (running max, log2 domain; sum)
+  int32_t* status;
+  long long num_blocks;         // > 0: block ids are checked against it
+};
+
+struct MergeParams {
+  const float* part_o;
+  const float2* part_ml;
+  int splits;
+  const int32_t* qo_indptr;  // rows [qo_indptr[0], qo_indptr[num_seqs]) have parts
+  int num_seqs, total_q, H_q, D;
+  const float* state;        // [total_q * H_q][D + 4] one more state of every row, or null
+  __nv_bfloat16* out;
+};
+
+cudaError_t launch_tile_d64(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
+                            cudaStream_t stream);
+cudaError_t launch_tile_d128(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
+                             cudaStream_t stream);
+cudaError_t launch_tile_d256(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
+                             cudaStream_t stream);
+cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
+
+}  // namespace pagedattn
