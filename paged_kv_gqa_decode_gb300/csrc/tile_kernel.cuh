@@ -12,18 +12,16 @@
 //   O = O + P V tcgen05.mma, P (bf16) in tensor memory, V in shared memory
 //
 // Roles: one warp copies pages (TMA, one box per page and 128-byte column half,
-// K and V tiles through one ring), one thread issues the products, and each warpgroup
-// of 128 threads owns the 128 rows of a score tile, a thread per row, so the
-// running maximum and sum never leave a thread.  Two warpgroups (head_dim 64 and
-// 128) work on different score tiles while the products of the other run: on the
-// two row tiles of a full piece, or, when a piece has at most 128 rows, on
-// alternate token tiles of the same rows, merged at the end.  head_dim 256 has
-// one warpgroup with two score buffers (its accumulators take half the tensor
-// memory).
-//
-// A score tile is read from tensor memory twice, in chunks of 64 columns: for its
-// maximum, then for its weights.  (Holding all 128 scores of a row in registers
-// between the two spills at the 168 registers that ten warps leave a thread.)
+// K and V tiles through one ring), one lane of another issues the products, and a
+// team of 256 threads turns a score tile into weights: two threads per row, each
+// with half of the columns in registers, exchanging only the row's maximum (one
+// thread per row with all 128 columns left two warps per SM sub-partition, too few to
+// hide their own latencies: 0.70 against TEAMMS ms on four prompt chunks).  Two teams
+// (head_dim 64 and 128) work on different score tiles while the products of the
+// other run: on the two row tiles of a full piece, or, when a piece has at most
+// 128 rows, on alternate token tiles of the same rows, merged at the end.
+// head_dim 256 has one team with two score buffers (its accumulators take half
+// the tensor memory).
 //
 // The running maximum is raised only when a tile passes it by 2^8, so most tiles
 // do not rescale O in tensor memory; the weights (at most 2^8) are rounded to bf16
@@ -43,49 +41,102 @@
 
 namespace pagedattn {
 
-constexpr int kTileStatusBadBlock = 1, kTileStatusBadLength = 2, kTileStatusTimeout = 4;
+constexpr int kTileStatusBadBlock = 1, kTileStatusBadLength = 2, kTileStatusTimeout = 4,
+              kTileStatusConfig = 8;
 constexpr float kTileLazyMax = 8.f;
 constexpr int kTileTmemColumns = 512;
 
 template <int D>
 struct TileShape {
-  static constexpr int kGroups = D == 256 ? 1 : 2;        // softmax warpgroups
+  static constexpr int kTeams = D == 256 ? 1 : 2;         // softmax teams of 256 threads
   static constexpr int kRows = tile_rows(D);
   static constexpr int BN = tile_tokens(D);
+  static constexpr int kCols = BN / 2;                    // score columns of a thread
   static constexpr int kHalves = D / 64;                  // 128-byte column halves of a row
   static constexpr int kQTileBytes = 128 * D * 2;         // one 128-row query tile
   static constexpr int kSlotBytes = BN * D * 2;           // one K or V tile
-  static constexpr int kSlots = D == 64 ? 8 : 5;
-  // softmax warpgroups, then a producer and a product warp
-  static constexpr int kThreads = kGroups * 128 + 64;
+  // Where the weights go: over the scores they come from, so that a buffer takes
+  // its next scores only after their product with V; for head_dim 64 apart, in
+  // tensor memory, so that it takes them as soon as these are in registers.  (128
+  // has no tensor memory left, and weights in shared memory were slower, 542 against
+  // 473 us on four plain prompt chunks: the products then read both operands from
+  // there, which alone takes its whole bandwidth.)
+  static constexpr bool kApart = D == 64;
+  static constexpr int kSlots = D == 64 ? 8 : 5;          // the K/V ring
+  static constexpr int kRingOff = kTeams * kQTileBytes;
+  // the teams' warps, then a producer and a product warp
+  static constexpr int kThreads = kTeams * 256 + 64;
   static constexpr int kOCol = 256;                       // first accumulator column
-  static constexpr int kBarOff = kGroups * kQTileBytes + kSlots * kSlotBytes;
-  static constexpr int kSmem = kBarOff + 1024 + 1024;     // + barriers and scalars, + alignment
+  static constexpr int kPCol = 384;                       // head_dim 64: the weights
+  // barriers and scalars (512 bytes), then
+  // the row maxima the two threads of a row exchange, [2][half][row]: a buffer for
+  // each of two teams, or two for one team's steps in turn
+  static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
+  static constexpr int kMaxOff = kBarOff + 512;
+  static constexpr int kSmem = kMaxOff + 2 * 2 * 128 * 4;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
 
-template <int D>
+// What the scores need, compiled apart so that each loop over a row holds only its
+// own arithmetic (one kernel with all three spent a third of its issue slots
+// waiting for instructions).  Plain and capped need scale > 0.
+enum { kTilePlain = 0, kTileCapped = 1, kTileGeneral = 2 };
+
+// Bits n .. 31 (all for n <= 0, none for n >= 32).
+__device__ __forceinline__ uint32_t bits_from(long long n) {
+  return n <= 0 ? 0xffffffffu : n >= 32 ? 0u : 0xffffffffu << (int)n;
+}
+
+// cap tanh(s c) - m for raw scores s, c = scale / cap, as the weights' exponent:
+// where |s c| < kTanhSeries for every score of the warp, which is the ordinary
+// case, from a polynomial with the powers of c and the cap folded into its
+// coefficients, s (a0 + s^2 (a1 + s^2 a2)): four operations a score with the
+// subtraction, and no MUFU operation.  tanh(y) / y = 1 - z / 3 + 2 z^2 / 15 -
+// 17 z^3 / 315 + ..., z = y^2; on [0, h], h = kTanhSeries^2, z^3 differs by h^3 / 32 at
+// most from 3 h z^2 / 2 - 9 h^2 z / 16 + h^3 / 32 (Chebyshev economisation), so the
+// cubic term becomes a change of the others, and the error is below 17 / 315 h^3 / 32
+// = 4.2e-7 plus the quartic term's 3.4e-7 of the score.
+struct CapSeries {
+  float a0, a1, a2;
+  float reach;  // |s| below which it holds (0: a coefficient overflowed; never used then)
+};
+__device__ __forceinline__ CapSeries cap_series(float c, float cap_log2) {
+  constexpr float h = kTanhSeries * kTanhSeries, t3 = -17.f / 315.f;
+  CapSeries t;
+  const float f = cap_log2 * c, z = c * c;
+  t.a0 = f * (1.f + t3 * h * h * h / 32.f);
+  t.a1 = f * z * (-1.f / 3.f - t3 * 9.f / 16.f * h * h);
+  t.a2 = f * z * z * (2.f / 15.f + t3 * 1.5f * h);
+  t.reach = isfinite(t.a2) ? kTanhSeries / c : 0.f;  // (c > 0)
+  return t;
+}
+__device__ __forceinline__ float cap_score(float s, float c, float cap_log2) {
+  const float y = s * c;
+  return cap_log2 * (fabsf(y) < kTanhSeries ? tanh_series(y) : tanh_exp(y));
+}
+
+template <int D, int MOD>
 __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TileParams p) {
   using T = TileShape<D>;
-  constexpr int kGroups = T::kGroups, kRows = T::kRows, BN = T::BN, kHalves = T::kHalves;
-  constexpr int kSlots = T::kSlots, kThreads = T::kThreads;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kTeams = T::kTeams, kRows = T::kRows, BN = T::BN, kHalves = T::kHalves;
+  constexpr int kThreads = T::kThreads;
+  extern __shared__ __align__(1024) uint8_t smem[];  // (no room for an alignment slack)
   uint8_t* sm_q = smem;
-  uint8_t* sm_kv = smem + kGroups * T::kQTileBytes;
+  uint8_t* sm_kv = smem + T::kRingOff;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kBarOff);
-  uint64_t* full = bars;                  // [kSlots] a tile has landed
-  uint64_t* empty = bars + kSlots;        // [kSlots] its products are done
-  uint64_t* s_full = bars + 2 * kSlots;   // [2] scores ready
-  uint64_t* p_full = s_full + 2;          // [2] weights stored, O rescaled
-  uint64_t* o_done = p_full + 2;          // [2] product with V done
+  uint64_t* full = bars;                        // [kMaxSlots] a tile has landed
+  uint64_t* empty = bars + T::kSlots;        // [kMaxSlots] its products are done
+  uint64_t* s_full = bars + 2 * T::kSlots;   // [2] scores ready
+  uint64_t* s_free = s_full + 2;                // [2] scores read (weights apart)
+  uint64_t* p_full = s_free + 2;                // [2] weights stored, O rescaled
+  uint64_t* o_done = p_full + 2;                // [2] product with V done
   uint64_t* q_full = o_done + 2;
   uint64_t* drain = q_full + 1;
-  int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 512);
+  int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 256);
   // sm_i: [0] TMEM address, [1] sequence, [2] row tile, [3] min lo, [4] max hi,
-  // [8..24) warp sums of the tile search
+  // [8..32) warp sums of the tile search
   uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(sm_i);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -93,6 +144,11 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   auto report = [&](int bits) { atomicOr(p.status, bits); };
 
   griddep_launch_dependents();
+  if (smem_addr(smem) & 1023) {  // never expected: the swizzle needs 1024-byte tiles
+    griddep_wait();
+    if (tid == 0) report(kTileStatusConfig);
+    return;
+  }
   if (tid == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
@@ -130,16 +186,17 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       sm_i[1] = -1;
       sm_i[3] = 0x7fffffff;
       sm_i[4] = -1;
-      for (int i = 0; i < kSlots; ++i) {
+      for (int i = 0; i < T::kSlots; ++i) {
         mbar_init(&full[i], 1);
         mbar_init(&empty[i], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 128);
+        mbar_init(&s_free[i], 8);  // a team's warps
+        mbar_init(&p_full[i], 8);  // a team's warps
         mbar_init(&o_done[i], 1);
       }
-      mbar_init(q_full, kGroups * 128);
+      mbar_init(q_full, kTeams * 8);
       mbar_init(drain, 1);
       fence_barrier_init();
     }
@@ -174,18 +231,19 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   }
   const int pre = p.prefix_lens != nullptr ? min(max(__ldg(p.prefix_lens + s), 0), len) : 0;
   const int n_rows = (int)min((long long)kRows, (long long)q_len * G - row0);
-  const bool both = kGroups == 2 && n_rows > 128;  // a row tile per warpgroup
+  const bool both = kTeams == 2 && n_rows > 128;  // a row tile per warpgroup
 
   // ---- this thread's row (softmax threads) and the tokens it sees
-  const int wg = warp >> 2;                // softmax warpgroup (kGroups and up: other roles)
+  const int team = warp >> 3;              // kTeams: the other roles
+  const int half = (warp >> 2) & 1;        // which columns of the row
   const int r128 = tid & 127;
-  const int rr = row0 + (both ? wg * 128 : 0) + r128;
-  const bool softmax_thread = wg < kGroups;
+  const int rr = row0 + (both ? team * 128 : 0) + r128;
+  const bool softmax_thread = team < kTeams;
   const int qi = rr / G;
   const bool valid = softmax_thread && (long long)rr < (long long)q_len * G && rr < row0 + kRows;
   long long q_row = -1;                    // row of q / out viewed as rows of D
   int lo = 0, hi = 0x7fffffff, pos = 0, head = 0;
-  if (valid) {
+  if (valid) {  // (a row's two threads agree on everything but their columns)
     head = g * G + (rr - qi * G);
     q_row = (long long)(qo + qi) * p.H_q + head;
     if (p.tail_lens != nullptr) {
@@ -204,20 +262,22 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     }
   }
   // ---- the query rows, swizzled for the products (128-byte rows, 16-byte chunk c
-  // of row r at c ^ (r % 8)); with one row tile the two warpgroups share the work
+  // of row r at c ^ (r % 8)); the threads of a row (four with one row tile for two
+  // teams) share the work
   if (softmax_thread) {
-    const int chunks = D / 8;
-    const int c0 = both || kGroups == 1 ? 0 : wg * (chunks / 2);
-    const int c1 = both || kGroups == 1 ? chunks : c0 + chunks / 2;
-    uint8_t* tile = sm_q + (both ? wg * T::kQTileBytes : 0);
-    for (int c = c0; c < c1; ++c) {
+    const int sharers = both ? 2 : 2 * kTeams, chunks = D / 8 / sharers;
+    const int c0 = (both ? half : 2 * team + half) * chunks;
+    uint8_t* tile = sm_q + (both ? team * T::kQTileBytes : 0);
+#pragma unroll 4
+    for (int c = c0; c < c0 + chunks; ++c) {
       const uint4 v = valid ? __ldg(reinterpret_cast<const uint4*>(p.q + q_row * D) + c)
                             : make_uint4(0u, 0u, 0u, 0u);
       *reinterpret_cast<uint4*>(tile + (c >> 3) * (128 * 128) + r128 * 128 +
                                 (((c & 7) ^ (r128 & 7)) << 4)) = v;
     }
     fence_proxy_async_shared();
-    mbar_arrive(q_full);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
   }
   __syncthreads();
   const int min_lo = sm_i[3], max_hi = sm_i[4];
@@ -241,7 +301,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   };
   const long long part_rows = (long long)p.total_q * p.H_q;
   if (n <= 0) {  // nothing to see here: a zero row, or an empty state
-    if (valid && (both || wg == 0)) {
+    if (valid && half == 0 && (both || team == 0)) {
       if (p.single) {
         uint4* o = reinterpret_cast<uint4*>(p.out + q_row * D);
         for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -252,17 +312,20 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     return;
   }
 
-  constexpr int kProducerWarp = kGroups * 4, kMmaWarp = kGroups * 4 + 1;
+  constexpr int kProducerWarp = kTeams * 8, kMmaWarp = kTeams * 8 + 1;
   if (warp == kMmaWarp) tmem_alloc(sm_tmem, kTileTmemColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sm_tmem;
 
-  // Items of the ring, in the order the products first use them: K_0, then K_j+1
-  // and V_j for every j, then the last V.
-  auto item_k = [&](int j) { return j == 0 ? 0 : 2 * j - 1; };
-  auto item_v = [&](int j) { return j == n - 1 ? 2 * n - 1 : 2 * j + 2; };
+  // Items of the ring, in the order the products first use them: the K tiles of
+  // the first steps, then a V tile and the K tile after those in turn.
+  const int ahead = T::kApart && !both ? 2 : 1;  // K tiles used before V_0, less one
+  auto item_k = [&](int j) { return j + max(0, j - ahead); };
+  auto item_v = [&](int j) { return j + min(n, j + 1 + ahead); };
+  constexpr int slots = T::kSlots;
+  auto slot_off = [&](int slot) -> int { return T::kRingOff + slot * T::kSlotBytes; };
   // Steps: one score tile each, alternating between the two score buffers.
   const int steps = both ? 2 * n : n;
   auto tile_of_step = [&](int k) { return both ? k >> 1 : k; };
@@ -271,191 +334,219 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     // =================================================================== producer
     const uint64_t policy = l2_evict_first_policy();
     const int pages = BN / p.BS, boxes = pages * kHalves;  // at most 16: one per lane
-    const int page = lane % pages, half = lane / pages;
+    const int page = lane % pages, half_col = lane / pages;
     auto block_of = [&](int j) -> int {  // this lane's page of tile j, -1: no row of it is seen
       if (j >= n || lane >= boxes) return -1;
       const int t0 = token_of(j) + page * p.BS;
       const bool seen = t0 < pre || (t0 <= max_hi && t0 + p.BS > min_lo);
       if (!seen) return -1;
       const int pb = __ldg(p.block_tables + (size_t)s * p.maxb + t0 / p.BS);
-      if (p.num_blocks > 0 && (pb < 0 || (long long)pb >= p.num_blocks) && half == 0)
+      if (p.num_blocks > 0 && (pb < 0 || (long long)pb >= p.num_blocks) && half_col == 0)
         report(kTileStatusBadBlock);  // the copy's bounds check reads it as zeros
       return pb;
     };
-    int b_cur = block_of(0), b_next = block_of(1);  // blocks of tiles j and j + 1
+    // blocks of the tiles V, V + 1 .. that are still to be copied
+    int b_v[4] = {block_of(0), block_of(1), block_of(2), block_of(3)};
     bool ok = true;
-    int it = 0;
+    int it = 0, slot = 0;
+    uint32_t phase = 0;
     auto copy = [&](const CUtensorMap* map, int pb) {
-      const int slot = it % kSlots;
-      ok = ok && mbar_wait(&empty[slot], (uint32_t)((it / kSlots) & 1) ^ 1u);
+      ok = ok && mbar_wait(&empty[slot], phase ^ 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return;
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], T::kSlotBytes);
       __syncwarp();
       if (lane < boxes)  // a block id of -1 is out of the map's bounds: zeros
-        tma_load_4d(sm_kv + slot * T::kSlotBytes + half * (BN * 128) + page * p.BS * 128, map,
-                    &full[slot], 0, g * p.BS, half, pb < 0 ? -1 : pb, policy);
+        tma_load_4d(smem + slot_off(slot) + half_col * (BN * 128) + page * p.BS * 128, map,
+                    &full[slot], 0, g * p.BS, half_col, pb < 0 ? -1 : pb, policy);
       ++it;
+      if (++slot == slots) {
+        slot = 0;
+        phase ^= 1u;
+      }
     };
-    copy(&tm_k, b_cur);
+    for (int j = 0; j < min(n, ahead + 1); ++j) copy(&tm_k, j == 0 ? b_v[0] : j == 1 ? b_v[1] : b_v[2]);
     for (int j = 0; j < n; ++j) {
-      const int b_after = block_of(j + 2);
-      if (j + 1 < n) copy(&tm_k, b_next);
-      copy(&tm_v, b_cur);
-      b_cur = b_next;
-      b_next = b_after;
+      const int b_after = block_of(j + 4);
+      copy(&tm_v, b_v[0]);
+      if (j + 1 + ahead < n) copy(&tm_k, ahead == 1 ? b_v[2] : b_v[3]);
+      b_v[0] = b_v[1];
+      b_v[1] = b_v[2];
+      b_v[2] = b_v[3];
+      b_v[3] = b_after;
     }
     if (!ok && lane == 0) report(kTileStatusTimeout);
     // no copy may be in flight when the CTA exits
-    for (int i = max(0, it - kSlots); i < it; ++i)
-      if (!mbar_wait(&full[i % kSlots], (uint32_t)((i / kSlots) & 1)) && lane == 0)
+    for (int i = max(0, it - slots); i < it; ++i)
+      if (!mbar_wait(&full[i % slots], (uint32_t)((i / slots) & 1)) && lane == 0)
         report(kTileStatusTimeout);
   } else if (warp == kMmaWarp) {
     // ==================================================================== products
-    if (lane == 0) {
+    // The warp walks the steps together, with warp-uniform operands, and one lane
+    // issues: the products take their operands from uniform registers.
+    {
+      const bool lead = elect_one();
+      const int n_steps = __shfl_sync(0xffffffffu, steps, 0);
+      const bool two = __shfl_sync(0xffffffffu, (int)both, 0) != 0;
+      const int n_tiles = __shfl_sync(0xffffffffu, n, 0);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       constexpr uint32_t kDescS = instr_desc(128, BN, false), kDescO = instr_desc(128, D, true);
       bool ok = mbar_wait(q_full, 0);
-      tc_fence_after();
-      const uint32_t q_addr = smem_addr(sm_q), kv_addr = smem_addr(sm_kv);
-      auto wait_item = [&](int item) {
-        ok = ok && mbar_wait(&full[item % kSlots], (uint32_t)((item / kSlots) & 1));
+      const uint32_t q_desc = desc_lo(smem_addr(smem), 16);
+      const uint32_t v_lead = ((uint32_t)(BN * 128 - 16) >> 4) << 16;  // K-major to MN-major lead
+      // The items in order: the next K and the next V tile's slot and phase.
+      int k_tile = 0, v_tile = 0;  // tiles waited for
+      auto place = [&](int item, int& slot, uint32_t& phase) {
+        slot = item % slots;
+        phase = (uint32_t)(item / slots) & 1u;
+      };
+      int k_slot = 0, v_slot = 0;
+      auto next_k = [&]() {
+        uint32_t ph;
+        place(item_k(k_tile++), k_slot, ph);
+        ok = ok && mbar_wait(&full[k_slot], ph);
+      };
+      auto next_v = [&]() {
+        uint32_t ph;
+        place(item_v(v_tile++), v_slot, ph);
+        ok = ok && mbar_wait(&full[v_slot], ph);
       };
       auto scores = [&](int k) {  // S[k & 1] = Q K^T
-        const int j = tile_of_step(k), item = item_k(j);
-        if (!both || !(k & 1)) wait_item(item);
+        if (!two || !(k & 1)) next_k();
+        if (T::kApart && k >= 2)  // step k - 2's scores are in registers
+          ok = ok && mbar_wait(&s_free[k & 1], (uint32_t)((k >> 1) - 1) & 1u);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t qa = q_addr + (both && (k & 1) ? T::kQTileBytes : 0);
-        const uint32_t ka = kv_addr + (item % kSlots) * T::kSlotBytes;
+        const uint32_t qd = q_desc + (two && (k & 1) ? T::kQTileBytes >> 4 : 0);
+        const uint32_t kd = q_desc + (slot_off(k_slot) >> 4);
+        if (lead) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + (k & 1) * BN,
-                 smem_desc(qa + (kk >> 2) * (128 * 128) + (kk & 3) * 32, 16, 1024),
-                 smem_desc(ka + (kk >> 2) * (BN * 128) + (kk & 3) * 32, 16, 1024), kDescS, kk > 0);
-        mma_commit(&s_full[k & 1]);
-        if (!both || (k & 1)) mma_commit(&empty[item % kSlots]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ss(tm + (k & 1) * BN, qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                   kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), kDescS, kk > 0);
+          mma_commit(&s_full[k & 1]);
+          if (!two || (k & 1)) mma_commit(&empty[k_slot]);
+        }
+        __syncwarp();
       };
-      auto values = [&](int k) {  // O = O + P[k & 1] V
-        const int j = tile_of_step(k), item = item_v(j);
+      auto values = [&](int k) {  // O = O + P V
+        if (!two || !(k & 1)) next_v();
         ok = ok && mbar_wait(&p_full[k & 1], (uint32_t)((k >> 1) & 1));
-        if (!both || !(k & 1)) wait_item(item);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const int o = kGroups == 2 ? (k & 1) : 0;
-        const bool first = kGroups == 2 ? k < 2 : k == 0;
-        const uint32_t va = kv_addr + (item % kSlots) * T::kSlotBytes;
+        const int o = kTeams == 2 ? (k & 1) : 0;
+        const bool first = kTeams == 2 ? k < 2 : k == 0;
+        const uint32_t vd = q_desc + v_lead + (slot_off(v_slot) >> 4);
+        if (lead) {
 #pragma unroll
-        for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tmem + T::kOCol + o * D, tmem + (k & 1) * BN + kk * 8,
-                 smem_desc(va + kk * 2048, BN * 128, 1024), kDescO, !first || kk > 0);
-        mma_commit(&o_done[o]);
-        if (!both || (k & 1)) mma_commit(&empty[item % kSlots]);
+          for (int kk = 0; kk < BN / 16; ++kk) {
+            mma_ts(tm + T::kOCol + o * D,
+                   tm + (T::kApart ? T::kPCol + (k & 1) * (BN / 2) : (k & 1) * BN) + kk * 8,
+                   vd + (kk * 2048 >> 4), kDescO, !first || kk > 0);
+          }
+          // (two teams over their scores need only their last product's completion)
+          if (kTeams == 1 || T::kApart || k + 2 >= n_steps) mma_commit(&o_done[k & 1]);
+          if (!two || (k & 1)) mma_commit(&empty[v_slot]);
+        }
+        __syncwarp();
       };
       scores(0);
-      if (steps > 1) scores(1);
-      for (int k = 0; k < steps; ++k) {
+      if (n_steps > 1) scores(1);
+      for (int k = 0; k < n_steps; ++k) {
+        if (T::kApart && k + 2 < n_steps) scores(k + 2);
         values(k);
-        if (k + 2 < steps) scores(k + 2);
+        if (!T::kApart && k + 2 < n_steps) scores(k + 2);
       }
-      mma_commit(drain);
+      if (lead) mma_commit(drain);
       if (!mbar_wait(drain, 0)) ok = false;
-      if (!ok) report(kTileStatusTimeout);
+      if (!ok && lead) report(kTileStatusTimeout);
     }
     __syncwarp();
   } else {
     // ===================================================================== softmax
+    constexpr int kCols = T::kCols;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t o_addr = tmem + lane_base + T::kOCol + (kGroups == 2 ? wg * D : 0);
-    float m = -INFINITY, l = 0.f;
+    const uint32_t o_addr =
+        tmem + lane_base + T::kOCol + (kTeams == 2 ? team * D : 0) + half * (D / 2);
+    float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * 256;
+    const uint32_t pair_bar = 1 + team * 4 + (warp & 3);  // the two warps of 32 rows
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+    };
+    float m = -INFINITY, l = 0.f;  // l: over this thread's columns
     bool ok = true;
-    int done = 0;  // products with V waited for
-    const float slope = valid && p.slopes != nullptr
+    const float slope = MOD == kTileGeneral && valid && p.slopes != nullptr
                             ? __ldg(p.slopes + head) * 1.4426950408889634f
                             : 0.f;
-    const bool capped = p.cap_log2 > 0.f, biased = p.slopes != nullptr;
-    // raw scores serve where the log2 score is a positive multiple of them
-    const bool raw = !capped && !biased && p.scale_log2 > 0.f;
-    const bool ordered = !biased && p.scale_log2 > 0.f;
-    const float factor = raw ? p.scale_log2 : 1.f;
+    CapSeries cap = {};
+    if constexpr (MOD == kTileCapped) cap = cap_series(p.cap_in, p.cap_log2);
     const int last_seen = max(max_hi, pre - 1);
-    constexpr int kStep = kGroups;  // this warpgroup's steps: wg, wg + kStep, ...
-    for (int k = wg; k < steps; k += kStep) {
+    for (int k = team; k < steps; k += kTeams) {
       const int buf = k & 1, j = tile_of_step(k), t0 = token_of(j);
+      const int c0 = t0 + half * kCols;  // token of this thread's first column
       const uint32_t s_addr = tmem + lane_base + buf * BN;
-      ok = ok && mbar_wait(&s_full[buf], (uint32_t)((k >> 1) & 1));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const bool whole = (t0 >= lo && t0 + BN - 1 <= hi) || t0 + BN <= pre;
-      const bool masked = !__all_sync(0xffffffffu, whole);
-      const int m_a = lo - t0, m_b = hi - t0, m_c = pre - t0;
-      auto unseen = [&](int i) { return !((i >= m_a && i <= m_b) || i < m_c); };
-      // 64 raw scores x (columns c..) -> the log2 domain, unless `raw`
-      auto transform = [&](uint32_t* x, int c) {
-        if (capped) {
-          bool big = false;
+      ok = ok && warp_wait(&s_full[buf], (uint32_t)((k >> 1) & 1));
+      if (ok) tc_fence_after();
+      float x[kCols];  // this thread's scores (a timeout leaves what is there: the walk goes
+                       // on without waiting, so that the row's threads stay together)
+      tmem_ld_begin(s_addr + half * kCols, x);
+      tmem_ld_end(x);
+      if constexpr (MOD == kTileGeneral) {
+        if (p.cap_log2 > 0.f) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const float y = __uint_as_float(x[i]) * p.cap_in;
-            big |= !(fabsf(y) < kTanhSeries);
-            x[i] = __float_as_uint(y);
-          }
-          // the series where every score of the warp is small next to the cap, which
-          // is the ordinary case and costs no MUFU operation
-          if (__any_sync(0xffffffffu, big)) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const float y = __uint_as_float(x[i]);
-              const float a = tanh_series(y), b = tanh_exp(y);
-              x[i] = __float_as_uint(p.cap_log2 * (fabsf(y) < kTanhSeries ? a : b));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              x[i] = __float_as_uint(p.cap_log2 * tanh_series(__uint_as_float(x[i])));
-          }
+          for (int i = 0; i < kCols; ++i) x[i] = cap_score(x[i], p.cap_in, p.cap_log2);
         } else {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            x[i] = __float_as_uint(__uint_as_float(x[i]) * p.scale_log2);
+          for (int i = 0; i < kCols; ++i) x[i] *= p.scale_log2;
         }
-        if (biased) {
-          const float d0 = (float)(pos - t0 - c);
+        const float d0 = (float)(pos - c0);
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            x[i] = __float_as_uint(fmaf(-slope, fabsf(d0 - (float)i), __uint_as_float(x[i])));
+        for (int i = 0; i < kCols; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
+      }
+      // ---- unseen tokens: a bit per column, from the interval ends
+      const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
+      const bool ragged = !__all_sync(0xffffffffu, whole);
+      if (ragged) {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          const uint32_t bits = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
+                                ~bits_from(pre - c0 - c);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (!(bits >> i & 1u)) x[c + i] = -INFINITY;
         }
-      };
-      // ---- first pass: the tile's maximum.  Scaling by a positive factor and the cap
-      // keep the order, so then only the maximum itself is transformed.
+      }
+      // ---- running maximum, raised only past kTileLazyMax.  Scaling by a positive
+      // factor and the cap keep the order: there only the maximum is transformed.
       float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < BN; c += 64) {
-        uint32_t x[64];
-        tmem_ld64(s_addr + c, x);
-        if (!ordered) transform(x, c);
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (unseen(c + i)) x[i] = 0xff800000u;  // -inf
-        }
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          mx0 = fmaxf(mx0, __uint_as_float(x[i]));
-          mx1 = fmaxf(mx1, __uint_as_float(x[i + 1]));
-          mx2 = fmaxf(mx2, __uint_as_float(x[i + 2]));
-          mx3 = fmaxf(mx3, __uint_as_float(x[i + 3]));
-        }
+      for (int i = 0; i < kCols; i += 8) {
+        mx0 = max3(mx0, x[i], x[i + 1]);
+        mx1 = max3(mx1, x[i + 2], x[i + 3]);
+        mx2 = max3(mx2, x[i + 4], x[i + 5]);
+        mx3 = max3(mx3, x[i + 6], x[i + 7]);
       }
-      float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-      if (ordered && mx != -INFINITY) {
-        if (capped) {
-          const float y = mx * p.cap_in;
-          mx = p.cap_log2 * (fabsf(y) < kTanhSeries ? tanh_series(y) : tanh_exp(y));
-        } else {
-          mx *= p.scale_log2;
-        }
+      const float own = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+      float mx = own;
+      // the other half's; where the packed weights overwrite the scores, its thread
+      // has read them by then
+      float* exchange = sm_max + (kTeams == 1 ? (k & 1) * 256 : 0);
+      exchange[half * 128 + r128] = mx;
+      named_barrier(pair_bar, 64);
+      mx = fmaxf(mx, exchange[(half ^ 1) * 128 + r128]);
+      if constexpr (T::kApart) {
+        // The score buffer may take its next scores, and the exchange its next maxima:
+        // they come from those scores.  (One team's two buffers alternate; a thread
+        // writes one again only after its pair's barrier of the step between.)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[buf]);
       }
+      if constexpr (MOD == kTilePlain) mx *= p.scale_log2;  // (-inf stays: the factor is positive)
+      if constexpr (MOD == kTileCapped)
+        mx = mx == -INFINITY ? mx : cap_score(mx, p.cap_in, p.cap_log2);
       float alpha = 1.f;
       if (mx > m + kTileLazyMax) {
         alpha = fast_exp2(m - mx);
@@ -463,59 +554,87 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         l *= alpha;
       }
       const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: weights 0
-      // ---- second pass: the weights, over the scores they come from (columns c / 2 ..
-      // of the packed weights cover scores already read)
-      float l0 = 0.f, l1 = 0.f;
+      // ---- The weights' place is free, and O may be rescaled, once the product of
+      // this team's step before is done.  Over the scores that is so as these exist
+      // (they were issued after it), except for one team's, whose O the step between
+      // works on.
+      if (T::kApart && k >= kTeams) ok = ok && warp_wait(&o_done[buf], (uint32_t)((k >> 1) - 1) & 1u);
+      // ---- weights 2^(x - m), 16 packed columns at a time
+      float2 sum = make_float2(0.f, 0.f);
+      const float2 sub2 = make_float2(-sub, -sub);
+      auto emit = [&](auto&& exponent) {
 #pragma unroll
-      for (int c = 0; c < BN; c += 64) {
-        uint32_t x[64], w[32];
-        tmem_ld64(s_addr + c, x);
-        if (!raw) transform(x, c);
-        if (masked) {
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (unseen(c + i)) x[i] = 0xff800000u;
+          for (int i = 0; i < 16; ++i) {
+            float2 e = exponent(make_float2(x[c + 2 * i], x[c + 2 * i + 1]));
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum = add2(sum, e);
+            w[i] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st((T::kApart ? tmem + lane_base + T::kPCol + buf * (BN / 2) : s_addr) +
+                      half * (kCols / 2) + c / 2,
+                  w);
         }
+      };
+      if constexpr (MOD == kTileCapped) {
+        float n0 = 0.f, n1 = 0.f;
+        if (!ragged) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(fmaf(__uint_as_float(x[2 * i]), factor, -sub));
-          const float b = fast_exp2(fmaf(__uint_as_float(x[2 * i + 1]), factor, -sub));
-          l0 += a;
-          l1 += b;
-          w[i] = pack_bf16x2(a, b);
+          for (int i = 0; i < kCols; i += 4) {
+            n0 = min3(n0, x[i], x[i + 1]);
+            n1 = min3(n1, x[i + 2], x[i + 3]);
+          }
         }
-        tmem_st32(s_addr + c / 2, w);
+        // (a NaN is not carried by the extremes; the series keeps it.  A ragged tile's
+        // -inf scores take the other way.)
+        if (!ragged && __all_sync(0xffffffffu, fmaxf(own, -fminf(n0, n1)) < cap.reach)) {
+          const float2 a0 = make_float2(cap.a0, cap.a0), a1 = make_float2(cap.a1, cap.a1);
+          const float2 a2 = make_float2(cap.a2, cap.a2);
+          emit([&](float2 s) {
+            const float2 z = mul2(s, s);
+            return fma2(s, fma2(z, fma2(z, a2, a1), a0), sub2);
+          });
+        } else {
+          emit([&](float2 s) {
+            const float a = cap_score(s.x, p.cap_in, p.cap_log2);
+            const float b = cap_score(s.y, p.cap_in, p.cap_log2);
+            return make_float2((s.x == -INFINITY ? s.x : a) - sub,
+                               (s.y == -INFINITY ? s.y : b) - sub);
+          });
+        }
+      } else {
+        const float f = MOD == kTilePlain ? p.scale_log2 : 1.f;
+        emit([&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
       }
-      l += l0 + l1;
+      l += sum.x + sum.y;
       tmem_st_wait();
-      // ---- O of the step before, rescaled where the maximum rose
-      if (k >= kStep) {
-        ok = ok && mbar_wait(&o_done[kGroups == 2 ? wg : 0], (uint32_t)(done & 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++done;
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+      // ---- O of the step before, rescaled where the maximum rose (each thread its
+      // half of the columns)
+      if (k >= kTeams && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if constexpr (kTeams == 1)
+          ok = ok && warp_wait(&o_done[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1u);
           tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) {
+            float o[32];
+            tmem_ld_begin(o_addr + c, o);
+            tmem_ld_end(o);
 #pragma unroll
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + c, o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(o_addr + c, o);
+            for (int i = 0; i < 32; ++i) o[i] *= alpha;
+            tmem_st(o_addr + c, o);
           }
           tmem_st_wait();
-        }
       }
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
-      if ((!both || wg == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
+      if ((!both || team == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
         const int item = item_v(j);
-        ok = ok && mbar_wait(&full[item % kSlots], (uint32_t)((item / kSlots) & 1));
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        uint8_t* v = sm_kv + (item % kSlots) * T::kSlotBytes;
-        for (int c = r128; c < BN * kHalves * 8; c += 128) {
+        ok = ok && warp_wait(&full[item % slots], (uint32_t)((item / slots) & 1));
+        uint8_t* v = smem + slot_off(item % slots);
+        for (int c = half * 128 + r128; ok && c < BN * kHalves * 8; c += 256) {
           const int row = (c >> 3) % BN, t = t0 + row;
           if (t > last_seen || (t < min_lo && t >= pre))
             *reinterpret_cast<uint4*>(v + (c >> 3) / BN * (BN * 128) + row * 128 +
@@ -524,75 +643,88 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         fence_proxy_async_shared();
       }
       tc_fence_before();
-      mbar_arrive(&p_full[buf]);
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&p_full[buf]);
     }
-    // ---- the last product of this warpgroup
-    const bool worked = wg < steps;
-    if (ok && worked) ok = mbar_wait(&o_done[kGroups == 2 ? wg : 0], (uint32_t)(done & 1));
-    ok = __all_sync(0xffffffffu, ok);
+    // ---- the last product of this team
+    if (team < steps) {
+      const int last = kTeams == 2 ? (steps - 1 - team) / 2 * 2 + team : steps - 1;  // its step
+      ok = ok && warp_wait(&o_done[last & 1],
+                           kTeams == 1 || T::kApart ? (uint32_t)(last >> 1) & 1u : 0u);
+    }
     if (!ok && lane == 0) report(kTileStatusTimeout);
     tc_fence_after();
-    // ---- one row tile: the second warpgroup hands its state over through the ring
-    // (idle once both have seen their last product), [D][128] floats, then (m, l)
-    const bool merge = kGroups == 2 && !both && steps > 1;
-    float* sm_o = reinterpret_cast<float*>(sm_kv);
+    // ---- the row's sum from its two threads
+    {
+      float* exchange = sm_max;
+      named_barrier(pair_bar, 64);  // every read of the maxima is done
+      exchange[half * 128 + r128] = l;
+      named_barrier(pair_bar, 64);
+      l = half == 0 ? l + exchange[128 + r128] : exchange[r128] + l;
+    }
+    // ---- one row tile: the second team hands its state over through the ring (idle
+    // once both have seen their last product), [D][128] floats, then (m, l)
+    const bool merge = kTeams == 2 && !both && steps > 1;
+    float* sm_o = reinterpret_cast<float*>(sm_kv) + half * (D / 2) * 128;
     float2* sm_ml = reinterpret_cast<float2*>(sm_kv + D * 128 * 4);
     float f_own = 1.f, f_other = 0.f;
     if (merge) {
-      named_barrier(1, kGroups * 128);
-      if (wg == 1) {
+      named_barrier(9, kTeams * 256);
+      if (team == 1) {
+#pragma unroll 1
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          tmem_ld_begin(o_addr + c, o);
+          tmem_ld_end(o);
 #pragma unroll
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_addr + c, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) sm_o[(c + i) * 128 + r128] = __uint_as_float(o[i]);
+          for (int i = 0; i < 32; ++i) sm_o[(c + i) * 128 + r128] = o[i];
         }
-        sm_ml[r128] = make_float2(m, l);
+        if (half == 0) sm_ml[r128] = make_float2(m, l);
       }
-      named_barrier(1, kGroups * 128);
-      if (wg == 0) {
-        const float2 x = sm_ml[r128];
-        const float top = fmaxf(m, x.x);
+      named_barrier(9, kTeams * 256);
+      if (team == 0) {
+        const float2 y = sm_ml[r128];
+        const float top = fmaxf(m, y.x);
         f_own = m == -INFINITY ? 0.f : fast_exp2(m - top);
-        f_other = x.x == -INFINITY ? 0.f : fast_exp2(x.x - top);
-        l = l * f_own + (f_other > 0.f ? x.y * f_other : 0.f);
+        f_other = y.x == -INFINITY ? 0.f : fast_exp2(y.x - top);
+        l = l * f_own + (f_other > 0.f ? y.y * f_other : 0.f);
         m = top;
       }
     }
-    if (both || wg == 0) {
+    if (both || team == 0) {
       const float inv = p.single ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-#pragma unroll
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        tmem_ld32(o_addr + c, o);
-        float y[32];
+#pragma unroll 1
+      for (int c = 0; c < D / 2; c += 32) {
+        float o[32];
+        tmem_ld_begin(o_addr + c, o);
+        tmem_ld_end(o);
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          y[i] = __uint_as_float(o[i]);
           if (merge)
-            y[i] = y[i] * f_own + (f_other > 0.f ? sm_o[(c + i) * 128 + r128] * f_other : 0.f);
-          y[i] *= inv;
+            o[i] = o[i] * f_own + (f_other > 0.f ? sm_o[(c + i) * 128 + r128] * f_other : 0.f);
+          o[i] *= inv;
         }
         if (valid) {
+          const int col = half * (D / 2) + c;
           if (p.single) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + q_row * D + c);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + q_row * D + col);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16x2(y[8 * i], y[8 * i + 1]),
-                                  pack_bf16x2(y[8 * i + 2], y[8 * i + 3]),
-                                  pack_bf16x2(y[8 * i + 4], y[8 * i + 5]),
-                                  pack_bf16x2(y[8 * i + 6], y[8 * i + 7]));
+              dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                  pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                  pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                  pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
           } else {
             float4* dst =
-                reinterpret_cast<float4*>(p.part_o + (split * part_rows + q_row) * D + c);
+                reinterpret_cast<float4*>(p.part_o + (split * part_rows + q_row) * D + col);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
       }
-      if (valid && !p.single) p.part_ml[split * part_rows + q_row] = make_float2(m, l);
+      if (valid && half == 0 && !p.single)
+        p.part_ml[split * part_rows + q_row] = make_float2(m, l);
     }
     tc_fence_before();
   }
@@ -603,12 +735,12 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   }
 }
 
-template <int D>
-cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
-                        cudaStream_t stream) {
+template <int D, int MOD>
+cudaError_t launch_tile_as(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
+                           cudaStream_t stream) {
   using T = TileShape<D>;
   static std::atomic<bool> limit_raised[64];
-  auto kernel = paged_tile_kernel<D>;
+  auto kernel = paged_tile_kernel<D, MOD>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -631,6 +763,15 @@ cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tv, const Tile
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
+}
+
+template <int D>
+cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
+                        cudaStream_t stream) {
+  if (p.slopes != nullptr || !(p.scale_log2 > 0.f))
+    return launch_tile_as<D, kTileGeneral>(tk, tv, p, stream);
+  return p.cap_log2 > 0.f ? launch_tile_as<D, kTileCapped>(tk, tv, p, stream)
+                          : launch_tile_as<D, kTilePlain>(tk, tv, p, stream);
 }
 
 }  // namespace pagedattn
