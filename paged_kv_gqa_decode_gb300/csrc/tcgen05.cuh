@@ -150,41 +150,47 @@ __host__ __device__ constexpr uint32_t instr_desc(int M, int N, bool b_mn) {
          (uint32_t)(M >> 4) << 24;
 }
 
-// One thread: D (TMEM) = A B (+ D when acc), K = 16.  A in shared memory or in TMEM;
-// shared operands by the low words of their descriptors.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
-                                       bool acc) {
+// The warp in step, one lane of it (`lead`) issuing: D (TMEM) = A B (+ D when acc),
+// K = 16.  A in shared memory or in TMEM; shared operands by the low words of
+// their descriptors.  The predicate sits on the instruction itself, so the
+// operands are computed in warp-uniform code and reach it in uniform registers.
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a_lo, uint32_t b_lo,
+                                       uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "setp.ne.u32 q, %6, 0;\n\t"
       "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(acc ? 1u : 0u)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(acc ? 1u : 0u), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
-                                       bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b_lo,
+                                       uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+      "setp.ne.u32 q, %6, 0;\n\t"
       "mov.b64 b, {%2, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(acc ? 1u : 0u)
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"(kDescHi), "r"(acc ? 1u : 0u), "r"(lead)
       : "memory");
 }
 
 // True in one lane of a converged warp (always the same one).
-__device__ __forceinline__ bool elect_one() {
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(r));
-  return r != 0;
+  return r;
 }
 
-// Arrives on `bar` once every tcgen05.mma this thread has issued has completed.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+// Arrives on `bar` once every tcgen05.mma the leading lane has issued has completed.
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar)),
+      "r"(lead)
       : "memory");
 }
 

@@ -50,31 +50,30 @@ template <int D>
 struct TileShape {
   static constexpr int kTeams = D == 256 ? 1 : 2;         // softmax teams of 256 threads
   static constexpr int kRows = tile_rows(D);
-  static constexpr int BN = tile_tokens(D);
+  static constexpr int BN = kTileTokens;
   static constexpr int kCols = BN / 2;                    // score columns of a thread
   static constexpr int kHalves = D / 64;                  // 128-byte column halves of a row
   static constexpr int kQTileBytes = 128 * D * 2;         // one 128-row query tile
   static constexpr int kSlotBytes = BN * D * 2;           // one K or V tile
-  // Where the weights go: over the scores they come from, so that a buffer takes
-  // its next scores only after their product with V; for head_dim 64 apart, in
-  // tensor memory, so that it takes them as soon as these are in registers.  (128
-  // has no tensor memory left, and weights in shared memory were slower, 542 against
-  // 473 us on four plain prompt chunks: the products then read both operands from
-  // there, which alone takes its whole bandwidth.)
-  static constexpr bool kApart = D == 64;
-  static constexpr int kSlots = D == 64 ? 8 : 5;          // the K/V ring
+  static constexpr int kSlots = D == 64 ? 15 : D == 128 ? 9 : 5;
+  // The product warp and the producers, then the teams' warps.  A warp's tensor
+  // copies are issued one after the other, about 54 cycles each and 214 for a group,
+  // whatever their size (measured on 2, 4 and 8 KB boxes), and warps side by side:
+  // one producer brings 2 KB boxes at 18 to 30 bytes a cycle, three at 50 to 70.
+  // Slot s of the ring belongs to producer s % kProducers, which so waits for its
+  // phases strictly in order (a parity wait cannot tell phase k from k - 2).
+  static constexpr int kProducers = D == 256 ? 5 : 3;
+  static_assert(kSlots % kProducers == 0, "a slot belongs to one producer");
+  static constexpr int kThreads = kTeams * 256 + 32 + kProducers * 32;
+  // tensor memory: two score buffers for each team, then the accumulators
+  static constexpr int kOCol = 256;
+  // shared memory: query tiles, the K/V ring, barriers (384 bytes) and scalars, the
+  // row maxima the two threads of a row exchange, [team][2][half][row]
   static constexpr int kRingOff = kTeams * kQTileBytes;
-  // the teams' warps, then a producer and a product warp
-  static constexpr int kThreads = kTeams * 256 + 64;
-  static constexpr int kOCol = 256;                       // first accumulator column
-  static constexpr int kPCol = 384;                       // head_dim 64: the weights
-  // barriers and scalars (512 bytes), then
-  // the row maxima the two threads of a row exchange, [2][half][row]: a buffer for
-  // each of two teams, or two for one team's steps in turn
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
-  static constexpr int kSmem = kMaxOff + 2 * 2 * 128 * 4;
-  static_assert(kSmem <= 227 * 1024, "shared memory of a block");
+  static constexpr int kSmem = kMaxOff + kTeams * 2 * 2 * 128 * 4;
+  static_assert(kSmem <= 227 * 1024 && (2 * kSlots + 14) * 8 <= 384, "shared memory of a block");
 };
 
 // What the scores need, compiled apart so that each loop over a row holds only its
@@ -126,15 +125,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   uint8_t* sm_q = smem;
   uint8_t* sm_kv = smem + T::kRingOff;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::kBarOff);
-  uint64_t* full = bars;                        // [kMaxSlots] a tile has landed
-  uint64_t* empty = bars + T::kSlots;        // [kMaxSlots] its products are done
-  uint64_t* s_full = bars + 2 * T::kSlots;   // [2] scores ready
-  uint64_t* s_free = s_full + 2;                // [2] scores read (weights apart)
-  uint64_t* p_full = s_free + 2;                // [2] weights stored, O rescaled
-  uint64_t* o_done = p_full + 2;                // [2] product with V done
-  uint64_t* q_full = o_done + 2;
+  uint64_t* full = bars;                     // [kSlots] a tile has landed
+  uint64_t* empty = bars + T::kSlots;        // [kSlots] its products are done
+  uint64_t* s_full = bars + 2 * T::kSlots;   // [team][2] scores ready
+  uint64_t* p_full = s_full + 4;             // [team][2] weights stored, O rescaled
+  uint64_t* o_done = p_full + 4;             // [team][2] product with V done
+  uint64_t* q_full = o_done + 4;
   uint64_t* drain = q_full + 1;
-  int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 256);
+  int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 384);
   // sm_i: [0] TMEM address, [1] sequence, [2] row tile, [3] min lo, [4] max hi,
   // [8..32) warp sums of the tile search
   uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(sm_i);
@@ -190,9 +188,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         mbar_init(&full[i], 1);
         mbar_init(&empty[i], 1);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&s_free[i], 8);  // a team's warps
         mbar_init(&p_full[i], 8);  // a team's warps
         mbar_init(&o_done[i], 1);
       }
@@ -234,11 +231,15 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   const bool both = kTeams == 2 && n_rows > 128;  // a row tile per warpgroup
 
   // ---- this thread's row (softmax threads) and the tokens it sees
-  const int team = warp >> 3;              // kTeams: the other roles
-  const int half = (warp >> 2) & 1;        // which columns of the row
-  const int r128 = tid & 127;
+  // The first warp issues products, the next ones copies.  Row r of
+  // a tile belongs to the warps with warp % 4 = r / 32, whose part of the tensor
+  // memory that is.
+  constexpr int kMmaWarp = 0, kTeamWarp = 1 + T::kProducers;  // (threads are whole teams)
+  const int team = (warp - kTeamWarp) >> 3;        // -1: the other roles
+  const int half = ((warp - kTeamWarp) >> 2) & 1;  // which columns of the row
+  const int r128 = (warp & 3) * 32 + lane;
   const int rr = row0 + (both ? team * 128 : 0) + r128;
-  const bool softmax_thread = team < kTeams;
+  const bool softmax_thread = warp >= kTeamWarp;
   const int qi = rr / G;
   const bool valid = softmax_thread && (long long)rr < (long long)q_len * G && rr < row0 + kRows;
   long long q_row = -1;                    // row of q / out viewed as rows of D
@@ -312,154 +313,159 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     return;
   }
 
-  constexpr int kProducerWarp = kTeams * 8, kMmaWarp = kTeams * 8 + 1;
   if (warp == kMmaWarp) tmem_alloc(sm_tmem, kTileTmemColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *sm_tmem;
 
+  // A team's step is one score tile: every token tile with two row tiles, else (two
+  // teams on one row tile) every other one.
+  const int stride = kTeams == 2 && !both ? 2 : 1;  // token tiles from step to step
   // Items of the ring, in the order the products first use them: the K tiles of
-  // the first steps, then a V tile and the K tile after those in turn.
-  const int ahead = T::kApart && !both ? 2 : 1;  // K tiles used before V_0, less one
+  // every team's first two steps, then a V tile and the K tile `ahead` + 1 further on.
+  const int ahead = 2 * stride - 1;
   auto item_k = [&](int j) { return j + max(0, j - ahead); };
   auto item_v = [&](int j) { return j + min(n, j + 1 + ahead); };
   constexpr int slots = T::kSlots;
   auto slot_off = [&](int slot) -> int { return T::kRingOff + slot * T::kSlotBytes; };
-  // Steps: one score tile each, alternating between the two score buffers.
-  const int steps = both ? 2 * n : n;
-  auto tile_of_step = [&](int k) { return both ? k >> 1 : k; };
 
-  if (warp == kProducerWarp) {
+  if (warp > kMmaWarp && warp < kTeamWarp) {
     // =================================================================== producer
     const uint64_t policy = l2_evict_first_policy();
-    const int pages = BN / p.BS, boxes = pages * kHalves;  // at most 16: one per lane
+    const int pages = BN / p.BS, boxes = pages * kHalves;  // at most 16 boxes: one per lane
     const int page = lane % pages, half_col = lane / pages;
-    auto block_of = [&](int j) -> int {  // this lane's page of tile j, -1: no row of it is seen
-      if (j >= n || lane >= boxes) return -1;
-      const int t0 = token_of(j) + page * p.BS;
+    // This warp's items are first, first + kProducers, ...; the K or V tile of each:
+    const int first = warp - 1, lead = min(n, ahead + 1), mixed = 2 * (n - lead);
+    auto tile_of = [&](int it, bool& is_v) -> int {
+      const int u = it - lead;
+      is_v = u >= 0 && (u >= mixed || !(u & 1));
+      return u < 0 ? it : u >= mixed ? n - lead + (u - mixed) : is_v ? u >> 1 : ahead + 1 + (u >> 1);
+    };
+    auto block_of = [&](int it) -> int {  // this lane's page, -1: no row of it is seen
+      if (it >= 2 * n || lane >= boxes) return -1;
+      bool is_v;
+      const int t0 = token_of(tile_of(it, is_v)) + page * p.BS;
       const bool seen = t0 < pre || (t0 <= max_hi && t0 + p.BS > min_lo);
       if (!seen) return -1;
       const int pb = __ldg(p.block_tables + (size_t)s * p.maxb + t0 / p.BS);
-      if (p.num_blocks > 0 && (pb < 0 || (long long)pb >= p.num_blocks) && half_col == 0)
+      if (p.num_blocks > 0 && (pb < 0 || (long long)pb >= p.num_blocks))
         report(kTileStatusBadBlock);  // the copy's bounds check reads it as zeros
       return pb;
     };
-    // blocks of the tiles V, V + 1 .. that are still to be copied
-    int b_v[4] = {block_of(0), block_of(1), block_of(2), block_of(3)};
     bool ok = true;
-    int it = 0, slot = 0;
+    int slot = first, end = first;  // end: one stride past the last item copied
     uint32_t phase = 0;
-    auto copy = [&](const CUtensorMap* map, int pb) {
+    int pb = block_of(first);
+    for (int it = first; it < 2 * n; it += T::kProducers) {
+      const int pb_next = block_of(it + T::kProducers);
+      bool is_v;
+      tile_of(it, is_v);
       ok = ok && mbar_wait(&empty[slot], phase ^ 1u);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
+      if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], T::kSlotBytes);
       __syncwarp();
       if (lane < boxes)  // a block id of -1 is out of the map's bounds: zeros
-        tma_load_4d(smem + slot_off(slot) + half_col * (BN * 128) + page * p.BS * 128, map,
-                    &full[slot], 0, g * p.BS, half_col, pb < 0 ? -1 : pb, policy);
-      ++it;
-      if (++slot == slots) {
-        slot = 0;
+        tma_load_4d(smem + slot_off(slot) + half_col * (BN * 128) + page * p.BS * 128,
+                    is_v ? &tm_v : &tm_k, &full[slot], 0, g * p.BS, half_col, pb < 0 ? -1 : pb,
+                    policy);
+      slot += T::kProducers;
+      if (slot >= slots) {
+        slot -= slots;
         phase ^= 1u;
       }
-    };
-    for (int j = 0; j < min(n, ahead + 1); ++j) copy(&tm_k, j == 0 ? b_v[0] : j == 1 ? b_v[1] : b_v[2]);
-    for (int j = 0; j < n; ++j) {
-      const int b_after = block_of(j + 4);
-      copy(&tm_v, b_v[0]);
-      if (j + 1 + ahead < n) copy(&tm_k, ahead == 1 ? b_v[2] : b_v[3]);
-      b_v[0] = b_v[1];
-      b_v[1] = b_v[2];
-      b_v[2] = b_v[3];
-      b_v[3] = b_after;
+      pb = pb_next;
+      end = it + T::kProducers;
     }
     if (!ok && lane == 0) report(kTileStatusTimeout);
-    // no copy may be in flight when the CTA exits
-    for (int i = max(0, it - slots); i < it; ++i)
-      if (!mbar_wait(&full[i % slots], (uint32_t)((i / slots) & 1)) && lane == 0)
+    // no copy may be in flight when the CTA exits: this warp's last ones
+    for (int it = end - T::kProducers; it >= first && it > end - T::kProducers - slots;
+         it -= T::kProducers)
+      if (!mbar_wait(&full[it % slots], (uint32_t)((it / slots) & 1)) && lane == 0)
         report(kTileStatusTimeout);
   } else if (warp == kMmaWarp) {
     // ==================================================================== products
     // The warp walks the steps together, with warp-uniform operands, and one lane
     // issues: the products take their operands from uniform registers.
     {
-      const bool lead = elect_one();
-      const int n_steps = __shfl_sync(0xffffffffu, steps, 0);
-      const bool two = __shfl_sync(0xffffffffu, (int)both, 0) != 0;
-      const int n_tiles = __shfl_sync(0xffffffffu, n, 0);
-      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      // (a reduction's result is uniform to the compiler)
+      const uint32_t lead = elect_one();
+      const bool two = __reduce_max_sync(0xffffffffu, (uint32_t)both) != 0;  // two row tiles
+      const int n_tiles = (int)__reduce_max_sync(0xffffffffu, (uint32_t)n);
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
       constexpr uint32_t kDescS = instr_desc(128, BN, false), kDescO = instr_desc(128, D, true);
       bool ok = mbar_wait(q_full, 0);
       const uint32_t q_desc = desc_lo(smem_addr(smem), 16);
       const uint32_t v_lead = ((uint32_t)(BN * 128 - 16) >> 4) << 16;  // K-major to MN-major lead
-      // The items in order: the next K and the next V tile's slot and phase.
-      int k_tile = 0, v_tile = 0;  // tiles waited for
-      auto place = [&](int item, int& slot, uint32_t& phase) {
-        slot = item % slots;
-        phase = (uint32_t)(item / slots) & 1u;
+      // The next K tile's and the next V tile's place in the ring: both advance
+      // through the items in order.
+      int k_slot = 0, v_slot = 0, item = 0;
+      uint32_t phase = 0;
+      // A wait's round trip is long in this kernel (200 to 600 cycles: barrier
+      // operations queue behind the exponentials of the other warps), so each is
+      // looked at as soon as the one before it has been used, and waited for only
+      // where that look came too early.
+      bool seen = mbar_test_wait(&full[0], 0u);
+      auto next_item = [&]() -> int {  // waits for the next item, returns its slot
+        if (!__all_sync(0xffffffffu, seen)) ok = ok && mbar_wait(&full[item], phase);
+        const int slot = item;
+        if (++item == slots) {
+          item = 0;
+          phase ^= 1u;
+        }
+        seen = mbar_test_wait(&full[item], phase);
+        return slot;
       };
-      int k_slot = 0, v_slot = 0;
-      auto next_k = [&]() {
-        uint32_t ph;
-        place(item_k(k_tile++), k_slot, ph);
-        ok = ok && mbar_wait(&full[k_slot], ph);
-      };
-      auto next_v = [&]() {
-        uint32_t ph;
-        place(item_v(v_tile++), v_slot, ph);
-        ok = ok && mbar_wait(&full[v_slot], ph);
-      };
-      auto scores = [&](int k) {  // S[k & 1] = Q K^T
-        if (!two || !(k & 1)) next_k();
-        if (T::kApart && k >= 2)  // step k - 2's scores are in registers
-          ok = ok && mbar_wait(&s_free[k & 1], (uint32_t)((k >> 1) - 1) & 1u);
+      // Step i of team t on token tile j.
+      auto scores = [&](int t, int i, int j) {  // S[t][i & 1] = Q K_j^T
+        if (!two || t == 0) k_slot = next_item();
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t qd = q_desc + (two && (k & 1) ? T::kQTileBytes >> 4 : 0);
+        const uint32_t qd = q_desc + (two && t == 1 ? T::kQTileBytes >> 4 : 0);
         const uint32_t kd = q_desc + (slot_off(k_slot) >> 4);
-        if (lead) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(tm + (k & 1) * BN, qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
-                   kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), kDescS, kk > 0);
-          mma_commit(&s_full[k & 1]);
-          if (!two || (k & 1)) mma_commit(&empty[k_slot]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(lead, tm + (2 * t + (i & 1)) * BN,
+                 qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
+                 kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), kDescS, kk > 0);
+        mma_commit(lead, &s_full[2 * t + (i & 1)]);
+        if (!two || t == 1) mma_commit(lead, &empty[k_slot]);
       };
-      auto values = [&](int k) {  // O = O + P V
-        if (!two || !(k & 1)) next_v();
-        ok = ok && mbar_wait(&p_full[k & 1], (uint32_t)((k >> 1) & 1));
+      auto values = [&](int t, int i, int j) {  // O[t] = O[t] + P[t][i & 1] V_j
+        if (!two || t == 0) v_slot = next_item();
+        ok = ok && mbar_wait(&p_full[2 * t + (i & 1)], (uint32_t)(i >> 1) & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
-        const int o = kTeams == 2 ? (k & 1) : 0;
-        const bool first = kTeams == 2 ? k < 2 : k == 0;
         const uint32_t vd = q_desc + v_lead + (slot_off(v_slot) >> 4);
-        if (lead) {
 #pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk) {
-            mma_ts(tm + T::kOCol + o * D,
-                   tm + (T::kApart ? T::kPCol + (k & 1) * (BN / 2) : (k & 1) * BN) + kk * 8,
-                   vd + (kk * 2048 >> 4), kDescO, !first || kk > 0);
-          }
-          // (two teams over their scores need only their last product's completion)
-          if (kTeams == 1 || T::kApart || k + 2 >= n_steps) mma_commit(&o_done[k & 1]);
-          if (!two || (k & 1)) mma_commit(&empty[v_slot]);
-        }
-        __syncwarp();
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(lead, tm + T::kOCol + t * D, tm + (2 * t + (i & 1)) * BN + kk * 8,
+                 vd + (kk * 2048 >> 4), kDescO, i > 0 || kk > 0);
+        mma_commit(lead, &o_done[2 * t + (i & 1)]);
+        if (!two || t == 1) mma_commit(lead, &empty[v_slot]);
       };
-      scores(0);
-      if (n_steps > 1) scores(1);
-      for (int k = 0; k < n_steps; ++k) {
-        if (T::kApart && k + 2 < n_steps) scores(k + 2);
-        values(k);
-        if (!T::kApart && k + 2 < n_steps) scores(k + 2);
+      // Two steps of scores ahead, each buffer's next scores behind the product that
+      // reads the weights over its last ones (products run in the order of issue).
+      // Every item is waited for in the ring's order: with two row tiles the second
+      // team's turn uses the tiles of the first's.
+      const int steps_of = two || kTeams == 1 ? 1 : 2;  // token tiles of one round
+      for (int i = 0; i < 2; ++i)
+        for (int t = 0; t < kTeams; ++t) {
+          const int j = steps_of * i + (steps_of == 2 ? t : 0);
+          if (j < n_tiles) scores(t, i, j);
+        }
+      for (int i = 0; steps_of * i < n_tiles; ++i) {
+        for (int t = 0; t < kTeams; ++t) {
+          const int j = steps_of * i + (steps_of == 2 ? t : 0);
+          if (j >= n_tiles) break;
+          values(t, i, j);
+          if (j + 2 * steps_of < n_tiles) scores(t, i + 2, j + 2 * steps_of);
+        }
       }
-      if (lead) mma_commit(drain);
+      mma_commit(lead, drain);
       if (!mbar_wait(drain, 0)) ok = false;
       if (!ok && lead) report(kTileStatusTimeout);
     }
@@ -470,7 +476,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_addr =
         tmem + lane_base + T::kOCol + (kTeams == 2 ? team * D : 0) + half * (D / 2);
-    float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * 256;
+    float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * 512;
     const uint32_t pair_bar = 1 + team * 4 + (warp & 3);  // the two warps of 32 rows
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
@@ -483,11 +489,12 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     CapSeries cap = {};
     if constexpr (MOD == kTileCapped) cap = cap_series(p.cap_in, p.cap_log2);
     const int last_seen = max(max_hi, pre - 1);
-    for (int k = team; k < steps; k += kTeams) {
-      const int buf = k & 1, j = tile_of_step(k), t0 = token_of(j);
+    const int my_steps = stride == 2 ? (n + 1 - team) / 2 : n;
+    for (int i = 0; i < my_steps; ++i) {
+      const int buf = 2 * team + (i & 1), j = stride == 2 ? 2 * i + team : i, t0 = token_of(j);
       const int c0 = t0 + half * kCols;  // token of this thread's first column
       const uint32_t s_addr = tmem + lane_base + buf * BN;
-      ok = ok && warp_wait(&s_full[buf], (uint32_t)((k >> 1) & 1));
+      ok = ok && warp_wait(&s_full[buf], (uint32_t)(i >> 1) & 1u);
       if (ok) tc_fence_after();
       float x[kCols];  // this thread's scores (a timeout leaves what is there: the walk goes
                        // on without waiting, so that the row's threads stay together)
@@ -496,54 +503,49 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       if constexpr (MOD == kTileGeneral) {
         if (p.cap_log2 > 0.f) {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) x[i] = cap_score(x[i], p.cap_in, p.cap_log2);
+          for (int c = 0; c < kCols; ++c) x[c] = cap_score(x[c], p.cap_in, p.cap_log2);
         } else {
 #pragma unroll
-          for (int i = 0; i < kCols; ++i) x[i] *= p.scale_log2;
+          for (int c = 0; c < kCols; ++c) x[c] *= p.scale_log2;
         }
         const float d0 = (float)(pos - c0);
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) x[i] = fmaf(-slope, fabsf(d0 - (float)i), x[i]);
+        for (int c = 0; c < kCols; ++c) x[c] = fmaf(-slope, fabsf(d0 - (float)c), x[c]);
       }
-      // ---- unseen tokens: a bit per column, from the interval ends
+      // ---- Unseen tokens: a bit per column, from the interval ends.  Their scores
+      // become -inf; capped ones only for the maximum, as the polynomial wants the
+      // others finite, and their exponents later.
       const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
       const bool ragged = !__all_sync(0xffffffffu, whole);
-      if (ragged) {
+      const uint32_t seen = (bits_from(lo - c0) & ~bits_from(hi + 1LL - c0)) | ~bits_from(pre - c0);
+      if (MOD != kTileCapped && ragged) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          const uint32_t bits = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
-                                ~bits_from(pre - c0 - c);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(bits >> i & 1u)) x[c + i] = -INFINITY;
-        }
+        for (int c = 0; c < kCols; ++c)
+          if (!(seen >> c & 1u)) x[c] = -INFINITY;
       }
       // ---- running maximum, raised only past kTileLazyMax.  Scaling by a positive
       // factor and the cap keep the order: there only the maximum is transformed.
       float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+      if (MOD == kTileCapped && ragged) {
 #pragma unroll
-      for (int i = 0; i < kCols; i += 8) {
-        mx0 = max3(mx0, x[i], x[i + 1]);
-        mx1 = max3(mx1, x[i + 2], x[i + 3]);
-        mx2 = max3(mx2, x[i + 4], x[i + 5]);
-        mx3 = max3(mx3, x[i + 6], x[i + 7]);
+        for (int c = 0; c < kCols; ++c) mx0 = seen >> c & 1u ? fmaxf(mx0, x[c]) : mx0;
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 8) {
+          mx0 = max3(mx0, x[c], x[c + 1]);
+          mx1 = max3(mx1, x[c + 2], x[c + 3]);
+          mx2 = max3(mx2, x[c + 4], x[c + 5]);
+          mx3 = max3(mx3, x[c + 6], x[c + 7]);
+        }
       }
-      const float own = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-      float mx = own;
-      // the other half's; where the packed weights overwrite the scores, its thread
-      // has read them by then
-      float* exchange = sm_max + (kTeams == 1 ? (k & 1) * 256 : 0);
+      float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+      // the other half's; its thread has read its scores by then, so the packed
+      // weights may overwrite them.  (Two buffers in turn: a thread writes one again
+      // only after its pair's barrier of the step between.)
+      float* exchange = sm_max + (i & 1) * 256;
       exchange[half * 128 + r128] = mx;
       named_barrier(pair_bar, 64);
       mx = fmaxf(mx, exchange[(half ^ 1) * 128 + r128]);
-      if constexpr (T::kApart) {
-        // The score buffer may take its next scores, and the exchange its next maxima:
-        // they come from those scores.  (One team's two buffers alternate; a thread
-        // writes one again only after its pair's barrier of the step between.)
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[buf]);
-      }
       if constexpr (MOD == kTilePlain) mx *= p.scale_log2;  // (-inf stays: the factor is positive)
       if constexpr (MOD == kTileCapped)
         mx = mx == -INFINITY ? mx : cap_score(mx, p.cap_in, p.cap_log2);
@@ -554,79 +556,67 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         l *= alpha;
       }
       const float sub = m == -INFINITY ? 0.f : m;  // a row that has seen nothing: weights 0
-      // ---- The weights' place is free, and O may be rescaled, once the product of
-      // this team's step before is done.  Over the scores that is so as these exist
-      // (they were issued after it), except for one team's, whose O the step between
-      // works on.
-      if (T::kApart && k >= kTeams) ok = ok && warp_wait(&o_done[buf], (uint32_t)((k >> 1) - 1) & 1u);
-      // ---- weights 2^(x - m), 16 packed columns at a time
+      // ---- weights 2^(x - m), packed
       float2 sum = make_float2(0.f, 0.f);
       const float2 sub2 = make_float2(-sub, -sub);
-      auto emit = [&](auto&& exponent) {
+      uint32_t w[kCols / 2];
+      auto weigh = [&](auto&& exponent) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 e = exponent(make_float2(x[c + 2 * i], x[c + 2 * i + 1]));
-            e.x = fast_exp2(e.x);
-            e.y = fast_exp2(e.y);
-            sum = add2(sum, e);
-            w[i] = pack_bf16x2(e.x, e.y);
+        for (int c = 0; c < kCols / 2; ++c) {
+          float2 e = exponent(make_float2(x[2 * c], x[2 * c + 1]));
+          if (MOD == kTileCapped && ragged) {
+            if (!(seen >> (2 * c) & 1u)) e.x = -INFINITY;
+            if (!(seen >> (2 * c + 1) & 1u)) e.y = -INFINITY;
           }
-          tmem_st((T::kApart ? tmem + lane_base + T::kPCol + buf * (BN / 2) : s_addr) +
-                      half * (kCols / 2) + c / 2,
-                  w);
+          e.x = fast_exp2(e.x);
+          e.y = fast_exp2(e.y);
+          sum = add2(sum, e);
+          w[c] = pack_bf16x2(e.x, e.y);
         }
       };
       if constexpr (MOD == kTileCapped) {
-        float n0 = 0.f, n1 = 0.f;
-        if (!ragged) {
+        float big0 = 0.f, big1 = 0.f;
 #pragma unroll
-          for (int i = 0; i < kCols; i += 4) {
-            n0 = min3(n0, x[i], x[i + 1]);
-            n1 = min3(n1, x[i + 2], x[i + 3]);
-          }
+        for (int c = 0; c < kCols; c += 4) {
+          big0 = max3(big0, fabsf(x[c]), fabsf(x[c + 1]));
+          big1 = max3(big1, fabsf(x[c + 2]), fabsf(x[c + 3]));
         }
-        // (a NaN is not carried by the extremes; the series keeps it.  A ragged tile's
-        // -inf scores take the other way.)
-        if (!ragged && __all_sync(0xffffffffu, fmaxf(own, -fminf(n0, n1)) < cap.reach)) {
+        // (a NaN is not carried by the maximum; the polynomial keeps it)
+        if (__all_sync(0xffffffffu, fmaxf(big0, big1) < cap.reach)) {
           const float2 a0 = make_float2(cap.a0, cap.a0), a1 = make_float2(cap.a1, cap.a1);
           const float2 a2 = make_float2(cap.a2, cap.a2);
-          emit([&](float2 s) {
+          weigh([&](float2 s) {
             const float2 z = mul2(s, s);
             return fma2(s, fma2(z, fma2(z, a2, a1), a0), sub2);
           });
         } else {
-          emit([&](float2 s) {
-            const float a = cap_score(s.x, p.cap_in, p.cap_log2);
-            const float b = cap_score(s.y, p.cap_in, p.cap_log2);
-            return make_float2((s.x == -INFINITY ? s.x : a) - sub,
-                               (s.y == -INFINITY ? s.y : b) - sub);
+          weigh([&](float2 s) {
+            return make_float2(cap_score(s.x, p.cap_in, p.cap_log2) - sub,
+                               cap_score(s.y, p.cap_in, p.cap_log2) - sub);
           });
         }
       } else {
         const float f = MOD == kTilePlain ? p.scale_log2 : 1.f;
-        emit([&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
+        weigh([&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
       }
+      tmem_st(s_addr + half * (kCols / 2), w);
       l += sum.x + sum.y;
       tmem_st_wait();
-      // ---- O of the step before, rescaled where the maximum rose (each thread its
-      // half of the columns)
-      if (k >= kTeams && __any_sync(0xffffffffu, alpha != 1.f)) {
-        if constexpr (kTeams == 1)
-          ok = ok && warp_wait(&o_done[(k - 1) & 1], (uint32_t)((k - 1) >> 1) & 1u);
-          tc_fence_after();
+      // ---- O, rescaled where the maximum rose, once the step before is in it (each
+      // thread its half of the columns)
+      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        ok = ok && warp_wait(&o_done[2 * team + ((i - 1) & 1)], (uint32_t)((i - 1) >> 1) & 1u);
+        tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            float o[32];
-            tmem_ld_begin(o_addr + c, o);
-            tmem_ld_end(o);
+        for (int c = 0; c < D / 2; c += 32) {
+          float o[32];
+          tmem_ld_begin(o_addr + c, o);
+          tmem_ld_end(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st(o_addr + c, o);
-          }
-          tmem_st_wait();
+          for (int e = 0; e < 32; ++e) o[e] *= alpha;
+          tmem_st(o_addr + c, o);
+        }
+        tmem_st_wait();
       }
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
@@ -646,11 +636,11 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&p_full[buf]);
     }
-    // ---- the last product of this team
-    if (team < steps) {
-      const int last = kTeams == 2 ? (steps - 1 - team) / 2 * 2 + team : steps - 1;  // its step
-      ok = ok && warp_wait(&o_done[last & 1],
-                           kTeams == 1 || T::kApart ? (uint32_t)(last >> 1) & 1u : 0u);
+    // ---- the last product of this team (the one before it has completed: the last
+    // scores were issued behind it)
+    if (my_steps > 0) {
+      const int last = my_steps - 1;
+      ok = ok && warp_wait(&o_done[2 * team + (last & 1)], (uint32_t)(last >> 1) & 1u);
     }
     if (!ok && lane == 0) report(kTileStatusTimeout);
     tc_fence_after();
@@ -664,7 +654,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     }
     // ---- one row tile: the second team hands its state over through the ring (idle
     // once both have seen their last product), [D][128] floats, then (m, l)
-    const bool merge = kTeams == 2 && !both && steps > 1;
+    const bool merge = stride == 2 && n > 1;
     float* sm_o = reinterpret_cast<float*>(sm_kv) + half * (D / 2) * 128;
     float2* sm_ml = reinterpret_cast<float2*>(sm_kv + D * 128 * 4);
     float f_own = 1.f, f_other = 0.f;
