@@ -14,7 +14,7 @@ namespace pagedattn {
 // (whose accumulators fill the tensor memory).
 constexpr int tile_rows(int D) { return D == 256 ? 128 : 256; }
 // Tokens of one K/V tile.
-constexpr int kTileTokens = 64;
+constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
 
 struct TileParams {
   const __nv_bfloat16* q;       // [total_q, H_q, D]

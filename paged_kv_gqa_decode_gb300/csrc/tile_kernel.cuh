@@ -50,29 +50,36 @@ template <int D>
 struct TileShape {
   static constexpr int kTeams = D == 256 ? 1 : 2;         // softmax teams of 256 threads
   static constexpr int kRows = tile_rows(D);
-  static constexpr int BN = kTileTokens;
+  static constexpr int BN = tile_tokens(D);
+  // Score buffers of a team.  With two, the scores of its next tile are there when
+  // it has finished one; but tensor memory then leaves two teams only 64 columns a
+  // buffer, and the products' own warp, which takes some hundred cycles of latency a
+  // step among busy ones, sets the pace (four capped prompt chunks: 704 us, against
+  // CHUNKUS with one buffer of 128).
+  static constexpr int kBufs = D == 256 ? 2 : 1;
   static constexpr int kCols = BN / 2;                    // score columns of a thread
   static constexpr int kHalves = D / 64;                  // 128-byte column halves of a row
   static constexpr int kQTileBytes = 128 * D * 2;         // one 128-row query tile
   static constexpr int kSlotBytes = BN * D * 2;           // one K or V tile
-  static constexpr int kSlots = D == 64 ? 15 : D == 128 ? 9 : 5;
-  // The product warp and the producers, then the teams' warps.  A warp's tensor
+  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 4 : 5;
+  // The teams' warps, then the producers and the product warp.  A warp's tensor
   // copies are issued one after the other, about 54 cycles each and 214 for a group,
   // whatever their size (measured on 2, 4 and 8 KB boxes), and warps side by side:
-  // one producer brings 2 KB boxes at 18 to 30 bytes a cycle, three at 50 to 70.
+  // one producer brings 2 KB boxes at 18 to 30 bytes a cycle, two at 35, four at 70.
   // Slot s of the ring belongs to producer s % kProducers, which so waits for its
   // phases strictly in order (a parity wait cannot tell phase k from k - 2).
-  static constexpr int kProducers = D == 256 ? 5 : 3;
+  static constexpr int kProducers = D == 256 ? 5 : 2;
   static_assert(kSlots % kProducers == 0, "a slot belongs to one producer");
   static constexpr int kThreads = kTeams * 256 + 32 + kProducers * 32;
-  // tensor memory: two score buffers for each team, then the accumulators
+  // tensor memory: the teams' score buffers, then the accumulators
   static constexpr int kOCol = 256;
+  static_assert(kTeams * kBufs * BN <= kOCol, "score buffers");
   // shared memory: query tiles, the K/V ring, barriers (384 bytes) and scalars, the
-  // row maxima the two threads of a row exchange, [team][2][half][row]
+  // row maxima the two threads of a row exchange, [team][kBufs][half][row]
   static constexpr int kRingOff = kTeams * kQTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
-  static constexpr int kSmem = kMaxOff + kTeams * 2 * 2 * 128 * 4;
+  static constexpr int kSmem = kMaxOff + kTeams * kBufs * 2 * 128 * 4;
   static_assert(kSmem <= 227 * 1024 && (2 * kSlots + 14) * 8 <= 384, "shared memory of a block");
 };
 
@@ -231,15 +238,14 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   const bool both = kTeams == 2 && n_rows > 128;  // a row tile per warpgroup
 
   // ---- this thread's row (softmax threads) and the tokens it sees
-  // The first warp issues products, the next ones copies.  Row r of
-  // a tile belongs to the warps with warp % 4 = r / 32, whose part of the tensor
-  // memory that is.
-  constexpr int kMmaWarp = 0, kTeamWarp = 1 + T::kProducers;  // (threads are whole teams)
-  const int team = (warp - kTeamWarp) >> 3;        // -1: the other roles
-  const int half = ((warp - kTeamWarp) >> 2) & 1;  // which columns of the row
+  // Row r of a tile belongs to the warps with warp % 4 = r / 32, whose part of the
+  // tensor memory that is.
+  constexpr int kTeamWarps = T::kTeams * 8, kMmaWarp = kTeamWarps + T::kProducers;
+  const int team = warp >> 3;              // kTeams and up: the other roles
+  const int half = (warp >> 2) & 1;        // which columns of the row
   const int r128 = (warp & 3) * 32 + lane;
   const int rr = row0 + (both ? team * 128 : 0) + r128;
-  const bool softmax_thread = warp >= kTeamWarp;
+  const bool softmax_thread = warp < kTeamWarps;
   const int qi = rr / G;
   const bool valid = softmax_thread && (long long)rr < (long long)q_len * G && rr < row0 + kRows;
   long long q_row = -1;                    // row of q / out viewed as rows of D
@@ -323,20 +329,21 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   // teams on one row tile) every other one.
   const int stride = kTeams == 2 && !both ? 2 : 1;  // token tiles from step to step
   // Items of the ring, in the order the products first use them: the K tiles of
-  // every team's first two steps, then a V tile and the K tile `ahead` + 1 further on.
-  const int ahead = 2 * stride - 1;
+  // every team's first kBufs steps, then a V tile and the K tile `ahead` + 1 further on.
+  const int ahead = T::kBufs * stride - 1;
   auto item_k = [&](int j) { return j + max(0, j - ahead); };
   auto item_v = [&](int j) { return j + min(n, j + 1 + ahead); };
-  constexpr int slots = T::kSlots;
+  constexpr int slots = T::kSlots, kBufs = T::kBufs;
+  auto buf_of = [&](int t, int i) -> int { return kBufs * t + (kBufs == 2 ? i & 1 : 0); };
   auto slot_off = [&](int slot) -> int { return T::kRingOff + slot * T::kSlotBytes; };
 
-  if (warp > kMmaWarp && warp < kTeamWarp) {
+  if (warp >= kTeamWarps && warp < kMmaWarp) {
     // =================================================================== producer
     const uint64_t policy = l2_evict_first_policy();
     const int pages = BN / p.BS, boxes = pages * kHalves;  // at most 16 boxes: one per lane
     const int page = lane % pages, half_col = lane / pages;
     // This warp's items are first, first + kProducers, ...; the K or V tile of each:
-    const int first = warp - 1, lead = min(n, ahead + 1), mixed = 2 * (n - lead);
+    const int first = warp - kTeamWarps, lead = min(n, ahead + 1), mixed = 2 * (n - lead);
     auto tile_of = [&](int it, bool& is_v) -> int {
       const int u = it - lead;
       is_v = u >= 0 && (u >= mixed || !(u & 1));
@@ -417,6 +424,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         seen = mbar_test_wait(&full[item], phase);
         return slot;
       };
+      const int steps_of = two || kTeams == 1 ? 1 : 2;  // token tiles of one round
       // Step i of team t on token tile j.
       auto scores = [&](int t, int i, int j) {  // S[t][i & 1] = Q K_j^T
         if (!two || t == 0) k_slot = next_item();
@@ -427,32 +435,33 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         const uint32_t kd = q_desc + (slot_off(k_slot) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(lead, tm + (2 * t + (i & 1)) * BN,
+          mma_ss(lead, tm + buf_of(t, i) * BN,
                  qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
                  kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), kDescS, kk > 0);
-        mma_commit(lead, &s_full[2 * t + (i & 1)]);
+        mma_commit(lead, &s_full[buf_of(t, i)]);
         if (!two || t == 1) mma_commit(lead, &empty[k_slot]);
       };
       auto values = [&](int t, int i, int j) {  // O[t] = O[t] + P[t][i & 1] V_j
         if (!two || t == 0) v_slot = next_item();
-        ok = ok && mbar_wait(&p_full[2 * t + (i & 1)], (uint32_t)(i >> 1) & 1u);
+        ok = ok && mbar_wait(&p_full[buf_of(t, i)], (uint32_t)(i / kBufs) & 1u);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) return;
         tc_fence_after();
         const uint32_t vd = q_desc + v_lead + (slot_off(v_slot) >> 4);
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(lead, tm + T::kOCol + t * D, tm + (2 * t + (i & 1)) * BN + kk * 8,
+          mma_ts(lead, tm + T::kOCol + t * D, tm + buf_of(t, i) * BN + kk * 8,
                  vd + (kk * 2048 >> 4), kDescO, i > 0 || kk > 0);
-        mma_commit(lead, &o_done[2 * t + (i & 1)]);
+        // (with one buffer only the last product's completion is waited for: a step's
+        // scores are issued behind the product before)
+        if (kBufs == 2 || j + steps_of >= n_tiles) mma_commit(lead, &o_done[buf_of(t, i)]);
         if (!two || t == 1) mma_commit(lead, &empty[v_slot]);
       };
-      // Two steps of scores ahead, each buffer's next scores behind the product that
+      // kBufs steps of scores ahead, each buffer's next scores behind the product that
       // reads the weights over its last ones (products run in the order of issue).
       // Every item is waited for in the ring's order: with two row tiles the second
       // team's turn uses the tiles of the first's.
-      const int steps_of = two || kTeams == 1 ? 1 : 2;  // token tiles of one round
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < kBufs; ++i)
         for (int t = 0; t < kTeams; ++t) {
           const int j = steps_of * i + (steps_of == 2 ? t : 0);
           if (j < n_tiles) scores(t, i, j);
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
           const int j = steps_of * i + (steps_of == 2 ? t : 0);
           if (j >= n_tiles) break;
           values(t, i, j);
-          if (j + 2 * steps_of < n_tiles) scores(t, i + 2, j + 2 * steps_of);
+          if (j + kBufs * steps_of < n_tiles) scores(t, i + kBufs, j + kBufs * steps_of);
         }
       }
       mma_commit(lead, drain);
@@ -476,7 +485,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_addr =
         tmem + lane_base + T::kOCol + (kTeams == 2 ? team * D : 0) + half * (D / 2);
-    float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * 512;
+    float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * kBufs * 256;
     const uint32_t pair_bar = 1 + team * 4 + (warp & 3);  // the two warps of 32 rows
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
@@ -491,10 +500,10 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     const int last_seen = max(max_hi, pre - 1);
     const int my_steps = stride == 2 ? (n + 1 - team) / 2 : n;
     for (int i = 0; i < my_steps; ++i) {
-      const int buf = 2 * team + (i & 1), j = stride == 2 ? 2 * i + team : i, t0 = token_of(j);
+      const int buf = buf_of(team, i), j = stride == 2 ? 2 * i + team : i, t0 = token_of(j);
       const int c0 = t0 + half * kCols;  // token of this thread's first column
       const uint32_t s_addr = tmem + lane_base + buf * BN;
-      ok = ok && warp_wait(&s_full[buf], (uint32_t)(i >> 1) & 1u);
+      ok = ok && warp_wait(&s_full[buf], (uint32_t)(i / kBufs) & 1u);
       if (ok) tc_fence_after();
       float x[kCols];  // this thread's scores (a timeout leaves what is there: the walk goes
                        // on without waiting, so that the row's threads stay together)
@@ -517,18 +526,23 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       // others finite, and their exponents later.
       const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
       const bool ragged = !__all_sync(0xffffffffu, whole);
-      const uint32_t seen = (bits_from(lo - c0) & ~bits_from(hi + 1LL - c0)) | ~bits_from(pre - c0);
+      uint32_t seen[kCols / 32];
+#pragma unroll
+      for (int c = 0; c < kCols; c += 32)
+        seen[c / 32] = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
+                       ~bits_from(pre - c0 - c);
+      auto sees = [&](int c) { return (seen[c / 32] >> (c & 31) & 1u) != 0; };
       if (MOD != kTileCapped && ragged) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          if (!(seen >> c & 1u)) x[c] = -INFINITY;
+          if (!sees(c)) x[c] = -INFINITY;
       }
       // ---- running maximum, raised only past kTileLazyMax.  Scaling by a positive
       // factor and the cap keep the order: there only the maximum is transformed.
       float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
       if (MOD == kTileCapped && ragged) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) mx0 = seen >> c & 1u ? fmaxf(mx0, x[c]) : mx0;
+        for (int c = 0; c < kCols; ++c) mx0 = sees(c) ? fmaxf(mx0, x[c]) : mx0;
       } else {
 #pragma unroll
         for (int c = 0; c < kCols; c += 8) {
@@ -540,9 +554,11 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       }
       float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
       // the other half's; its thread has read its scores by then, so the packed
-      // weights may overwrite them.  (Two buffers in turn: a thread writes one again
-      // only after its pair's barrier of the step between.)
-      float* exchange = sm_max + (i & 1) * 256;
+      // weights may overwrite them.  (With one score buffer a thread comes here again
+      // only when all have finished this step; with two, the buffers of the exchange
+      // take turns, and a thread writes one again only after its pair's barrier of
+      // the step between.)
+      float* exchange = sm_max + (buf - buf_of(team, 0)) * 256;
       exchange[half * 128 + r128] = mx;
       named_barrier(pair_bar, 64);
       mx = fmaxf(mx, exchange[(half ^ 1) * 128 + r128]);
@@ -559,19 +575,23 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       // ---- weights 2^(x - m), packed
       float2 sum = make_float2(0.f, 0.f);
       const float2 sub2 = make_float2(-sub, -sub);
-      uint32_t w[kCols / 2];
       auto weigh = [&](auto&& exponent) {
 #pragma unroll
-        for (int c = 0; c < kCols / 2; ++c) {
-          float2 e = exponent(make_float2(x[2 * c], x[2 * c + 1]));
-          if (MOD == kTileCapped && ragged) {
-            if (!(seen >> (2 * c) & 1u)) e.x = -INFINITY;
-            if (!(seen >> (2 * c + 1) & 1u)) e.y = -INFINITY;
+        for (int c = 0; c < kCols; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e2 = 0; e2 < 16; ++e2) {
+            float2 e = exponent(make_float2(x[c + 2 * e2], x[c + 2 * e2 + 1]));
+            if (MOD == kTileCapped && ragged) {
+              if (!sees(c + 2 * e2)) e.x = -INFINITY;
+              if (!sees(c + 2 * e2 + 1)) e.y = -INFINITY;
+            }
+            e.x = fast_exp2(e.x);
+            e.y = fast_exp2(e.y);
+            sum = add2(sum, e);
+            w[e2] = pack_bf16x2(e.x, e.y);
           }
-          e.x = fast_exp2(e.x);
-          e.y = fast_exp2(e.y);
-          sum = add2(sum, e);
-          w[c] = pack_bf16x2(e.x, e.y);
+          tmem_st(s_addr + half * (kCols / 2) + c / 2, w);
         }
       };
       if constexpr (MOD == kTileCapped) {
@@ -599,13 +619,13 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         const float f = MOD == kTilePlain ? p.scale_log2 : 1.f;
         weigh([&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
       }
-      tmem_st(s_addr + half * (kCols / 2), w);
       l += sum.x + sum.y;
       tmem_st_wait();
       // ---- O, rescaled where the maximum rose, once the step before is in it (each
       // thread its half of the columns)
       if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        ok = ok && warp_wait(&o_done[2 * team + ((i - 1) & 1)], (uint32_t)((i - 1) >> 1) & 1u);
+        if constexpr (kBufs == 2)
+          ok = ok && warp_wait(&o_done[buf_of(team, i - 1)], (uint32_t)((i - 1) >> 1) & 1u);
         tc_fence_after();
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 32) {
@@ -640,7 +660,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     // scores were issued behind it)
     if (my_steps > 0) {
       const int last = my_steps - 1;
-      ok = ok && warp_wait(&o_done[2 * team + (last & 1)], (uint32_t)(last >> 1) & 1u);
+      ok = ok && warp_wait(&o_done[buf_of(team, last)],
+                           kBufs == 2 ? (uint32_t)(last >> 1) & 1u : 0u);
     }
     if (!ok && lane == 0) report(kTileStatusTimeout);
     tc_fence_after();
