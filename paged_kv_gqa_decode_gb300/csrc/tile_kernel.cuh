@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   uint64_t* drain = q_full + 1;
   int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 384);
   // sm_i: [0] TMEM address, [1] sequence, [2] row tile, [3] min lo, [4] max hi,
+  // [5] max lo, [6] min hi,
   // [8..32) warp sums of the tile search
   uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(sm_i);
 
@@ -191,6 +192,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       sm_i[1] = -1;
       sm_i[3] = 0x7fffffff;
       sm_i[4] = -1;
+      sm_i[5] = 0;
+      sm_i[6] = 0x7fffffff;
       for (int i = 0; i < T::kSlots; ++i) {
         mbar_init(&full[i], 1);
         mbar_init(&empty[i], 1);
@@ -267,6 +270,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       atomicMin(&sm_i[3], lo);
       atomicMax(&sm_i[4], hi);
     }
+    atomicMax(&sm_i[5], lo);
+    atomicMin(&sm_i[6], hi);
   }
   // ---- the query rows, swizzled for the products (128-byte rows, 16-byte chunk c
   // of row r at c ^ (r % 8)); the threads of a row (four with one row tile for two
@@ -288,6 +293,8 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   }
   __syncthreads();
   const int min_lo = sm_i[3], max_hi = sm_i[4];
+  // tiles beginning in [clean_lo, clean_hi] are seen whole by every row
+  const int clean_lo = sm_i[5], clean_hi = sm_i[6] - (BN - 1);
 
   // ---- the walk over token tiles: those of the prefix, then those from the first
   // to the last one an interval touches
@@ -415,7 +422,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       // where that look came too early.
       bool seen = mbar_test_wait(&full[0], 0u);
       auto next_item = [&]() -> int {  // waits for the next item, returns its slot
-        if (!__all_sync(0xffffffffu, seen)) ok = ok && mbar_wait(&full[item], phase);
+        if (!seen && ok) ok = mbar_wait(&full[item], phase);
         const int slot = item;
         if (++item == slots) {
           item = 0;
@@ -428,9 +435,6 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       // Step i of team t on token tile j.
       auto scores = [&](int t, int i, int j) {  // S[t][i & 1] = Q K_j^T
         if (!two || t == 0) k_slot = next_item();
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
-        tc_fence_after();
         const uint32_t qd = q_desc + (two && t == 1 ? T::kQTileBytes >> 4 : 0);
         const uint32_t kd = q_desc + (slot_off(k_slot) >> 4);
 #pragma unroll
@@ -443,9 +447,9 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       };
       auto values = [&](int t, int i, int j) {  // O[t] = O[t] + P[t][i & 1] V_j
         if (!two || t == 0) v_slot = next_item();
-        ok = ok && mbar_wait(&p_full[buf_of(t, i)], (uint32_t)(i / kBufs) & 1u);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+        // (after a timeout the walk goes on without waiting: what it then multiplies is
+        // in bounds, and the call has reported)
+        if (ok) ok = mbar_wait(&p_full[buf_of(t, i)], (uint32_t)(i / kBufs) & 1u);
         tc_fence_after();
         const uint32_t vd = q_desc + v_lead + (slot_off(v_slot) >> 4);
 #pragma unroll
@@ -524,13 +528,16 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       // ---- Unseen tokens: a bit per column, from the interval ends.  Their scores
       // become -inf; capped ones only for the maximum, as the polynomial wants the
       // others finite, and their exponents later.
-      const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
-      const bool ragged = !__all_sync(0xffffffffu, whole);
+      bool ragged = false;
       uint32_t seen[kCols / 32];
+      if (t0 < clean_lo || t0 > clean_hi) {
+        const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
+        ragged = !__all_sync(0xffffffffu, whole);
 #pragma unroll
-      for (int c = 0; c < kCols; c += 32)
-        seen[c / 32] = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
-                       ~bits_from(pre - c0 - c);
+        for (int c = 0; c < kCols; c += 32)
+          seen[c / 32] = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
+                         ~bits_from(pre - c0 - c);
+      }
       auto sees = [&](int c) { return (seen[c / 32] >> (c & 31) & 1u) != 0; };
       if (MOD != kTileCapped && ragged) {
 #pragma unroll
@@ -640,7 +647,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       }
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
-      if ((!both || team == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
+      if ((t0 < clean_lo || t0 > clean_hi) && (!both || team == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
         const int item = item_v(j);
         ok = ok && warp_wait(&full[item % slots], (uint32_t)((item / slots) & 1));
         uint8_t* v = smem + slot_off(item % slots);
