@@ -767,13 +767,28 @@ int decode_mods_impl(Operands& o, int head_dim, int block_size, bool fp8, void* 
 // Row-tile attention (multi-token decode with score options, shared prefixes).
 constexpr int kMaxSplits = 32;  // the merge gives one lane to each part
 
-// Parts of each piece's token range: as many as fill the SMs once when the
-// pieces do not.  The part count bounds what the kernel uses (it never makes
-// parts of fewer than two tiles).
+// Row tiles a launch provides for (an upper bound that needs no device value).
+long long tile_bound(int D, int total_q, int num_seqs, int G) {
+  const long long rows = (long long)total_q * G;
+  return rows / (128 * tile_teams(D, rows, num_seqs)) + num_seqs;
+}
+
+// Parts of each piece's token range: one when the pieces fill the places there are
+// for CTAs (two on an SM for the one-team kernels of head_dim 64 and 128), else as many as
+// make 1.75 CTAs a place, so that the longest parts end near the others (fewer
+// leave SMs idle behind a long sequence, more pay each CTA's 4 us of start and end:
+// verification of five tokens, 272 pieces, 1 / 2 / 3 / 6 parts 100 / 81 / 78 / 87 us;
+// 64 chats over three prompts, 40 pieces, 4 / 8 / 12 / 24 parts 64 / 58 / 56 / 69 us).
+// The part count bounds what the kernel uses (it never makes parts of fewer than
+// two tiles).
 int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms) {
-  const long long tiles = (long long)total_q * (H_q / H_kv) / tile_rows(D) + num_seqs;
-  const long long s = sms / (tiles * H_kv);
-  return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
+  const int G = H_q / H_kv;
+  const bool pairs = D < 256 && tile_teams(D, (long long)total_q * G, num_seqs) == 1;
+  const long long places = (pairs ? 2 : 1) * (long long)sms;
+  const long long pieces = tile_bound(D, total_q, num_seqs, G) * H_kv;
+  if (pieces >= places) return 1;
+  const long long s = (7 * places / 4 + pieces / 2) / pieces;
+  return s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
 // Workspace of the partial states: (m, l) of every part and row, then their o.
@@ -784,8 +799,8 @@ size_t tile_part_bytes(int D, int total_q, int H_q, int splits) {
 
 // Validates what the row-tile kernel's index arithmetic needs.
 bool tile_sizes_ok(int total_q, int num_seqs, int H_q, int H_kv, int D) {
-  const long long tiles = (long long)total_q * (H_q / H_kv) / tile_rows(D) + num_seqs;
-  return (long long)total_q * (H_q / H_kv) < 0x7ffffff0LL && tiles * H_kv < 0x7fffffffLL &&
+  return (long long)total_q * (H_q / H_kv) < 0x7ffffff0LL &&
+         tile_bound(D, total_q, num_seqs, H_q / H_kv) * H_kv < 0x7fffffffLL &&
          (long long)total_q * H_q * D < (1LL << 40);
 }
 
@@ -818,7 +833,7 @@ int launch_merge_parts(const MergeParams& p, cudaStream_t st) {
 }
 
 // The parameters common to both uses.
-TileParams tile_params(const void* q, void* out, const int32_t* bt, const int32_t* lens,
+TileParams tile_params(int D, const void* q, void* out, const int32_t* bt, const int32_t* lens,
                        const int32_t* qo, int num_seqs, int total_q, int H_q, int H_kv, int maxb,
                        int BS, float scale, float softcap, const float* slopes) {
   TileParams t = {};
@@ -832,6 +847,7 @@ TileParams tile_params(const void* q, void* out, const int32_t* bt, const int32_
   t.H_q = H_q;
   t.H_kv = H_kv;
   t.G = H_q / H_kv;
+  t.teams = tile_teams(D, (long long)total_q * t.G, num_seqs);
   t.maxb = maxb;
   t.BS = BS;
   t.scale_log2 = scale * 1.4426950408889634f;
@@ -1274,7 +1290,7 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   DeviceInfo di;
   if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  TileParams t = tile_params(q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
+  TileParams t = tile_params(head_dim, q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
                              H_kv, max_blocks_per_seq, block_size, scale, softcap, alibi_slopes);
   t.causal = is_causal ? 1 : 0;
   t.window = window;
@@ -1386,7 +1402,7 @@ int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_c
   if (rc != PAGED_ATTN_OK) return rc;
   apply_checks(&o);
   uint8_t* base = static_cast<uint8_t*>(o.ws);
-  TileParams t = tile_params(q, out, prefix_tables, prefix_lens, group_indptr, num_groups,
+  TileParams t = tile_params(head_dim, q, out, prefix_tables, prefix_lens, group_indptr, num_groups,
                              num_seqs, H_q, H_kv, prefix_max_blocks, block_size, scale, softcap,
                              alibi_slopes);
   t.tail_lens = seq_lens;

@@ -10,11 +10,13 @@
 
 namespace pagedattn {
 
-// Query rows of one CTA: two tiles of 128 for head_dim 64 and 128, one for 256
-// (whose accumulators fill the tensor memory).
-constexpr int tile_rows(int D) { return D == 256 ? 128 : 256; }
-// Tokens of one K/V tile.
-constexpr int tile_tokens(int D) { return D == 256 ? 64 : 128; }
+// Softmax teams of a CTA, each with a tile of 128 query rows.  Two for head_dim 64
+// and 128, where a sequence has more than 128 rows for a KV head on average; else
+// one, in CTAs of which two run on an SM (64, 128), as their starts and ends then
+// overlap; one for 256, whose accumulators take half the tensor memory.
+constexpr int tile_teams(int D, long long total_rows, long long num_seqs) {
+  return D < 256 && total_rows > 128 * num_seqs ? 2 : 1;
+}
 
 struct TileParams {
   const __nv_bfloat16* q;       // [total_q, H_q, D]
@@ -33,6 +35,7 @@ struct TileParams {
   // (the prefix's) last one (null: the rows are the sequence's last tokens).
   const int32_t* tail_lens;     // [total_q] or null
   int tail_cap;                 // largest value tail_lens is clamped to
+  int teams;                    // tile_teams: picks the kernel
   int splits;                   // parts of each piece's token range
   int single;                   // 1: splits is 1 and the kernel writes the output itself
   float* part_o;                // [splits][total_q * H_q][D]

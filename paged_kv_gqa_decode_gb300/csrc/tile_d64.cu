@@ -1,11 +1,12 @@
-// Row-tile attention kernel for head_dim = 64.
+// Row-tile attention kernels for head_dim = 64.
 #include "tile_kernel.cuh"
 
 namespace pagedattn {
 
 cudaError_t launch_tile_d64(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                             cudaStream_t stream) {
-  return launch_tile<64>(tk, tv, p, stream);
+  if (p.teams == 2) return launch_tile<64, 2>(tk, tv, p, stream);
+  return launch_tile<64, 1>(tk, tv, p, stream);
 }
 
 }  // namespace pagedattn

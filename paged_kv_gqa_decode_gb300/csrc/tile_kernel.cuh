@@ -44,24 +44,24 @@ namespace pagedattn {
 constexpr int kTileStatusBadBlock = 1, kTileStatusBadLength = 2, kTileStatusTimeout = 4,
               kTileStatusConfig = 8;
 constexpr float kTileLazyMax = 8.f;
-constexpr int kTileTmemColumns = 512;
 
-template <int D>
+template <int D, int TEAMS>
 struct TileShape {
-  static constexpr int kTeams = D == 256 ? 1 : 2;         // softmax teams of 256 threads
-  static constexpr int kRows = tile_rows(D);
-  static constexpr int BN = tile_tokens(D);
-  // Score buffers of a team.  With two, the scores of its next tile are there when
-  // it has finished one; but tensor memory then leaves two teams only 64 columns a
-  // buffer, and the products' own warp, which takes some hundred cycles of latency a
-  // step among busy ones, sets the pace (four capped prompt chunks: 704 us, against
-  // CHUNKUS with one buffer of 128).
-  static constexpr int kBufs = D == 256 ? 2 : 1;
+  static constexpr int kTeams = TEAMS;                    // softmax teams of 256 threads
+  static constexpr int kRows = 128 * TEAMS;
+  // Tokens of one K/V tile, and the score buffers of a team.  With two buffers the
+  // scores of its next tile are there when it has finished one; but tensor memory
+  // then leaves two teams only 64 columns a buffer, and the products' own warp,
+  // which takes some hundred cycles of latency a step among busy ones, sets the pace
+  // (four capped prompt chunks: 704 us, against 548 with one buffer of 128).
+  static constexpr int BN = TEAMS == 2 ? 128 : 64;
+  static constexpr int kBufs = TEAMS == 2 ? 1 : 2;
+  static constexpr int kCtas = TEAMS == 1 && D < 256 ? 2 : 1;  // CTAs on an SM
   static constexpr int kCols = BN / 2;                    // score columns of a thread
   static constexpr int kHalves = D / 64;                  // 128-byte column halves of a row
   static constexpr int kQTileBytes = 128 * D * 2;         // one 128-row query tile
   static constexpr int kSlotBytes = BN * D * 2;           // one K or V tile
-  static constexpr int kSlots = D == 64 ? 8 : D == 128 ? 4 : 5;
+  static constexpr int kSlots = D == 256 ? 5 : D == 64 ? 8 : 4;
   // The teams' warps, then the producers and the product warp.  A warp's tensor
   // copies are issued one after the other, about 54 cycles each and 214 for a group,
   // whatever their size (measured on 2, 4 and 8 KB boxes), and warps side by side:
@@ -72,15 +72,17 @@ struct TileShape {
   static_assert(kSlots % kProducers == 0, "a slot belongs to one producer");
   static constexpr int kThreads = kTeams * 256 + 32 + kProducers * 32;
   // tensor memory: the teams' score buffers, then the accumulators
-  static constexpr int kOCol = 256;
-  static_assert(kTeams * kBufs * BN <= kOCol, "score buffers");
+  static constexpr int kOCol = kTeams * kBufs * BN;
+  static constexpr int kTmemColumns = kCtas == 2 ? 256 : 512;
+  static_assert(kOCol + kTeams * D <= kTmemColumns, "tensor memory");
   // shared memory: query tiles, the K/V ring, barriers (384 bytes) and scalars, the
   // row maxima the two threads of a row exchange, [team][kBufs][half][row]
   static constexpr int kRingOff = kTeams * kQTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
   static constexpr int kSmem = kMaxOff + kTeams * kBufs * 2 * 128 * 4;
-  static_assert(kSmem <= 227 * 1024 && (2 * kSlots + 14) * 8 <= 384, "shared memory of a block");
+  static_assert((kSmem + 1024) * kCtas <= 228 * 1024 && (2 * kSlots + 14) * 8 <= 384,
+                "shared memory");
 };
 
 // What the scores need, compiled apart so that each loop over a row holds only its
@@ -121,11 +123,11 @@ __device__ __forceinline__ float cap_score(float s, float c, float cap_log2) {
   return cap_log2 * (fabsf(y) < kTanhSeries ? tanh_series(y) : tanh_exp(y));
 }
 
-template <int D, int MOD>
-__global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
+template <int D, int TEAMS, int MOD>
+__global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TEAMS>::kCtas)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TileParams p) {
-  using T = TileShape<D>;
+  using T = TileShape<D, TEAMS>;
   constexpr int kTeams = T::kTeams, kRows = T::kRows, BN = T::BN, kHalves = T::kHalves;
   constexpr int kThreads = T::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];  // (no room for an alignment slack)
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     return;
   }
 
-  if (warp == kMmaWarp) tmem_alloc(sm_tmem, kTileTmemColumns);
+  if (warp == kMmaWarp) tmem_alloc(sm_tmem, T::kTmemColumns);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -502,6 +504,9 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
     CapSeries cap = {};
     if constexpr (MOD == kTileCapped) cap = cap_series(p.cap_in, p.cap_log2);
     const int last_seen = max(max_hi, pre - 1);
+    // A warp none of whose rows is the piece's only keeps step: what is then in its
+    // rows of the weights reaches its rows of O alone, which nobody stores.
+    const bool idle = !__any_sync(0xffffffffu, valid);
     const int my_steps = stride == 2 ? (n + 1 - team) / 2 : n;
     for (int i = 0; i < my_steps; ++i) {
       const int buf = buf_of(team, i), j = stride == 2 ? 2 * i + team : i, t0 = token_of(j);
@@ -509,6 +514,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
       const uint32_t s_addr = tmem + lane_base + buf * BN;
       ok = ok && warp_wait(&s_full[buf], (uint32_t)(i / kBufs) & 1u);
       if (ok) tc_fence_after();
+      if (!idle) {
       float x[kCols];  // this thread's scores (a timeout leaves what is there: the walk goes
                        // on without waiting, so that the row's threads stay together)
       tmem_ld_begin(s_addr + half * kCols, x);
@@ -645,6 +651,7 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
         }
         tmem_st_wait();
       }
+      }
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
       if ((t0 < clean_lo || t0 > clean_hi) && (!both || team == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
@@ -749,16 +756,16 @@ __global__ void __launch_bounds__(TileShape<D>::kThreads, 1)
   __syncthreads();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTileTmemColumns);
+    tmem_dealloc(tmem, T::kTmemColumns);
   }
 }
 
-template <int D, int MOD>
+template <int D, int TEAMS, int MOD>
 cudaError_t launch_tile_as(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                            cudaStream_t stream) {
-  using T = TileShape<D>;
+  using T = TileShape<D, TEAMS>;
   static std::atomic<bool> limit_raised[64];
-  auto kernel = paged_tile_kernel<D, MOD>;
+  auto kernel = paged_tile_kernel<D, TEAMS, MOD>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -783,13 +790,13 @@ cudaError_t launch_tile_as(const CUtensorMap& tk, const CUtensorMap& tv, const T
   return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
 }
 
-template <int D>
+template <int D, int TEAMS>
 cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                         cudaStream_t stream) {
   if (p.slopes != nullptr || !(p.scale_log2 > 0.f))
-    return launch_tile_as<D, kTileGeneral>(tk, tv, p, stream);
-  return p.cap_log2 > 0.f ? launch_tile_as<D, kTileCapped>(tk, tv, p, stream)
-                          : launch_tile_as<D, kTilePlain>(tk, tv, p, stream);
+    return launch_tile_as<D, TEAMS, kTileGeneral>(tk, tv, p, stream);
+  return p.cap_log2 > 0.f ? launch_tile_as<D, TEAMS, kTileCapped>(tk, tv, p, stream)
+                          : launch_tile_as<D, TEAMS, kTilePlain>(tk, tv, p, stream);
 }
 
 }  // namespace pagedattn
