@@ -543,7 +543,7 @@ PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int to
  *
  * Everything else as paged_attn_decode; rows past a prefix's or a sequence's end
  * may hold anything.  A sequence without any token gets zero rows.  Three
- * launches: the prefixes, the own tokens, the merge.  num_groups = 0 is
+ * launches: the prefixes and, side by side with them, the own tokens, then the merge.  num_groups = 0 is
  * paged_attn_decode_mods.  workspace: as there,
  * paged_attn_shared_workspace_bytes(...) bytes.
  */

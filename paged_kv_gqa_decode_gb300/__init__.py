@@ -519,66 +519,80 @@ def paged_attn_append_decode_fp8(q, k_new, v_new, k8, v8, k_scale, v_scale, bloc
     return out
 
 
-def _same_device(tensors) -> None:
-    """CUDA tensors must lie on the current device (whose stream the call uses);
-    a host tensor must be pinned."""
+def _same_device(*tensors) -> int:
+    """CUDA tensors must lie on the current device (whose stream the call uses); a host
+    tensor must be pinned.  Returns the current device."""
     import torch
 
-    current = -1
+    current = torch.cuda.current_device() if tensors[0].is_cuda else -1
     for t in tensors:
         if t is None:
             continue
         if t.is_cuda:
-            if current < 0:
-                current = torch.cuda.current_device()
             if t.get_device() != current:
-                raise ValueError("every tensor must be on the current CUDA device")
+                if current >= 0:
+                    raise ValueError("every tensor must be on the current CUDA device")
+                current = torch.cuda.current_device()
+                if t.get_device() != current:
+                    raise ValueError("every tensor must be on the current CUDA device")
         elif not t.is_pinned():
             raise ValueError("host tensors must be pinned")
+    return current
 
 
 def _need(name, t, dtype, shape) -> None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
-def _mods_problem(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
-                  doc_starts, workspace, cache_dtype, rows=None):
-    """Checks the tensors of a decode call with score options; returns the sizes and out."""
+def _raw_stream(stream, device) -> int:
+    """The stream's handle: the one given, or the device's current one."""
+    if stream is not None:
+        return int(stream.cuda_stream)
     import torch
 
-    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2 or seq_lens.dim() != 1:
+    return torch.cuda.current_stream(device if device >= 0 else None).cuda_stream
+
+
+def _mods_problem(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
+                  doc_starts, workspace, cache_dtype, rows=None):
+    """Checks the tensors of a decode call with score options; returns the sizes, out and
+    the device."""
+    import torch
+
+    i32 = torch.int32
+    qs, ks, bs, ls = q.shape, k_cache.shape, block_tables.shape, seq_lens.shape
+    if len(qs) != 3 or len(ks) != 4 or len(bs) != 2 or len(ls) != 1:
         raise ValueError("q must be [rows, H_q, D], the caches [num_blocks, H_kv, block_size, D], "
                          "block_tables [num_seqs, max_blocks] and seq_lens [num_seqs]")
-    n, H_q, D = q.shape
-    nb, H_kv, BS, Dk = k_cache.shape
-    num_seqs = seq_lens.shape[0]
-    if Dk != D:
+    n, H_q, D = qs
+    num_seqs = ls[0]
+    maxb = bs[1]
+    if ks[3] != D:
         raise ValueError("q and the caches disagree on head_dim")
     if rows is None and n != num_seqs:
         raise ValueError("q must have one row per sequence")
-    maxb = block_tables.shape[1]
-    _need("q", q, torch.bfloat16, (n, H_q, D))
-    _need("k_cache", k_cache, cache_dtype, (nb, H_kv, BS, D))
-    _need("v_cache", v_cache, cache_dtype, (nb, H_kv, BS, D))
-    _need("block_tables", block_tables, torch.int32, (num_seqs, maxb))
-    _need("seq_lens", seq_lens, torch.int32, (num_seqs,))
+    _need("q", q, torch.bfloat16, qs)
+    _need("k_cache", k_cache, cache_dtype, ks)
+    _need("v_cache", v_cache, cache_dtype, ks)
+    _need("block_tables", block_tables, i32, (num_seqs, maxb))
+    _need("seq_lens", seq_lens, i32, ls)
     if alibi_slopes is not None:
         _need("alibi_slopes", alibi_slopes, torch.float32, (H_q,))
     if prefix_lens is not None:
-        _need("prefix_lens", prefix_lens, torch.int32, (num_seqs,))
+        _need("prefix_lens", prefix_lens, i32, ls)
     if doc_starts is not None:
-        _need("doc_starts", doc_starts, torch.int32, (n,))
+        _need("doc_starts", doc_starts, i32, (n,))
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need("out", out, torch.bfloat16, (n, H_q, D))
-    _same_device((q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
-                  doc_starts, workspace))
-    return n, num_seqs, H_q, H_kv, D, maxb, BS, out
+        _need("out", out, torch.bfloat16, qs)
+    device = _same_device(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes,
+                          prefix_lens, doc_starts, workspace)
+    return n, num_seqs, H_q, ks[1], D, maxb, ks[2], out, device
 
 
 def _bytes(t) -> int:
@@ -597,14 +611,14 @@ def paged_attn_decode_mods(q, k_cache, v_cache, block_tables, seq_lens, scale: f
     needed while a stream is being captured."""
     import torch
 
-    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+    _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
         workspace, torch.bfloat16)
-    _check(load().paged_attn_decode_mods(
+    _check((_lib or load()).paged_attn_decode_mods(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
         float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens), _ptr(doc_starts),
-        _ptr(workspace), _bytes(workspace), _stream(stream)))
+        _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
     return out
 
 
@@ -615,17 +629,17 @@ def paged_attn_decode_fp8_mods(q, k8, v8, k_scale, v_scale, block_tables, seq_le
     """paged_attn_decode_mods over FP8 caches (as paged_attn_decode_fp8; head_dim 128 or 256)."""
     import torch
 
-    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+    _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k8, v8, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts, workspace,
         torch.uint8)
     _need("k_scale", k_scale, torch.float32, k8.shape[:3])
     _need("v_scale", v_scale, torch.float32, k8.shape[:3])
-    _same_device((k_scale, v_scale))
-    _check(load().paged_attn_decode_fp8_mods(
+    _same_device(k_scale, v_scale)
+    _check((_lib or load()).paged_attn_decode_fp8_mods(
         q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS,
         float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
-        _ptr(doc_starts), _ptr(workspace), _bytes(workspace), _stream(stream)))
+        _ptr(doc_starts), _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
     return out
 
 
@@ -645,17 +659,17 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     [total_q], one per query row; the other options as paged_attn_decode_mods."""
     import torch
 
-    total_q, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+    total_q, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
         workspace, torch.bfloat16, rows="many")
     _need("qo_indptr", qo_indptr, torch.int32, (n + 1,))
-    _same_device((qo_indptr,))
-    _check(load().paged_attn_decode_multi_mods(
+    _same_device(qo_indptr)
+    _check((_lib or load()).paged_attn_decode_multi_mods(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         qo_indptr.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, total_q, H_q, H_kv,
         D, maxb, BS, float(scale), 1 if causal else 0, float(softcap), _ptr(alibi_slopes),
         int(window), _ptr(prefix_lens), _ptr(doc_starts), _ptr(workspace), _bytes(workspace),
-        _stream(stream)))
+        _raw_stream(stream, dev)))
     return out
 
 
@@ -676,7 +690,7 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
     seq_lens are those of the sequences' own tokens."""
     import torch
 
-    _, n, H_q, H_kv, D, maxb, BS, out = _mods_problem(
+    _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, None, None, workspace,
         torch.bfloat16)
     if prefix_tables.dim() != 2:
@@ -685,12 +699,12 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
     _need("prefix_tables", prefix_tables, torch.int32, (groups, pmax))
     _need("prefix_lens", prefix_lens, torch.int32, (groups,))
     _need("group_indptr", group_indptr, torch.int32, (groups + 1,))
-    _same_device((prefix_tables, prefix_lens, group_indptr))
-    _check(load().paged_attn_decode_shared(
+    _same_device(prefix_tables, prefix_lens, group_indptr)
+    _check((_lib or load()).paged_attn_decode_shared(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         group_indptr.data_ptr(), prefix_tables.data_ptr(), prefix_lens.data_ptr(), groups, pmax,
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
-        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace), _stream(stream)))
+        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
     return out
 
 
@@ -723,17 +737,17 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
     _need("block_tables", block_tables, i32, (n, block_tables.shape[1]))
     _need("free_blocks", free_blocks, i32, (free_blocks.numel(),))
     _need("free_count", free_count, i32, (1,))
-    dev = seq_lens.device
+    where = seq_lens.device
     if seq_lens_out is None:
         seq_lens_out = torch.empty_like(seq_lens)
     else:
         _need("seq_lens_out", seq_lens_out, i32, (n,))
     if qo_indptr is None:
-        qo_indptr = torch.empty(n + 1, dtype=i32, device=dev)
+        qo_indptr = torch.empty(n + 1, dtype=i32, device=where)
     else:
         _need("qo_indptr", qo_indptr, i32, (n + 1,))
     if slot_map is None:
-        slot_map = torch.empty(max_new, dtype=torch.int64, device=dev)
+        slot_map = torch.empty(max_new, dtype=torch.int64, device=where)
     else:
         _need("slot_map", slot_map, torch.int64, (max_new,))
     if free_count_out is None:
@@ -742,14 +756,14 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
         _need("free_count_out", free_count_out, i32, (1,))
     if refused is not None:
         _need("refused", refused, i32, (1,))
-    _same_device((seq_lens, new_lens, block_tables, free_blocks, free_count, seq_lens_out,
-                  qo_indptr, slot_map, free_count_out, refused))
-    _check(load().paged_kv_assign(
+    dev = _same_device(seq_lens, new_lens, block_tables, free_blocks, free_count, seq_lens_out,
+                       qo_indptr, slot_map, free_count_out, refused)
+    _check((_lib or load()).paged_kv_assign(
         seq_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
         free_blocks.data_ptr(), free_count.data_ptr(), seq_lens_out.data_ptr(),
         qo_indptr.data_ptr(), slot_map.data_ptr(), free_count_out.data_ptr(), _ptr(refused), n,
         block_tables.shape[1], int(block_size), free_blocks.numel(), int(max_new),
-        _stream(stream)))
+        _raw_stream(stream, dev)))
     return seq_lens_out, qo_indptr, slot_map, free_count_out
 
 
@@ -766,16 +780,16 @@ def paged_kv_append_slots(k_new, v_new, k_cache, v_cache, slot_map, stream=None)
     nb, H_kv, BS, D = k_cache.shape
     rows = k_new.shape[0]
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (rows, H_kv, D):
+        if t.dtype is not torch.bfloat16 or t.shape != (rows, H_kv, D):
             raise ValueError(f"{name} must be bfloat16 [rows, H_kv, head_dim]")
         if rows and (t.stride(2) != 1 or (H_kv > 1 and t.stride(1) != D)):
             raise ValueError(f"the rows of {name} must be contiguous [H_kv, head_dim]")
     _need("k_cache", k_cache, torch.bfloat16, (nb, H_kv, BS, D))
     _need("v_cache", v_cache, torch.bfloat16, (nb, H_kv, BS, D))
     _need("slot_map", slot_map, torch.int64, (rows,))
-    _same_device((k_new, v_new, k_cache, v_cache, slot_map))
+    dev = _same_device(k_new, v_new, k_cache, v_cache, slot_map)
     row = H_kv * D
-    _check(load().paged_kv_append_slots(
+    _check((_lib or load()).paged_kv_append_slots(
         k_new.data_ptr(), v_new.data_ptr(), k_new.stride(0) if rows > 1 else row,
         v_new.stride(0) if rows > 1 else row, k_cache.data_ptr(), v_cache.data_ptr(),
-        slot_map.data_ptr(), rows, H_kv, D, BS, nb, _stream(stream)))
+        slot_map.data_ptr(), rows, H_kv, D, BS, nb, _raw_stream(stream, dev)))

@@ -12,20 +12,25 @@
 // block * BS + t % BS.
 //
 // What bounds it: eight bytes written per token and the latency of one scan.
-// The whole grid is one thread-block cluster (a single CTA for a decode step,
-// eight for prompts): every CTA scans all the lengths into per-thread sums in
-// shared memory and fills its part of the slot map from them, and the cluster
-// barrier separates those reads from the writes of the new lengths and the
-// free count, so a caller may update both in place and needs no workspace.
+// Every CTA scans all the lengths into per-thread sums in shared memory and fills
+// its part of the slot map from them.  When the new lengths or the free count go
+// over the old ones, all those reads have to come before the writes: the grid is
+// then one thread-block cluster (a single CTA for a decode step, eight for prompts),
+// whose barrier separates them without a workspace; else it is as large as the
+// rows ask for.
 #include "assign.h"
 
 namespace pagedattn {
 namespace {
 
 constexpr int kAssignThreads = 1024;
-constexpr int kAssignMaxCtas = 8;        // a portable cluster
-constexpr int kRowsPerThread = 8;        // consecutive rows (64 bytes of slots) of one search
+constexpr int kClusterCtas = 8;          // a portable cluster
+constexpr int kMaxCtas = 128;
 constexpr int kRowsPerCta = 4096;        // rows from which a further CTA joins
+// Consecutive rows that a thread fills after one search: few while a CTA has
+// threads for all rows (the rows of a thread are filled one after the other), else
+// 64 bytes of slots.
+constexpr int kFewRows = 2, kManyRows = 8;
 constexpr int kStatusBadBlockId = 1, kStatusBadLengthGiven = 2;
 
 // One sequence as the scan sees it.
@@ -54,6 +59,7 @@ __device__ __forceinline__ bool served(const AssignParams& a, const Seq& x, long
          tokens + x.new_len <= a.max_new;
 }
 
+template <int kRowsPerThread, bool CLUSTER>
 __global__ void __launch_bounds__(kAssignThreads) paged_kv_assign_kernel(const AssignParams a) {
   __shared__ long long tok[kAssignThreads + 1], blk[kAssignThreads + 1];
   __shared__ long long warp_tok[32], warp_blk[32];
@@ -179,7 +185,7 @@ __global__ void __launch_bounds__(kAssignThreads) paged_kv_assign_kernel(const A
   }
 
   // ---- 3. every CTA has read the lengths and the free count: they may be overwritten
-  if (gridDim.x > 1) {
+  if constexpr (CLUSTER) {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
                  ::: "memory");
   } else {
@@ -219,12 +225,17 @@ __global__ void __launch_bounds__(kAssignThreads) paged_kv_assign_kernel(const A
 }  // namespace
 
 cudaError_t launch_assign(const AssignParams& a, cudaStream_t stream) {
-  int ctas = 1;  // a power of two up to kAssignMaxCtas, by the rows there may be
-  while (ctas < kAssignMaxCtas && (long long)ctas * kRowsPerCta < a.max_new) ctas *= 2;
+  const bool in_place = a.seq_lens_out == a.seq_lens || a.free_count_out == a.free_count;
+  const int most = in_place ? kClusterCtas : kMaxCtas;
+  int ctas = 1;  // a power of two, by the rows there may be
+  while (ctas < most && (long long)ctas * kRowsPerCta < a.max_new) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kAssignThreads);
   cfg.stream = stream;
+  if (!in_place || ctas == 1)
+    return ctas == 1 ? cudaLaunchKernelEx(&cfg, paged_kv_assign_kernel<kFewRows, false>, a)
+                     : cudaLaunchKernelEx(&cfg, paged_kv_assign_kernel<kManyRows, false>, a);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)ctas;
@@ -232,7 +243,7 @@ cudaError_t launch_assign(const AssignParams& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_kv_assign_kernel, a);
+  return cudaLaunchKernelEx(&cfg, paged_kv_assign_kernel<kManyRows, true>, a);
 }
 
 }  // namespace pagedattn

@@ -185,6 +185,11 @@ struct DecodeParams {
   // MOD: write each row's softmax state [M, L, -, -, o[0..D)] (fp32, M in the log2
   // domain) here instead of the bf16 output (null: off).
   float* state;                // [num_seqs * H_q][D + 4]
+  // MOD: the launch just ahead began its dependents only after the work before it
+  // was complete, and this launch uses nothing of it: its CTAs do not wait.  The
+  // grid then has one CTA more, which waits and does nothing else, so that this
+  // launch completes after the one ahead.
+  int independent;
 #ifdef PAGED_ATTN_WAIT_TEST
   // Test build only: CTA 0 arms the ring slot of its unit `test_skip_unit` but
   // issues no copy into it, so the consumer's bounded wait for that page runs
@@ -414,6 +419,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
   const int lane = tid & 31;
+  int grid_ctas = (int)gridDim.x;  // CTAs that share the work
+  if constexpr (MOD) {
+    if (p.independent) {
+      --grid_ctas;
+      if ((int)blockIdx.x == grid_ctas) {
+        griddep_launch_dependents();
+        griddep_wait();
+        return;
+      }
+    }
+  }
   const int N = p.num_seqs;
   const int H_kv = p.H_kv;
   const int G = p.G;
@@ -481,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (!p.early) griddep_wait();
+  if (!p.early && !(MOD && p.independent)) griddep_wait();
   {
     const size_t bt_bytes = (size_t)N * p.maxb * sizeof(int32_t);
     if (bt_bytes <= kBlockTablePrefetchBytes) {
       const char* bt = reinterpret_cast<const char*>(p.block_tables);
       for (size_t off = ((size_t)blockIdx.x * kThreads + tid) * 128; off < bt_bytes;
-           off += (size_t)gridDim.x * kThreads * 128)
+           off += (size_t)grid_ctas * kThreads * 128)
         prefetch_l2(bt + off);
     }
   }
@@ -601,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   const long long W = (long long)sm_prefix[NW] * H_kv;
   if (W == 0) {  // nothing to stream: every CTA zeroes its share and leaves
     if (p.early) griddep_wait();
-    zero_empty(gridDim.x, tid, kThreads);
+    zero_empty(grid_ctas, tid, kThreads);
     return;
   }
   if (p.stages < kConsumerWarps) {  // the host plan never launches fewer
@@ -609,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     return;
   }
   const long long C =
-      min((long long)gridDim.x, max(1LL, (W + kMinPagesPerCta - 1) / kMinPagesPerCta));
+      min((long long)grid_ctas, max(1LL, (W + kMinPagesPerCta - 1) / kMinPagesPerCta));
   if ((long long)blockIdx.x >= C) return;
   // (with the early prologue the consumers zero them once they have waited)
   if (!p.early) zero_empty(C, tid, kThreads);

@@ -505,6 +505,7 @@ struct Operands {
   int window = 0;
   const int32_t* prefix_lens = nullptr;
   const int32_t* doc_starts = nullptr;
+  bool independent = false;  // needs nothing of the launch just ahead (DecodeParams)
   float* state = nullptr;  // softmax states [num_seqs * H_q][D + 4] instead of the output
 };
 
@@ -569,6 +570,7 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
     p.window = o.window;
     p.prefix_lens = o.prefix_lens ? o.prefix_lens + s0 : nullptr;
     p.doc_starts = o.doc_starts ? o.doc_starts + s0 : nullptr;
+    p.independent = o.independent && s0 == 0 ? 1 : 0;
     p.state = o.state ? o.state + (size_t)s0 * o.H_q * (pl.D + 4) : nullptr;
     p.k_new = o.k_new ? static_cast<const __nv_bfloat16*>(o.k_new) + (size_t)s0 * o.H_kv * pl.D
                       : nullptr;
@@ -583,8 +585,8 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
     p.test_skip_publish = g_test_skip_publish;
 #endif
     cudaError_t e =
-        launch_dim(pl.D, pl.BS, pl.g16, pl.fp8, pl.xp, pl.mod, tk, tv, p, pl.grid, pl.smem,
-                   stream);
+        launch_dim(pl.D, pl.BS, pl.g16, pl.fp8, pl.xp, pl.mod, tk, tv, p,
+                   pl.grid + p.independent, pl.smem, stream);
     if (e != cudaSuccess) return cuda_fail(e);
   }
   return PAGED_ATTN_OK;
@@ -778,16 +780,22 @@ long long tile_bound(int D, int total_q, int num_seqs, int G) {
 // make 1.75 CTAs a place, so that the longest parts end near the others (fewer
 // leave SMs idle behind a long sequence, more pay each CTA's 4 us of start and end:
 // verification of five tokens, 272 pieces, 1 / 2 / 3 / 6 parts 100 / 81 / 78 / 87 us;
-// 64 chats over three prompts, 40 pieces, 4 / 8 / 12 / 24 parts 64 / 58 / 56 / 69 us).
+// 64 chats over three prompts, 40 pieces, one pass after the other, 4 / 8 / 12 / 24
+// parts 64 / 58 / 56 / 69 us).
+// `beside`: another launch runs at the same time (shared prefixes: the sequences'
+// own tokens), for which SMs are left: 1.25 CTAs an SM (the same 40 pieces 4 / 5 / 6 /
+// 12 parts 47.9 / 46.8 / 47.5 / 52.7 us).
 // The part count bounds what the kernel uses (it never makes parts of fewer than
 // two tiles).
-int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms) {
+int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,
+                bool beside = false) {
   const int G = H_q / H_kv;
   const bool pairs = D < 256 && tile_teams(D, (long long)total_q * G, num_seqs) == 1;
   const long long places = (pairs ? 2 : 1) * (long long)sms;
   const long long pieces = tile_bound(D, total_q, num_seqs, G) * H_kv;
-  if (pieces >= places) return 1;
-  const long long s = (7 * places / 4 + pieces / 2) / pieces;
+  if (pieces >= (beside ? sms : places)) return 1;
+  const long long want = beside ? 5LL * sms / 4 : 7 * places / 4;
+  const long long s = (want + pieces / 2) / pieces;
   return s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
@@ -1338,7 +1346,7 @@ int shared_plan(int num_seqs, int num_groups, int H_q, int H_kv, int head_dim, i
   rc = cached_plan(num_seqs, H_q, H_kv, head_dim, block_size, dev, di, &sp->own, false, 0, 0,
                    true);
   if (rc != PAGED_ATTN_OK) return rc;
-  sp->splits = tile_splits(head_dim, num_seqs, num_groups, H_q, H_kv, di.sms);
+  sp->splits = tile_splits(head_dim, num_seqs, num_groups, H_q, H_kv, di.sms, true);
   sp->off_state = round_up(sp->own.ws_bytes, kWsAlign);
   sp->off_parts =
       sp->off_state + round_up((size_t)num_seqs * H_q * (head_dim + 4) * 4, kWsAlign);
@@ -1411,6 +1419,8 @@ int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_c
   t.status = o.status ? o.status : static_cast<int32_t*>(o.ws);
   set_parts(&t, base + sp.off_parts);
   if ((rc = launch_tiles(head_dim, t, k_cache, v_cache, st)) != PAGED_ATTN_OK) return rc;
+  // The two passes over keys need nothing of each other and run side by side.
+  o.independent = true;
   o.state = reinterpret_cast<float*>(base + sp.off_state);
   if ((rc = run(sp.own, o, st)) != PAGED_ATTN_OK) return rc;
   MergeParams m = {};

@@ -151,7 +151,6 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   const int N = p.num_seqs, G = p.G;
   auto report = [&](int bits) { atomicOr(p.status, bits); };
 
-  griddep_launch_dependents();
   if (smem_addr(smem) & 1023) {  // never expected: the swizzle needs 1024-byte tiles
     griddep_wait();
     if (tid == 0) report(kTileStatusConfig);
@@ -162,6 +161,9 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     tma_prefetch_desc(&tm_v);
   }
   griddep_wait();
+  // (after the wait: a dependent launch that needs nothing of this one may then go on
+  // without waiting itself, since the work before both is complete)
+  griddep_launch_dependents();
 
   // ---- which piece: tiles are numbered through the sequences, the last first (a
   // causal batch's longest pieces start first)
