@@ -770,9 +770,8 @@ int decode_mods_impl(Operands& o, int head_dim, int block_size, bool fp8, void* 
 constexpr int kMaxSplits = 32;  // the merge gives one lane to each part
 
 // Row tiles a launch provides for (an upper bound that needs no device value).
-long long tile_bound(int D, int total_q, int num_seqs, int G) {
-  const long long rows = (long long)total_q * G;
-  return rows / (128 * tile_teams(D, rows, num_seqs)) + num_seqs;
+long long tile_bound(int total_q, int num_seqs, int G, int teams) {
+  return (long long)total_q * G / (128 * teams) + num_seqs;
 }
 
 // Parts of each piece's token range: one when the pieces fill the places there are
@@ -789,10 +788,9 @@ long long tile_bound(int D, int total_q, int num_seqs, int G) {
 // two tiles).
 int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,
                 bool beside = false) {
-  const int G = H_q / H_kv;
-  const bool pairs = D < 256 && tile_teams(D, (long long)total_q * G, num_seqs) == 1;
-  const long long places = (pairs ? 2 : 1) * (long long)sms;
-  const long long pieces = tile_bound(D, total_q, num_seqs, G) * H_kv;
+  const int G = H_q / H_kv, teams = tile_teams(D, (long long)total_q * G, num_seqs, H_kv, sms);
+  const long long places = (D < 256 && teams == 1 ? 2 : 1) * (long long)sms;
+  const long long pieces = tile_bound(total_q, num_seqs, G, teams) * H_kv;
   if (pieces >= (beside ? sms : places)) return 1;
   const long long want = beside ? 5LL * sms / 4 : 7 * places / 4;
   const long long s = (want + pieces / 2) / pieces;
@@ -808,7 +806,7 @@ size_t tile_part_bytes(int D, int total_q, int H_q, int splits) {
 // Validates what the row-tile kernel's index arithmetic needs.
 bool tile_sizes_ok(int total_q, int num_seqs, int H_q, int H_kv, int D) {
   return (long long)total_q * (H_q / H_kv) < 0x7ffffff0LL &&
-         tile_bound(D, total_q, num_seqs, H_q / H_kv) * H_kv < 0x7fffffffLL &&
+         tile_bound(total_q, num_seqs, H_q / H_kv, 1) * H_kv < 0x7fffffffLL / kMaxSplits &&
          (long long)total_q * H_q * D < (1LL << 40);
 }
 
@@ -841,7 +839,7 @@ int launch_merge_parts(const MergeParams& p, cudaStream_t st) {
 }
 
 // The parameters common to both uses.
-TileParams tile_params(int D, const void* q, void* out, const int32_t* bt, const int32_t* lens,
+TileParams tile_params(int D, int sms, const void* q, void* out, const int32_t* bt, const int32_t* lens,
                        const int32_t* qo, int num_seqs, int total_q, int H_q, int H_kv, int maxb,
                        int BS, float scale, float softcap, const float* slopes) {
   TileParams t = {};
@@ -855,7 +853,7 @@ TileParams tile_params(int D, const void* q, void* out, const int32_t* bt, const
   t.H_q = H_q;
   t.H_kv = H_kv;
   t.G = H_q / H_kv;
-  t.teams = tile_teams(D, (long long)total_q * t.G, num_seqs);
+  t.teams = tile_teams(D, (long long)total_q * t.G, num_seqs, H_kv, sms);
   t.maxb = maxb;
   t.BS = BS;
   t.scale_log2 = scale * 1.4426950408889634f;
@@ -1298,7 +1296,7 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   DeviceInfo di;
   if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  TileParams t = tile_params(head_dim, q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
+  TileParams t = tile_params(head_dim, di.sms, q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
                              H_kv, max_blocks_per_seq, block_size, scale, softcap, alibi_slopes);
   t.causal = is_causal ? 1 : 0;
   t.window = window;
@@ -1405,12 +1403,14 @@ int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_c
   SharedPlan sp;
   rc = shared_plan(num_seqs, num_groups, H_q, H_kv, head_dim, block_size, &sp);
   if (rc != PAGED_ATTN_OK) return rc;
+  DeviceInfo di;
+  if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   rc = optional_workspace(workspace, workspace_bytes, sp.bytes, st, &o.ws);
   if (rc != PAGED_ATTN_OK) return rc;
   apply_checks(&o);
   uint8_t* base = static_cast<uint8_t*>(o.ws);
-  TileParams t = tile_params(head_dim, q, out, prefix_tables, prefix_lens, group_indptr, num_groups,
+  TileParams t = tile_params(head_dim, di.sms, q, out, prefix_tables, prefix_lens, group_indptr, num_groups,
                              num_seqs, H_q, H_kv, prefix_max_blocks, block_size, scale, softcap,
                              alibi_slopes);
   t.tail_lens = seq_lens;

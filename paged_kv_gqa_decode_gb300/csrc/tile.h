@@ -11,11 +11,16 @@
 namespace pagedattn {
 
 // Softmax teams of a CTA, each with a tile of 128 query rows.  Two for head_dim 64
-// and 128, where a sequence has more than 128 rows for a KV head on average; else
-// one, in CTAs of which two run on an SM (64, 128), as their starts and ends then
-// overlap; one for 256, whose accumulators take half the tensor memory.
-constexpr int tile_teams(int D, long long total_rows, long long num_seqs) {
-  return D < 256 && total_rows > 128 * num_seqs ? 2 : 1;
+// and 128, where a sequence has more than 128 rows for a KV head on average and the
+// pieces of 256 rows fill the SMs (a K/V tile then serves both: four capped prompt
+// chunks 552 us, 594 with one); else one, in CTAs of which two run on an SM (64, 128),
+// as their starts and ends then overlap (chunks of 40 to 64 tokens 57 us, 71 with two);
+// one for 256, whose accumulators take half the tensor memory.
+constexpr int tile_teams(int D, long long total_rows, long long num_seqs, int H_kv, int sms) {
+  return D < 256 && total_rows > 128 * num_seqs &&
+                 (total_rows / 256 + num_seqs) * H_kv >= sms
+             ? 2
+             : 1;
 }
 
 struct TileParams {

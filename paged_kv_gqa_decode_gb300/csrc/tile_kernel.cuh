@@ -522,16 +522,46 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       tmem_ld_begin(s_addr + half * kCols, x);
       tmem_ld_end(x);
       if constexpr (MOD == kTileGeneral) {
+        // the whole transformation here, in place: with a bias the order of the raw
+        // scores says nothing
+        const float d0 = (float)(pos - c0), base = -slope * d0;
+        // -slope |pos - t| is linear over the columns where no token lies past the
+        // query, which is everywhere but on a causal diagonal and beyond
+        const bool behind = __all_sync(0xffffffffu, pos >= c0 + kCols - 1 || slope == 0.f);
         if (p.cap_log2 > 0.f) {
+          float big0 = 0.f, big1 = 0.f;
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c] = cap_score(x[c], p.cap_in, p.cap_log2);
+          for (int c = 0; c < kCols; c += 4) {
+            big0 = max3(big0, fabsf(x[c]), fabsf(x[c + 1]));
+            big1 = max3(big1, fabsf(x[c + 2]), fabsf(x[c + 3]));
+          }
+          const CapSeries cap = cap_series(p.cap_in, p.cap_log2);
+          if (__all_sync(0xffffffffu, fmaxf(big0, big1) < cap.reach)) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) {
+              const float z = x[c] * x[c];
+              x[c] = x[c] * fmaf(z, fmaf(z, cap.a2, cap.a1), cap.a0);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) x[c] = cap_score(x[c], p.cap_in, p.cap_log2);
+          }
+          if (behind) {
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) x[c] += fmaf(slope, (float)c, base);
+          }
+        } else if (behind) {
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            x[c] = fmaf(x[c], p.scale_log2, fmaf(slope, (float)c, base));
         } else {
 #pragma unroll
           for (int c = 0; c < kCols; ++c) x[c] *= p.scale_log2;
         }
-        const float d0 = (float)(pos - c0);
+        if (!behind) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) x[c] = fmaf(-slope, fabsf(d0 - (float)c), x[c]);
+          for (int c = 0; c < kCols; ++c) x[c] = fmaf(-slope, fabsf(d0 - (float)c), x[c]);
+        }
       }
       // ---- Unseen tokens: a bit per column, from the interval ends.  Their scores
       // become -inf; capped ones only for the maximum, as the polynomial wants the
