@@ -44,6 +44,9 @@ namespace pagedattn {
 constexpr int kTileStatusBadBlock = 1, kTileStatusBadLength = 2, kTileStatusTimeout = 4,
               kTileStatusConfig = 8;
 constexpr float kTileLazyMax = 8.f;
+// Batches up to this many sequences start with the longest ones (a loop over all of
+// them in every CTA): verification of five tokens, 512 to 4096 tokens, 71 -> 52 us.
+constexpr int kRankedSeqs = 128;
 
 template <int D, int TEAMS>
 struct TileShape {
@@ -165,12 +168,12 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   // without waiting itself, since the work before both is complete)
   griddep_launch_dependents();
 
-  // ---- which piece: tiles are numbered through the sequences, the last first (a
-  // causal batch's longest pieces start first)
+  // ---- which piece: tiles are numbered through the sequences, those with the most
+  // tokens to walk first where the batch is small enough to rank, and within one
+  // from its last rows (causally the longest walk) to its first
   const int split = (int)(blockIdx.x % p.splits);
   const int g = (int)(blockIdx.x / p.splits % p.H_kv);
-  const int tiles_bound = (int)(gridDim.x / ((unsigned)p.splits * p.H_kv));
-  const int want = tiles_bound - 1 - (int)(blockIdx.x / ((unsigned)p.splits * p.H_kv));
+  const int want = (int)(blockIdx.x / ((unsigned)p.splits * p.H_kv));
   // rows of sequence s, and the first of them (clamped into [0, total_q])
   auto rows_at = [&](int s, int& first) -> int {
     first = min(max(__ldg(p.qo_indptr + s), 0), p.total_q);
@@ -180,7 +183,56 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     int first;
     return (int)(((long long)rows_at(s, first) * G + kRows - 1) / kRows);
   };
-  {
+  if (tid == 0) {
+    sm_i[1] = -1;
+    sm_i[3] = 0x7fffffff;
+    sm_i[4] = -1;
+    sm_i[5] = 0;
+    sm_i[6] = 0x7fffffff;
+    for (int i = 0; i < T::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);  // a team's warps
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(q_full, kTeams * 8);
+    mbar_init(drain, 1);
+    fence_barrier_init();
+  }
+  if (N <= kRankedSeqs) {
+    int2* rank = reinterpret_cast<int2*>(smem);  // (tokens, tiles) of each sequence
+    int tokens = 0, tiles = 0;
+    if (tid < N) {
+      // what the sequence's last row sees, which is near what each of its pieces walks
+      int first;
+      const int rows = rows_at(tid, first), L = __ldg(p.seq_lens + tid);
+      int from = p.window > 0 ? L - p.window : 0;
+      if (p.doc_starts != nullptr && rows > 0)
+        from = max(from, __ldg(p.doc_starts + first + rows - 1));
+      from = min(max(from, 0), max(L, 0));
+      tokens = max(L, 0) - from;
+      if (p.prefix_lens != nullptr) tokens += min(max(__ldg(p.prefix_lens + tid), 0), from);
+      tiles = (int)(((long long)rows * G + kRows - 1) / kRows);
+      rank[tid] = make_int2(tokens, tiles);
+    }
+    __syncthreads();
+    if (tid < N) {
+      int before = 0;
+#pragma unroll 4
+      for (int u = 0; u < N; ++u) {
+        const int2 x = rank[u];
+        if (x.x > tokens || (x.x == tokens && u < tid)) before += x.y;
+      }
+      if (want >= before && want < before + tiles) {
+        sm_i[1] = tid;
+        sm_i[2] = tiles - 1 - (want - before);
+      }
+    }
+    __syncthreads();
+  } else {
     const int per = (N + kThreads - 1) / kThreads;
     const int s0 = min(N, tid * per), s1 = min(N, s0 + per);
     int local = 0;
@@ -192,25 +244,6 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       if (lane >= o) incl += v;
     }
     if (lane == 31) sm_i[8 + warp] = incl;
-    if (tid == 0) {
-      sm_i[1] = -1;
-      sm_i[3] = 0x7fffffff;
-      sm_i[4] = -1;
-      sm_i[5] = 0;
-      sm_i[6] = 0x7fffffff;
-      for (int i = 0; i < T::kSlots; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&empty[i], 1);
-      }
-      for (int i = 0; i < 4; ++i) {
-        mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 8);  // a team's warps
-        mbar_init(&o_done[i], 1);
-      }
-      mbar_init(q_full, kTeams * 8);
-      mbar_init(drain, 1);
-      fence_barrier_init();
-    }
     __syncthreads();
     int before = incl - local;
     for (int w = 0; w < warp; ++w) before += sm_i[8 + w];
@@ -223,7 +256,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         ++s;
       }
       sm_i[1] = s;
-      sm_i[2] = want - before;
+      sm_i[2] = tiles_of(s) - 1 - (want - before);
     }
     __syncthreads();
   }
