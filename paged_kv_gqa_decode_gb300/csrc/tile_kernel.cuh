@@ -346,8 +346,11 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   const int k0 = split < parts ? (int)((long long)split * n_all / parts) : 0;
   const int k1 = split < parts ? (int)((long long)(split + 1) * n_all / parts) : 0;
   const int n = k1 - k0;
-  auto token_of = [&](int j) -> int {  // first token of this part's tile j
-    const int k = k0 + j;
+  // First token of this part's tile j, from its last to its first: under a distance
+  // bias the scores fall that way, so the maximum is found at once and O is not
+  // rescaled at every tile.
+  auto token_of = [&](int j) -> int {
+    const int k = k1 - 1 - j;
     return (k < head_tiles ? k : k + skip) * BN;
   };
   const long long part_rows = (long long)p.total_q * p.H_q;
