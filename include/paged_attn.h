@@ -82,7 +82,7 @@ extern "C" {
 #define PAGED_ATTN_ERR_SCALE (-8)      /* scale is not finite */
 #define PAGED_ATTN_ERR_STATIC_SCRATCH (-9) /* sizes exceed paged_attn_decode_static's scratch */
 #define PAGED_ATTN_ERR_FLAGS (-10)     /* unknown bits in paged_attn_set_launch_flags */
-#define PAGED_ATTN_ERR_MODS (-11)      /* softcap negative or not finite, or window negative */
+#define PAGED_ATTN_ERR_MODS (-11)      /* softcap not 0 and outside [1e-30, 1e30] (or scale / softcap past 1e30), or window < 0 */
 
 /* Launch flags (paged_attn_set_launch_flags). */
 #define PAGED_ATTN_FLAG_EARLY_PROLOGUE 1
@@ -442,7 +442,8 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
  *   doc_starts    [num_seqs]  int32    (read; null: 0) the first token of the
  *                 document the query is in, in a sequence that packs several
  *
- * prefix_lens and doc_starts are clamped to [0, L].  A query that sees no token
+ * softcap is 0 or in [1e-30, 1e30], and max_blocks_per_seq * block_size at most
+ * 2^31 - 256.  prefix_lens and doc_starts are clamped to [0, L].  A query that sees no token
  * gets a zero row.  Pages that hold no token the query sees are not read (their
  * table entries neither), and unseen rows of the pages that are may hold
  * anything, NaN included.  The arrays are 4-byte aligned device (or pinned
@@ -659,7 +660,7 @@ PAGED_ATTN_API const char* paged_attn_status_string(int status);
 PAGED_ATTN_API int paged_attn_set_launch_flags(int flags);
 
 /*
- * Zero-fills the library-owned workspace of the current device on `stream`
+ * Zero-fills the library-owned workspaces of the current device on `stream`
  * (nothing to do when none exists yet).  Needed only after a call reported a
  * combine wait that ran out (status bit 2), which can leave split counters set.
  */

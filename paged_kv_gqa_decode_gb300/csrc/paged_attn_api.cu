@@ -741,9 +741,14 @@ int plan_and_run(Operands& o, int head_dim, int block_size, bool fp8, bool xp, i
 // Score options as the entry points take them (arrays 4-byte aligned or null).
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
 
-int mods_checks(float softcap, const float* slopes, int window, const int32_t* prefix_lens,
-                const int32_t* doc_starts) {
-  if (!std::isfinite(softcap) || softcap < 0.f) return PAGED_ATTN_ERR_MODS;
+int mods_checks(float scale, long long max_tokens, float softcap, const float* slopes,
+                int window, const int32_t* prefix_lens, const int32_t* doc_starts) {
+  // token positions a tile past the last one stay inside int32
+  if (max_tokens > 0x7fffff00LL) return PAGED_ATTN_ERR_SIZES;
+  // (what the score arithmetic needs: scale / softcap and softcap log2(e) far inside float32)
+  if (softcap != 0.f &&
+      !(softcap >= 1e-30f && softcap <= 1e30f && std::fabs(scale / softcap) <= 1e30f))
+    return PAGED_ATTN_ERR_MODS;
   if (window < 0) return PAGED_ATTN_ERR_MODS;
   if (!aligned4(slopes) || !aligned4(prefix_lens) || !aligned4(doc_starts))
     return PAGED_ATTN_ERR_POINTER;
@@ -1222,7 +1227,8 @@ int paged_attn_decode_mods(const void* q, const void* k_cache, const void* v_cac
                            void* stream) {
   int rc = common_checks(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
                          head_dim, max_blocks_per_seq, block_size, scale);
-  if (rc == PAGED_ATTN_OK) rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  if (rc == PAGED_ATTN_OK) rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+                     window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
   Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
                         max_blocks_per_seq, scale);
@@ -1245,7 +1251,8 @@ int paged_attn_decode_fp8_mods(const void* q, const void* k_cache, const void* v
                                void* stream) {
   int rc = fp8_checks(q, k_cache, v_cache, k_scale, v_scale, out, block_tables, seq_lens,
                       num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size, scale);
-  if (rc == PAGED_ATTN_OK) rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  if (rc == PAGED_ATTN_OK) rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+                     window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
   Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
                         max_blocks_per_seq, scale);
@@ -1288,7 +1295,8 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   if (!std::isfinite(scale)) return PAGED_ATTN_ERR_SCALE;
   if (total_q < 0 || !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
     return PAGED_ATTN_ERR_SIZES;
-  rc = mods_checks(softcap, alibi_slopes, window, prefix_lens, doc_starts);
+  rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+                     window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0 || total_q == 0) return rc;
   rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
   if (rc != PAGED_ATTN_OK) return rc;
@@ -1386,7 +1394,10 @@ int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_c
                         prefix_max_blocks, block_size);
   if (rc != PAGED_ATTN_OK) return rc;
   if (!std::isfinite(scale)) return PAGED_ATTN_ERR_SCALE;
-  rc = mods_checks(softcap, alibi_slopes, 0, nullptr, nullptr);
+  const int most_blocks =
+      max_blocks_per_seq > prefix_max_blocks ? max_blocks_per_seq : prefix_max_blocks;
+  rc = mods_checks(scale, (long long)most_blocks * block_size, softcap, alibi_slopes, 0, nullptr,
+                   nullptr);
   if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
   rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
   if (rc != PAGED_ATTN_OK) return rc;
@@ -1633,7 +1644,7 @@ const char* paged_attn_status_string(int status) {
     case PAGED_ATTN_ERR_STATIC_SCRATCH:
       return "sizes need more scratch than paged_attn_decode_static's fixed 4 MiB array";
     case PAGED_ATTN_ERR_FLAGS: return "unknown launch flag bits";
-    case PAGED_ATTN_ERR_MODS: return "softcap must be finite and >= 0, window >= 0";
+    case PAGED_ATTN_ERR_MODS: return "softcap must be 0 or in [1e-30, 1e30], window >= 0";
     default: return "unknown status";
   }
 }
@@ -1663,10 +1674,12 @@ int paged_attn_reset_workspace(void* stream) {
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
   std::lock_guard<std::mutex> lk(g_mu);
-  const OwnedWorkspace& w = g_ws[dev];
-  if (w.ptr == nullptr) return PAGED_ATTN_OK;
-  cudaError_t e = cudaMemsetAsync(w.ptr, 0, w.bytes, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+  for (const OwnedWorkspace* w : {&g_ws[dev], &g_opt_ws[dev]}) {
+    if (w->ptr == nullptr) continue;
+    cudaError_t e = cudaMemsetAsync(w->ptr, 0, w->bytes, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  return PAGED_ATTN_OK;
 }
 
 int paged_attn_last_cuda_error(void) { return g_last_cuda_error; }

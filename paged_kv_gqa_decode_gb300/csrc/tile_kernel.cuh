@@ -5,7 +5,7 @@
 // One piece of work is (sequence, KV head, tile of query rows, part of the
 // token range).  The q_len * G rows of a KV head are token-major (row r is query
 // r / G, head r % G), so a K/V tile read once serves the whole group and up to
-// 256 rows.  Per 128 x 128 tile of scores and D = 128:
+// 256 rows.  Per 128 x BN tile of scores:
 //
 //   S = Q K^T   tcgen05.mma, Q and K in shared memory, S (fp32) in tensor memory
 //   P = 2^(x - m), x the scaled, capped, biased, masked score in the log2 domain
@@ -16,12 +16,21 @@
 // team of 256 threads turns a score tile into weights: two threads per row, each
 // with half of the columns in registers, exchanging only the row's maximum (one
 // thread per row with all 128 columns left two warps per SM sub-partition, too few to
-// hide their own latencies: 0.70 against TEAMMS ms on four prompt chunks).  Two teams
-// (head_dim 64 and 128) work on different score tiles while the products of the
-// other run: on the two row tiles of a full piece, or, when a piece has at most
-// 128 rows, on alternate token tiles of the same rows, merged at the end.
-// head_dim 256 has one team with two score buffers (its accumulators take half
-// the tensor memory).
+// hide their own latencies: four capped prompt chunks 702 us, 636 with two).  Two
+// teams (head_dim 64 and 128, long query runs) work on different score tiles while
+// the products of the other run: on the two row tiles of a full piece, or, when a
+// piece has at most 128 rows, on alternate token tiles of the same rows, merged at
+// the end.  One team has two score buffers; head_dim 64 and 128 then have two CTAs
+// on an SM, while the accumulators of 256 take half the tensor memory.
+//
+// What bounds it.  On four prompt chunks (1500 to 2048 tokens each before up to 8192,
+// window 4096, 32 query and 8 KV heads of 128, 472 GFLOP) it takes 545 us with capped
+// scores and 416 without, 865 and 1134 TFLOP/s (0.45 and 0.59 of the measured peak):
+// a team's weights and its products follow each other, since its one score buffer
+// holds both, and the other team's products fill half of that.  For 64 tokens of
+// head_dim 128 the two products take 620 cycles back to back; what keeps them apart is
+// latency, of the tensor-memory loads, of the barrier operations behind the other
+// warps' arithmetic, and of the 4 cycles a warp's 32 exponentials take.
 //
 // The running maximum is raised only when a tile passes it by 2^8, so most tiles
 // do not rescale O in tensor memory; the weights (at most 2^8) are rounded to bf16
@@ -183,6 +192,12 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     int first;
     return (int)(((long long)rows_at(s, first) * G + kRows - 1) / kRows);
   };
+  // row offsets that fall, or pass total_q, are reported (such rows are not written)
+  auto check_rows = [&](int s) {
+    if (p.num_blocks <= 0 || blockIdx.x != 0) return;
+    const int a = __ldg(p.qo_indptr + s), b = __ldg(p.qo_indptr + s + 1);
+    if (a < 0 || b < a || b > p.total_q) report(kTileStatusBadLength);
+  };
   if (tid == 0) {
     sm_i[1] = -1;
     sm_i[3] = 0x7fffffff;
@@ -209,6 +224,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       // what the sequence's last row sees, which is near what each of its pieces walks
       int first;
       const int rows = rows_at(tid, first), L = __ldg(p.seq_lens + tid);
+      check_rows(tid);
       int from = p.window > 0 ? L - p.window : 0;
       if (p.doc_starts != nullptr && rows > 0)
         from = max(from, __ldg(p.doc_starts + first + rows - 1));
@@ -236,7 +252,10 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     const int per = (N + kThreads - 1) / kThreads;
     const int s0 = min(N, tid * per), s1 = min(N, s0 + per);
     int local = 0;
-    for (int s = s0; s < s1; ++s) local += tiles_of(s);
+    for (int s = s0; s < s1; ++s) {
+      local += tiles_of(s);
+      check_rows(s);
+    }
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -124,3 +124,63 @@ def test_the_binding_refuses_scattered_new_rows():
             pa.paged_kv_append_slots(bad, good, kc, vc, slots)
     with pytest.raises(ValueError):
         pa.paged_kv_append_slots(good, good, kc, vc, slots.int())
+
+
+MULTI = dict(q=16, k=16, v=16, out=16, qo=16, bt=16, sl=16, num_seqs=2, total_q=5, H_q=8, H_kv=2,
+             D=128, maxb=4, BS=16, scale=0.125, causal=1, softcap=0.0, slopes=None, window=0,
+             prefix=None, docs=None, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H_q=6, H_kv=4), -2), (dict(D=32), -3), (dict(BS=64), -4), (dict(num_seqs=-1), -5),
+    (dict(total_q=-1), -5), (dict(total_q=2 ** 29), -5), (dict(scale=float("nan")), -8),
+    (dict(q=8), -1), (dict(qo=None), -1), (dict(softcap=1e-31), -11), (dict(softcap=2e30), -11),
+    (dict(softcap=1e-25, scale=1e6), -11), (dict(window=-5), -11), (dict(docs=1), -1),
+    (dict(maxb=2 ** 27 - 8), -5),
+])
+def test_decode_multi_mods_refuses(lib, kw, code):
+    assert lib.paged_attn_decode_multi_mods(*dict(MULTI, **kw).values()) == code
+
+
+def test_empty_query_batches_are_no_ops(lib):
+    for kw in (dict(total_q=0), dict(num_seqs=0)):
+        a = dict(MULTI, q=None, k=None, v=None, out=None, qo=None, bt=None, sl=None, **kw)
+        assert lib.paged_attn_decode_multi_mods(*a.values()) == 0
+
+
+SHARED = dict(q=16, k=16, v=16, out=16, gi=16, pt=16, pl=16, groups=1, pmax=4, bt=16, sl=16,
+              num_seqs=2, H_q=8, H_kv=2, D=128, maxb=4, BS=16, scale=0.125, softcap=0.0,
+              slopes=None, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(H_q=6, H_kv=4), -2), (dict(D=32), -3), (dict(BS=64), -4), (dict(num_seqs=-1), -5),
+    (dict(groups=-1), -5), (dict(pmax=0), -5), (dict(pmax=2 ** 27 - 8), -5),
+    (dict(scale=float("inf")), -8), (dict(gi=None), -1), (dict(pt=8), -1), (dict(pl=None), -1),
+    (dict(bt=None), -1), (dict(softcap=-2.0), -11), (dict(slopes=3), -1),
+])
+def test_decode_shared_refuses(lib, kw, code):
+    assert lib.paged_attn_decode_shared(*dict(SHARED, **kw).values()) == code
+
+
+@pytest.mark.parametrize("name,args", [
+    ("paged_attn_mods_workspace_bytes", (4, 6, 4, 128, 8, 16)),
+    ("paged_attn_mods_workspace_bytes", (4, 8, 2, 80, 8, 16)),
+    ("paged_attn_multi_mods_workspace_bytes", (4, -1, 8, 2, 128, 8, 16)),
+    ("paged_attn_multi_mods_workspace_bytes", (4, 5, 8, 2, 128, 8, 8)),
+    ("paged_attn_shared_workspace_bytes", (4, -1, 8, 2, 128, 8, 16)),
+])
+def test_workspace_queries_reject_bad_sizes(lib, name, args):
+    assert getattr(lib, name)(*args) == 0
+
+
+def test_the_binding_refuses_mismatched_groups_and_offsets():
+    q, kc, vc, bt, sl = problem()
+    gi, pt, pl = (torch.zeros(2, dtype=torch.int32), torch.zeros(1, 4, dtype=torch.int32),
+                  torch.zeros(1, dtype=torch.int32))
+    for bad in ((gi[:1], pt, pl), (gi, pt[0], pl), (gi, pt, gi), (gi.long(), pt, pl)):
+        with pytest.raises(ValueError):
+            pa.paged_attn_decode_shared(q, kc, vc, *bad, bt, sl, 0.1)
+    for qo in (torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int64)):
+        with pytest.raises(ValueError):
+            pa.paged_attn_decode_multi_mods(q, kc, vc, qo, bt, sl, 0.1)
