@@ -44,6 +44,7 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "tcgen05.cuh"
 #include "tile.h"
@@ -653,6 +654,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         }
       }
       float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+      const float own_max = mx;
       // the other half's; its thread has read its scores by then, so the packed
       // weights may overwrite them.  (With one score buffer a thread comes here again
       // only when all have finished this step; with two, the buffers of the exchange
@@ -675,14 +677,14 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       // ---- weights 2^(x - m), packed
       float2 sum = make_float2(0.f, 0.f);
       const float2 sub2 = make_float2(-sub, -sub);
-      auto weigh = [&](auto&& exponent) {
+      auto weigh = [&](auto masked, auto&& exponent) {
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
           uint32_t w[16];
 #pragma unroll
           for (int e2 = 0; e2 < 16; ++e2) {
             float2 e = exponent(make_float2(x[c + 2 * e2], x[c + 2 * e2 + 1]));
-            if (MOD == kTileCapped && ragged) {
+            if constexpr (decltype(masked)::value) {
               if (!sees(c + 2 * e2)) e.x = -INFINITY;
               if (!sees(c + 2 * e2 + 1)) e.y = -INFINITY;
             }
@@ -695,29 +697,40 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         }
       };
       if constexpr (MOD == kTileCapped) {
-        float big0 = 0.f, big1 = 0.f;
+        float mn0 = INFINITY, mn1 = INFINITY;
 #pragma unroll
         for (int c = 0; c < kCols; c += 4) {
-          big0 = max3(big0, fabsf(x[c]), fabsf(x[c + 1]));
-          big1 = max3(big1, fabsf(x[c + 2]), fabsf(x[c + 3]));
+          mn0 = min3(mn0, x[c], x[c + 1]);
+          mn1 = min3(mn1, x[c + 2], x[c + 3]);
         }
-        // (a NaN is not carried by the maximum; the polynomial keeps it)
-        if (__all_sync(0xffffffffu, fmaxf(big0, big1) < cap.reach)) {
+        // (of a ragged tile own_max leaves the unseen scores out: what the polynomial
+        // makes of them is not used.  A NaN is carried neither here nor there; the
+        // polynomial keeps it.)
+        if (__all_sync(0xffffffffu, fmaxf(own_max, -fminf(mn0, mn1)) < cap.reach)) {
           const float2 a0 = make_float2(cap.a0, cap.a0), a1 = make_float2(cap.a1, cap.a1);
           const float2 a2 = make_float2(cap.a2, cap.a2);
-          weigh([&](float2 s) {
+          auto series = [&](float2 s) {
             const float2 z = mul2(s, s);
             return fma2(s, fma2(z, fma2(z, a2, a1), a0), sub2);
-          });
+          };
+          // (two loops: as a condition inside one the selection costs every tile)
+          if (ragged)
+            weigh(std::true_type(), series);
+          else
+            weigh(std::false_type(), series);
         } else {
-          weigh([&](float2 s) {
+          if (!ragged) {
+#pragma unroll
+            for (int c = 0; c < kCols; c += 32) seen[c / 32] = 0xffffffffu;
+          }
+          weigh(std::true_type(), [&](float2 s) {
             return make_float2(cap_score(s.x, p.cap_in, p.cap_log2) - sub,
                                cap_score(s.y, p.cap_in, p.cap_log2) - sub);
           });
         }
       } else {
         const float f = MOD == kTilePlain ? p.scale_log2 : 1.f;
-        weigh([&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
+        weigh(std::false_type(), [&](float2 s) { return fma2(s, make_float2(f, f), sub2); });
       }
       l += sum.x + sum.y;
       tmem_st_wait();
