@@ -89,6 +89,26 @@ __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// mbar_wait whose first looks may each suspend the warp for that long, so that a
+// waiting warp leaves the issue slots to the working ones (plain prompt chunks 409 ->
+// 401 us).  In all at most kTileWaits of them, then mbar_wait's own limit.
+constexpr uint32_t kTileWaitNs = 16384;
+constexpr int kTileWaits = 64;
+__device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < kTileWaits; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kTileWaitNs)
+        : "memory");
+    if (done) return true;
+  }
+  return mbar_wait(bar, parity);
+}
+
 // ---------------------------------------------------------------- pairs of floats
 
 // Two fp32 operations in one instruction (each rounded as its scalar form).

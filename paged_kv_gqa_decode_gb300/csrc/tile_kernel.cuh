@@ -24,8 +24,8 @@
 // on an SM, while the accumulators of 256 take half the tensor memory.
 //
 // What bounds it.  On four prompt chunks (1500 to 2048 tokens each before up to 8192,
-// window 4096, 32 query and 8 KV heads of 128, 472 GFLOP) it takes 545 us with capped
-// scores and 416 without, 865 and 1134 TFLOP/s (0.45 and 0.59 of the measured peak):
+// window 4096, 32 query and 8 KV heads of 128, 472 GFLOP) it takes 482 us with capped
+// scores and 400 without, 979 and 1180 TFLOP/s (0.51 and 0.61 of the measured peak):
 // a team's weights and its products follow each other, since its one score buffer
 // holds both, and the other team's products fill half of that.  For 64 tokens of
 // head_dim 128 the two products take 620 cycles back to back; what keeps them apart is
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       const int pb_next = block_of(it + T::kProducers);
       bool is_v;
       tile_of(it, is_v);
-      ok = ok && mbar_wait(&empty[slot], phase ^ 1u);
+      ok = ok && tile_wait(&empty[slot], phase ^ 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(&full[slot], T::kSlotBytes);
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       // where that look came too early.
       bool seen = mbar_test_wait(&full[0], 0u);
       auto next_item = [&]() -> int {  // waits for the next item, returns its slot
-        if (!seen && ok) ok = mbar_wait(&full[item], phase);
+        if (!seen && ok) ok = tile_wait(&full[item], phase);
         const int slot = item;
         if (++item == slots) {
           item = 0;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         if (!two || t == 0) v_slot = next_item();
         // (after a timeout the walk goes on without waiting: what it then multiplies is
         // in bounds, and the call has reported)
-        if (ok) ok = mbar_wait(&p_full[buf_of(t, i)], (uint32_t)(i / kBufs) & 1u);
+        if (ok) ok = tile_wait(&p_full[buf_of(t, i)], (uint32_t)(i / kBufs) & 1u);
         tc_fence_after();
         const uint32_t vd = q_desc + v_lead + (slot_off(v_slot) >> 4);
 #pragma unroll
@@ -545,14 +545,19 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     __syncwarp();
   } else {
     // ===================================================================== softmax
-    constexpr int kCols = T::kCols;
+    // A thread's 32 or 64 columns.  With 64 registers are scarce (96 a thread): capped
+    // scores, whose polynomial wants some, are read in two blocks, and the first one a
+    // second time for its weights instead of being kept (four capped prompt chunks 507
+    // -> 485 us; plain ones lose by it, 401 -> 427).
+    constexpr int kCols = T::kCols, kBlocks = kCols / 32;
+    constexpr bool kReload = kBlocks == 2 && MOD == kTileCapped;
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_addr =
         tmem + lane_base + T::kOCol + (kTeams == 2 ? team * D : 0) + half * (D / 2);
     float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * kBufs * 256;
     const uint32_t pair_bar = 1 + team * 4 + (warp & 3);  // the two warps of 32 rows
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+      return __all_sync(0xffffffffu, tile_wait(bar, parity)) != 0;
     };
     float m = -INFINITY, l = 0.f;  // l: over this thread's columns
     bool ok = true;
@@ -573,10 +578,32 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       ok = ok && warp_wait(&s_full[buf], (uint32_t)(i / kBufs) & 1u);
       if (ok) tc_fence_after();
       if (!idle) {
-      float x[kCols];  // this thread's scores (a timeout leaves what is there: the walk goes
-                       // on without waiting, so that the row's threads stay together)
-      tmem_ld_begin(s_addr + half * kCols, x);
-      tmem_ld_end(x);
+      // ---- Unseen tokens: a bit per column, from the interval ends.
+      bool ragged = false;
+      uint32_t seen[kBlocks];
+      auto find_seen = [&] {
+        if (t0 >= clean_lo && t0 <= clean_hi) return;
+        const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
+        ragged = !__all_sync(0xffffffffu, whole);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          seen[b] = (bits_from(lo - c0 - 32 * b) & ~bits_from(hi + 1LL - c0 - 32 * b)) |
+                    ~bits_from(pre - c0 - 32 * b);
+      };
+      auto sees = [&](int b, int c) { return (seen[b] >> c & 1u) != 0; };
+      // ---- this thread's scores (a timeout leaves what is there: the walk goes on
+      // without waiting, so that the row's threads stay together)
+      float x[kReload ? 1 : kBlocks][32];
+      auto load = [&](int b) {
+        tmem_ld_begin(s_addr + half * kCols + b * 32, x[kReload ? 0 : b]);
+        tmem_ld_end(x[kReload ? 0 : b]);
+      };
+      if constexpr (kReload || kBlocks == 1) {
+        if constexpr (!kReload) load(0);
+      } else {
+        tmem_ld_begin(s_addr + half * kCols, reinterpret_cast<float (&)[64]>(x));
+        tmem_ld_end(reinterpret_cast<float (&)[64]>(x));
+      }
       if constexpr (MOD == kTileGeneral) {
         // the whole transformation here, in place: with a bias the order of the raw
         // scores says nothing
@@ -588,72 +615,80 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
           float big0 = 0.f, big1 = 0.f;
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
-            big0 = max3(big0, fabsf(x[c]), fabsf(x[c + 1]));
-            big1 = max3(big1, fabsf(x[c + 2]), fabsf(x[c + 3]));
+            const float* y = &x[c >> 5][c & 31];
+            big0 = max3(big0, fabsf(y[0]), fabsf(y[1]));
+            big1 = max3(big1, fabsf(y[2]), fabsf(y[3]));
           }
           const CapSeries cap = cap_series(p.cap_in, p.cap_log2);
           if (__all_sync(0xffffffffu, fmaxf(big0, big1) < cap.reach)) {
 #pragma unroll
             for (int c = 0; c < kCols; ++c) {
-              const float z = x[c] * x[c];
-              x[c] = x[c] * fmaf(z, fmaf(z, cap.a2, cap.a1), cap.a0);
+              float& y = x[c >> 5][c & 31];
+              const float z = y * y;
+              y = y * fmaf(z, fmaf(z, cap.a2, cap.a1), cap.a0);
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c] = cap_score(x[c], p.cap_in, p.cap_log2);
+            for (int c = 0; c < kCols; ++c)
+              x[c >> 5][c & 31] = cap_score(x[c >> 5][c & 31], p.cap_in, p.cap_log2);
           }
           if (behind) {
 #pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c] += fmaf(slope, (float)c, base);
+            for (int c = 0; c < kCols; ++c) x[c >> 5][c & 31] += fmaf(slope, (float)c, base);
           }
         } else if (behind) {
 #pragma unroll
           for (int c = 0; c < kCols; ++c)
-            x[c] = fmaf(x[c], p.scale_log2, fmaf(slope, (float)c, base));
+            x[c >> 5][c & 31] = fmaf(x[c >> 5][c & 31], p.scale_log2, fmaf(slope, (float)c, base));
         } else {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c] *= p.scale_log2;
+          for (int c = 0; c < kCols; ++c) x[c >> 5][c & 31] *= p.scale_log2;
         }
         if (!behind) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c] = fmaf(-slope, fabsf(d0 - (float)c), x[c]);
+          for (int c = 0; c < kCols; ++c)
+            x[c >> 5][c & 31] = fmaf(-slope, fabsf(d0 - (float)c), x[c >> 5][c & 31]);
         }
       }
-      // ---- Unseen tokens: a bit per column, from the interval ends.  Their scores
-      // become -inf; capped ones only for the maximum, as the polynomial wants the
-      // others finite, and their exponents later.
-      bool ragged = false;
-      uint32_t seen[kCols / 32];
-      if (t0 < clean_lo || t0 > clean_hi) {
-        const bool whole = (c0 >= lo && c0 + kCols - 1 <= hi) || c0 + kCols <= pre;
-        ragged = !__all_sync(0xffffffffu, whole);
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32)
-          seen[c / 32] = (bits_from(lo - c0 - c) & ~bits_from(hi + 1LL - c0 - c)) |
-                         ~bits_from(pre - c0 - c);
-      }
-      auto sees = [&](int c) { return (seen[c / 32] >> (c & 31) & 1u) != 0; };
+      find_seen();
+      // (capped scores are left alone, as the polynomial wants them finite: out of the
+      // maximum here, and given no weight below)
       if (MOD != kTileCapped && ragged) {
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
-          if (!sees(c)) x[c] = -INFINITY;
+          if (!sees(c >> 5, c & 31)) x[c >> 5][c & 31] = -INFINITY;
       }
       // ---- running maximum, raised only past kTileLazyMax.  Scaling by a positive
       // factor and the cap keep the order: there only the maximum is transformed.
-      float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-      if (MOD == kTileCapped && ragged) {
+      float mx = -INFINITY, mn = INFINITY;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) mx0 = sees(c) ? fmaxf(mx0, x[c]) : mx0;
-      } else {
+      for (int b = 0; b < kBlocks; ++b) {
+        if constexpr (kReload) load(b);
+        const float (&y)[32] = x[kReload ? 0 : b];
+        if (MOD == kTileCapped && ragged) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 8) {
-          mx0 = max3(mx0, x[c], x[c + 1]);
-          mx1 = max3(mx1, x[c + 2], x[c + 3]);
-          mx2 = max3(mx2, x[c + 4], x[c + 5]);
-          mx3 = max3(mx3, x[c + 6], x[c + 7]);
+          for (int c = 0; c < 32; ++c) mx = sees(b, c) ? fmaxf(mx, y[c]) : mx;
+        } else {
+          float mx0 = mx, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 8) {
+            mx0 = max3(mx0, y[c], y[c + 1]);
+            mx1 = max3(mx1, y[c + 2], y[c + 3]);
+            mx2 = max3(mx2, y[c + 4], y[c + 5]);
+            mx3 = max3(mx3, y[c + 6], y[c + 7]);
+          }
+          mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+        }
+        if constexpr (MOD == kTileCapped) {
+          float mn1 = INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            mn = min3(mn, y[c], y[c + 1]);
+            mn1 = min3(mn1, y[c + 2], y[c + 3]);
+          }
+          mn = fminf(mn, mn1);
         }
       }
-      float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
       const float own_max = mx;
       // the other half's; its thread has read its scores by then, so the packed
       // weights may overwrite them.  (With one score buffer a thread comes here again
@@ -679,34 +714,34 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       const float2 sub2 = make_float2(-sub, -sub);
       auto weigh = [&](auto masked, auto&& exponent) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
+        for (int k = 0; k < kBlocks; ++k) {
+          const int b = kReload ? kBlocks - 1 - k : k;
+          const float (&y)[32] = x[kReload ? 0 : b];
           uint32_t w[16];
 #pragma unroll
           for (int e2 = 0; e2 < 16; ++e2) {
-            float2 e = exponent(make_float2(x[c + 2 * e2], x[c + 2 * e2 + 1]));
+            float2 e = exponent(make_float2(y[2 * e2], y[2 * e2 + 1]));
             if constexpr (decltype(masked)::value) {
-              if (!sees(c + 2 * e2)) e.x = -INFINITY;
-              if (!sees(c + 2 * e2 + 1)) e.y = -INFINITY;
+              if (!sees(b, 2 * e2)) e.x = -INFINITY;
+              if (!sees(b, 2 * e2 + 1)) e.y = -INFINITY;
             }
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             sum = add2(sum, e);
             w[e2] = pack_bf16x2(e.x, e.y);
           }
-          tmem_st(s_addr + half * (kCols / 2) + c / 2, w);
+          // (the first block's scores again, before the weights over them: those of the
+          // second take the place of its last 16)
+          if constexpr (kReload)
+            if (b > 0) load(b - 1);
+          tmem_st(s_addr + half * (kCols / 2) + b * 16, w);
         }
       };
       if constexpr (MOD == kTileCapped) {
-        float mn0 = INFINITY, mn1 = INFINITY;
-#pragma unroll
-        for (int c = 0; c < kCols; c += 4) {
-          mn0 = min3(mn0, x[c], x[c + 1]);
-          mn1 = min3(mn1, x[c + 2], x[c + 3]);
-        }
         // (of a ragged tile own_max leaves the unseen scores out: what the polynomial
         // makes of them is not used.  A NaN is carried neither here nor there; the
         // polynomial keeps it.)
-        if (__all_sync(0xffffffffu, fmaxf(own_max, -fminf(mn0, mn1)) < cap.reach)) {
+        if (__all_sync(0xffffffffu, fmaxf(own_max, -mn) < cap.reach)) {
           const float2 a0 = make_float2(cap.a0, cap.a0), a1 = make_float2(cap.a1, cap.a1);
           const float2 a2 = make_float2(cap.a2, cap.a2);
           auto series = [&](float2 s) {
@@ -721,7 +756,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         } else {
           if (!ragged) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 32) seen[c / 32] = 0xffffffffu;
+            for (int b = 0; b < kBlocks; ++b) seen[b] = 0xffffffffu;
           }
           weigh(std::true_type(), [&](float2 s) {
             return make_float2(cap_score(s.x, p.cap_in, p.cap_log2) - sub,
@@ -754,7 +789,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       }
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
-      if ((t0 < clean_lo || t0 > clean_hi) && (!both || team == 0) && (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
+      if ((t0 < clean_lo || t0 > clean_hi) && (!both || team == 0) &&
+          (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
         const int item = item_v(j);
         ok = ok && warp_wait(&full[item % slots], (uint32_t)((item / slots) & 1));
         uint8_t* v = smem + slot_off(item % slots);
