@@ -443,8 +443,8 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
  *                 document the query is in, in a sequence that packs several
  *
  * softcap is 0 or in [1e-30, 1e30], and max_blocks_per_seq * block_size at most
- * 2^31 - 256.  prefix_lens and doc_starts are clamped to [0, L].  A query that sees no token
- * gets a zero row.  Pages that hold no token the query sees are not read (their
+ * 2^31 - 256.  prefix_lens and doc_starts are clamped to [0, L].  A query that
+ * sees no token gets a zero row.  Pages that hold no token the query sees are not read (their
  * table entries neither), and unseen rows of the pages that are may hold
  * anything, NaN included.  The arrays are 4-byte aligned device (or pinned
  * host) memory.  The cap is computed in float32 to about 1e-6 of the score, the
@@ -454,8 +454,8 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
  * workspace: at least paged_attn_mods_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use, not shared by calls that may
  * overlap (one workspace serves any calls of the _mods and _shared entry points
- * on a device, in any order); or null, for a workspace the library owns, as paged_attn_decode's
- * (its own one, so calls of the two kinds may overlap).  A stream that is
+ * on a device, in any order); or null, for a workspace the library owns, as
+ * paged_attn_decode's (its own one, so calls of the two kinds may overlap).  A stream that is
  * being captured must pass one: with a null workspace the call returns
  * PAGED_ATTN_ERR_WORKSPACE there.  Launch flags do not apply.
  */
@@ -544,8 +544,8 @@ PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int to
  *
  * Everything else as paged_attn_decode; rows past a prefix's or a sequence's end
  * may hold anything.  A sequence without any token gets zero rows.  Three
- * launches: the prefixes and, side by side with them, the own tokens, then the merge.  num_groups = 0 is
- * paged_attn_decode_mods.  workspace: as there,
+ * launches: the prefixes and, side by side with them, the own tokens, then the
+ * merge.  num_groups = 0 is paged_attn_decode_mods.  workspace: as there,
  * paged_attn_shared_workspace_bytes(...) bytes.
  */
 PAGED_ATTN_API int paged_attn_decode_shared(
@@ -592,7 +592,8 @@ PAGED_ATTN_API size_t paged_attn_shared_workspace_bytes(int num_seqs, int num_gr
  * whatever is free.  Other outputs must not overlap inputs.
  *
  * max_new bounds the sum of new_lens, so that a captured step serves any batch
- * of up to that many rows.  Any number of sequences; max_blocks_per_seq and
+ * of up to that many rows.  Any number of sequences (of none, the padding slots,
+ * qo_indptr[0] and the counts are written); max_blocks_per_seq and
  * block_size as paged_attn_decode.  The tensors are 16-byte aligned, the
  * one-element ones 4-byte.  With paged_attn_set_checks on, a block id outside the
  * pool sets bit 0 and an invalid length bit 1 of the status word (such an id is

@@ -1227,7 +1227,8 @@ int paged_attn_decode_mods(const void* q, const void* k_cache, const void* v_cac
                            void* stream) {
   int rc = common_checks(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
                          head_dim, max_blocks_per_seq, block_size, scale);
-  if (rc == PAGED_ATTN_OK) rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+  if (rc == PAGED_ATTN_OK)
+    rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
                      window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
   Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
@@ -1251,7 +1252,8 @@ int paged_attn_decode_fp8_mods(const void* q, const void* k_cache, const void* v
                                void* stream) {
   int rc = fp8_checks(q, k_cache, v_cache, k_scale, v_scale, out, block_tables, seq_lens,
                       num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size, scale);
-  if (rc == PAGED_ATTN_OK) rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+  if (rc == PAGED_ATTN_OK)
+    rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
                      window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0) return rc;
   Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
@@ -1296,7 +1298,7 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   if (total_q < 0 || !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
     return PAGED_ATTN_ERR_SIZES;
   rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
-                     window, prefix_lens, doc_starts);
+                   window, prefix_lens, doc_starts);
   if (rc != PAGED_ATTN_OK || num_seqs == 0 || total_q == 0) return rc;
   rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
   if (rc != PAGED_ATTN_OK) return rc;
@@ -1475,10 +1477,11 @@ int paged_kv_assign(const int32_t* seq_lens, const int32_t* new_lens, int32_t* b
   int rc = validate_sizes(num_seqs, 1, 1, 64, max_blocks_per_seq, block_size);
   if (rc != PAGED_ATTN_OK) return rc;
   if (free_capacity < 0 || max_new < 0) return PAGED_ATTN_ERR_SIZES;
-  if (num_seqs == 0) return PAGED_ATTN_OK;
-  // what a launch without new rows or free blocks never touches may be null
-  if (!aligned16(seq_lens) || !aligned16(new_lens) || !aligned16(block_tables) ||
-      !aligned16(seq_lens_out) || !aligned16(qo_indptr) || free_count == nullptr ||
+  // What a launch without sequences, new rows or free blocks never touches may be null.
+  // (Without sequences there still are the padding slots and the counts to write.)
+  if ((num_seqs > 0 && (!aligned16(seq_lens) || !aligned16(new_lens) ||
+                        !aligned16(block_tables) || !aligned16(seq_lens_out))) ||
+      !aligned16(qo_indptr) || free_count == nullptr ||
       !aligned4(free_count) || free_count_out == nullptr || !aligned4(free_count_out) ||
       !aligned4(refused) || (max_new > 0 && !aligned16(slot_map)) ||
       (free_capacity > 0 && !aligned16(free_blocks)))

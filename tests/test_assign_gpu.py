@@ -83,6 +83,13 @@ def test_prompts_of_every_size(BS, in_place):
     check(*p, len(p[3]), BS, int(new.sum()) + 37, in_place)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("max_new", [0, 1, 50, 20000])
+def test_no_sequences(in_place, max_new):
+    none = np.zeros(0, dtype=int)
+    check(none, none, np.zeros((0, 4), dtype=int), np.arange(9), 9, 16, max_new, in_place)
+
+
 @pytest.mark.parametrize("short", [0, 1, 5, 40, 10 ** 6])
 def test_too_few_free_blocks(short):
     rng = np.random.default_rng(short)
