@@ -704,7 +704,8 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         group_indptr.data_ptr(), prefix_tables.data_ptr(), prefix_lens.data_ptr(), groups, pmax,
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
-        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
+        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace),
+        _raw_stream(stream, dev)))
     return out
 
 

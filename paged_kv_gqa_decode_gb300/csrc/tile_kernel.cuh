@@ -11,7 +11,7 @@
 //   P = 2^(x - m), x the scaled, capped, biased, masked score in the log2 domain
 //   O = O + P V tcgen05.mma, P (bf16) in tensor memory, V in shared memory
 //
-// Roles: one warp copies pages (TMA, one box per page and 128-byte column half,
+// Roles: a few warps copy pages (TMA, one box per page and 128-byte column half,
 // K and V tiles through one ring), one lane of another issues the products, and a
 // team of 256 threads turns a score tile into weights: two threads per row, each
 // with half of the columns in registers, exchanging only the row's maximum (one
@@ -271,12 +271,13 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       int s = s0;
       for (;;) {
         const int n = tiles_of(s);
-        if (want < before + n) break;
+        if (want < before + n || s + 1 >= s1) break;
         before += n;
         ++s;
       }
       sm_i[1] = s;
-      sm_i[2] = tiles_of(s) - 1 - (want - before);
+      // (clamped: offsets that overlap without end may wrap the sums)
+      sm_i[2] = min(max(tiles_of(s) - 1 - (want - before), 0), max(tiles_of(s) - 1, 0));
     }
     __syncthreads();
   }
