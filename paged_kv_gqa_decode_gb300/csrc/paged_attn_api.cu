@@ -785,7 +785,9 @@ long long tile_bound(int total_q, int num_seqs, int G, int teams) {
 // leave SMs idle behind a long sequence, more pay each CTA's 4 us of start and end:
 // verification of five tokens, 272 pieces, 1 / 2 / 3 / 6 parts 100 / 81 / 78 / 87 us;
 // 64 chats over three prompts, 40 pieces, one pass after the other, 4 / 8 / 12 / 24
-// parts 64 / 58 / 56 / 69 us).
+// parts 64 / 58 / 56 / 69 us; where pieces fill the places parts only cost: a chunk of
+// 1200 tokens, 160 pieces, 1 / 2 / 3 parts 88 / 118 / 140 us, two head_dim 256 chunks,
+// 156 pieces, 134 / 143 / 170 us).
 // `beside`: another launch runs at the same time (shared prefixes: the sequences'
 // own tokens), for which SMs are left: 1.25 CTAs an SM (the same 40 pieces 4 / 5 / 6 /
 // 12 parts 47.9 / 46.8 / 47.5 / 52.7 us).
