@@ -612,38 +612,50 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         // -slope |pos - t| is linear over the columns where no token lies past the
         // query, which is everywhere but on a causal diagonal and beyond
         const bool behind = __all_sync(0xffffffffu, pos >= c0 + kCols - 1 || slope == 0.f);
+        auto each_pair = [&](auto&& f) {  // column pairs (c, c + 1)
+#pragma unroll
+          for (int c = 0; c < kCols; c += 2) {
+            float* y = &x[c >> 5][c & 31];
+            const float2 v = f(make_float2(y[0], y[1]), c);
+            y[0] = v.x;
+            y[1] = v.y;
+          }
+        };
+        const float2 slope2 = make_float2(slope, slope), base2 = make_float2(base, base);
+        auto bias = [&](int c) {
+          return fma2(slope2, make_float2((float)c, (float)(c + 1)), base2);
+        };
         if (p.cap_log2 > 0.f) {
-          float big0 = 0.f, big1 = 0.f;
+          float mx0 = -INFINITY, mx1 = -INFINITY, mn0 = INFINITY, mn1 = INFINITY;
 #pragma unroll
           for (int c = 0; c < kCols; c += 4) {
             const float* y = &x[c >> 5][c & 31];
-            big0 = max3(big0, fabsf(y[0]), fabsf(y[1]));
-            big1 = max3(big1, fabsf(y[2]), fabsf(y[3]));
+            mx0 = max3(mx0, y[0], y[1]);
+            mx1 = max3(mx1, y[2], y[3]);
+            mn0 = min3(mn0, y[0], y[1]);
+            mn1 = min3(mn1, y[2], y[3]);
           }
           const CapSeries cap = cap_series(p.cap_in, p.cap_log2);
-          if (__all_sync(0xffffffffu, fmaxf(big0, big1) < cap.reach)) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) {
-              float& y = x[c >> 5][c & 31];
-              const float z = y * y;
-              y = y * fmaf(z, fmaf(z, cap.a2, cap.a1), cap.a0);
-            }
+          if (__all_sync(0xffffffffu, fmaxf(fmaxf(mx0, mx1), -fminf(mn0, mn1)) < cap.reach)) {
+            const float2 a0 = make_float2(cap.a0, cap.a0), a1 = make_float2(cap.a1, cap.a1);
+            const float2 a2 = make_float2(cap.a2, cap.a2);
+            each_pair([&](float2 y, int) {
+              const float2 z = mul2(y, y);
+              return mul2(y, fma2(z, fma2(z, a2, a1), a0));
+            });
           } else {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c)
-              x[c >> 5][c & 31] = cap_score(x[c >> 5][c & 31], p.cap_in, p.cap_log2);
+            each_pair([&](float2 y, int) {
+              return make_float2(cap_score(y.x, p.cap_in, p.cap_log2),
+                                 cap_score(y.y, p.cap_in, p.cap_log2));
+            });
           }
-          if (behind) {
-#pragma unroll
-            for (int c = 0; c < kCols; ++c) x[c >> 5][c & 31] += fmaf(slope, (float)c, base);
-          }
-        } else if (behind) {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            x[c >> 5][c & 31] = fmaf(x[c >> 5][c & 31], p.scale_log2, fmaf(slope, (float)c, base));
+          if (behind) each_pair([&](float2 y, int c) { return add2(y, bias(c)); });
         } else {
-#pragma unroll
-          for (int c = 0; c < kCols; ++c) x[c >> 5][c & 31] *= p.scale_log2;
+          const float2 f = make_float2(p.scale_log2, p.scale_log2);
+          if (behind)
+            each_pair([&](float2 y, int c) { return fma2(y, f, bias(c)); });
+          else
+            each_pair([&](float2 y, int) { return mul2(y, f); });
         }
         if (!behind) {
 #pragma unroll
