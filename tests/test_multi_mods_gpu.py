@@ -209,3 +209,33 @@ def test_bad_pages_are_reported():
         assert int(status) & 2
     finally:
         pa.paged_attn_set_checks(0, None)
+
+
+# Launches with as many pieces as the GPU has places run the kernel of two teams (head_dim 64
+# and 128): on both row tiles of a full piece, on alternate token tiles of a short one.
+@pytest.mark.parametrize("D,BS", [(64, 32), (128, 16)])
+@pytest.mark.parametrize("o", range(len(OPTIONS)))
+def test_options_on_many_pieces(D, BS, o):
+    run_case(LENS, QLENS, 32, 8, D, BS, 17 * D + BS + o, gain=2.0, **OPTIONS[o])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [0.0, 1.0, 1e6])
+@pytest.mark.parametrize("gain", [0.01, 60.0])
+def test_caps_and_scores_of_any_size_on_many_pieces(D, cap, gain):
+    run_case([300, 400, 129], [300, 257, 70], 32, 32, D, 16, 14, softcap=cap, gain=gain)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("cap", [1e-3, 1.0, 1e6])
+@pytest.mark.parametrize("gain", [0.01, 60.0])
+def test_caps_and_scores_of_any_size(D, cap, gain, alibi):
+    run_case([300, 77], [130, 77], 4, 2, D, 16, 15, softcap=cap, gain=gain, alibi=alibi)
+
+
+def test_repeat_calls_on_many_pieces_are_bitwise_identical():
+    a = run_case([1500, 700], [900, 700], 32, 8, 128, 16, 16, softcap=50.0, window=333)
+    for _ in range(3):
+        b = run_case([1500, 700], [900, 700], 32, 8, 128, 16, 16, softcap=50.0, window=333)
+        assert torch.equal(a, b)

@@ -95,6 +95,14 @@ def test_a_group_wider_than_a_row_tile():
     check([90], [300], list(np.random.default_rng(4).integers(0, 60, size=90)), 6, 1, 256, 16, 6)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(softcap=2.0, alibi=True)])
+def test_as_many_pieces_as_the_gpu_has_places(D, kw):
+    """The two-team kernel: full pieces, and a group of one short piece."""
+    check([290, 8], [333, 140], list(np.random.default_rng(5).integers(0, 40, size=300)), 128, 8,
+          D, 16, 12 + D, **kw)
+
+
 def test_empty_prefixes_empty_tails_and_sequences_in_no_group():
     out, _, _ = check([2, 2, 3], [0, 50, 0], [0, 4, 0, 3, 1, 0, 2, 90, 0], 4, 2, 64, 16, 7)
     assert torch.count_nonzero(out[0]) == 0 and torch.count_nonzero(out[8]) == 0
