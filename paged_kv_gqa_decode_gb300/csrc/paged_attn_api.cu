@@ -792,7 +792,7 @@ long long tile_bound(int total_q, int num_seqs, int G, int teams) {
 // own tokens), for which SMs are left: 1.25 CTAs an SM (the same 40 pieces 4 / 5 / 6 /
 // 12 parts 47.9 / 46.8 / 47.5 / 52.7 us).
 // The part count bounds what the kernel uses (it never makes parts of fewer than
-// two tiles).
+// two tiles).  num_seqs > 0, so there is at least one piece.
 int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,
                 bool beside = false) {
   const int G = H_q / H_kv, teams = tile_teams(D, (long long)total_q * G, num_seqs, H_kv, sms);
@@ -1356,6 +1356,11 @@ int shared_plan(int num_seqs, int num_groups, int H_q, int H_kv, int head_dim, i
   rc = cached_plan(num_seqs, H_q, H_kv, head_dim, block_size, dev, di, &sp->own, false, 0, 0,
                    true);
   if (rc != PAGED_ATTN_OK) return rc;
+  if (num_groups == 0) {  // the decode alone: no pieces, no states to merge
+    sp->splits = 0;
+    sp->off_state = sp->off_parts = sp->bytes = sp->own.ws_bytes;
+    return PAGED_ATTN_OK;
+  }
   sp->splits = tile_splits(head_dim, num_seqs, num_groups, H_q, H_kv, di.sms, true);
   sp->off_state = round_up(sp->own.ws_bytes, kWsAlign);
   sp->off_parts =
