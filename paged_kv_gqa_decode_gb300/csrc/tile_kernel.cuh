@@ -40,7 +40,8 @@
 // tiles that no row of the piece sees are not walked, their pages not read; in
 // the few tiles where an interval ends the scores are selected, and V rows that no
 // row of the piece sees, which may hold anything, are zeroed in shared memory
-// before the product.
+// before the product.  Those are the rows outside the hull of the rows' intervals and, where
+// a row sees nothing, its own token if no later row sees it.
 #pragma once
 
 #include <atomic>
@@ -94,7 +95,7 @@ struct TileShape {
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
   static constexpr int kSmem = kMaxOff + kTeams * kBufs * 2 * 128 * 4;
-  static_assert((kSmem + 1024) * kCtas <= 228 * 1024 && (2 * kSlots + 14) * 8 <= 384,
+  static_assert((kSmem + 1024) * kCtas <= 228 * 1024 && (2 * kSlots + 14 + kProducers) * 8 <= 384,
                 "shared memory");
 };
 
@@ -154,10 +155,13 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   uint64_t* o_done = p_full + 4;             // [team][2] product with V done
   uint64_t* q_full = o_done + 4;
   uint64_t* drain = q_full + 1;
+  uint64_t* landed = drain + 1;              // [kProducers] a copy's landing (with sm_i[7])
   int* sm_i = reinterpret_cast<int*>(smem + T::kBarOff + 384);
   // sm_i: [0] TMEM address, [1] sequence, [2] row tile, [3] min lo, [4] max hi,
-  // [5] max lo, [6] min hi,
-  // [8..32) warp sums of the tile search
+  // [5] max lo, [6] min hi, [7] a row sees nothing: there may be tokens between min lo
+  // and max hi that no row sees,
+  // [8..32) warp sums of the tile search; then [8..16) a bit per query of the piece, set when
+  // a row sees its token (used with [7] only)
   uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(sm_i);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -205,6 +209,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     sm_i[4] = -1;
     sm_i[5] = 0;
     sm_i[6] = 0x7fffffff;
+    sm_i[7] = 0;
     for (int i = 0; i < T::kSlots; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -327,6 +332,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     if (lo <= hi) {
       atomicMin(&sm_i[3], lo);
       atomicMax(&sm_i[4], hi);
+    } else if (p.causal) {
+      sm_i[7] = 1;
     }
     atomicMax(&sm_i[5], lo);
     atomicMin(&sm_i[6], hi);
@@ -349,6 +356,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
   }
+  if (tid < 8) sm_i[8 + tid] = 0;
   __syncthreads();
   const int min_lo = sm_i[3], max_hi = sm_i[4];
   // tiles beginning in [clean_lo, clean_hi] are seen whole by every row
@@ -428,6 +436,43 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         report(kTileStatusBadBlock);  // the copy's bounds check reads it as zeros
       return pb;
     };
+    // Tokens inside [min_lo, max_hi] that no row sees.  Rows that see up to themselves cover
+    // what lies between the first and the last of them, so only tokens of rows which see
+    // nothing can be such.  Their V rows are zeroed here, between a tile's landing
+    // and its arrival at `full`: one copy at a time, but only in these rare pieces, and
+    // nothing of it in the loops of the other warps (the same in the softmax loop: four
+    // capped prompt chunks 478 -> 492 us).
+    const bool between = sm_i[7] != 0;
+    const int pos0 = len - q_len + row0 / G;  // the token of the piece's first query
+    uint32_t land_phase = 0;
+    if (between) {  // (every warp sets all the bits, and its own barrier up)
+      if (lane == 0) {
+        mbar_init(&landed[first], 1);
+        fence_barrier_init();
+        fence_proxy_async_shared();
+      }
+      const int last = (row0 + n_rows - 1) / G - row0 / G;
+      for (int k = lane; k <= last; k += 32) {
+        int from = p.window > 0 ? (int)max(0LL, (long long)pos0 + k - p.window + 1) : 0;
+        if (p.doc_starts != nullptr)
+          from = max(from, min(__ldg(p.doc_starts + qo + row0 / G + k), len));
+        if (from > pos0 + k) continue;
+        const int a = max(from - pos0, 0);
+        for (int w = a >> 5; w <= k >> 5; ++w)
+          atomicOr(&sm_i[8 + w], (int)(bits_from(a - 32 * w) & ~bits_from(k + 1 - 32 * w)));
+      }
+      __syncwarp();
+    }
+    auto zero_between = [&](uint8_t* v, int t0) {
+      for (int row = 0; row < BN; ++row) {
+        const int t = t0 + row, k = t - pos0;
+        if (t < pre || t > max_hi || k < 0 || (sm_i[8 + (k >> 5)] >> (k & 31) & 1)) continue;
+        if (lane < kHalves * 8)
+          *reinterpret_cast<uint4*>(v + (lane >> 3) * (BN * 128) + row * 128 + (lane & 7) * 16) =
+              make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_shared();
+    };
     bool ok = true;
     int slot = first, end = first;  // end: one stride past the last item copied
     uint32_t phase = 0;
@@ -435,16 +480,24 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     for (int it = first; it < 2 * n; it += T::kProducers) {
       const int pb_next = block_of(it + T::kProducers);
       bool is_v;
-      tile_of(it, is_v);
+      const int tile = tile_of(it, is_v);
       ok = ok && tile_wait(&empty[slot], phase ^ 1u);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], T::kSlotBytes);
+      uint64_t* bar = between ? &landed[first] : &full[slot];
+      if (lane == 0) mbar_arrive_expect_tx(bar, T::kSlotBytes);
       __syncwarp();
       if (lane < boxes)  // a block id of -1 is out of the map's bounds: zeros
         tma_load_4d(smem + slot_off(slot) + half_col * (BN * 128) + page * p.BS * 128,
-                    is_v ? &tm_v : &tm_k, &full[slot], 0, g * p.BS, half_col, pb < 0 ? -1 : pb,
-                    policy);
+                    is_v ? &tm_v : &tm_k, bar, 0, g * p.BS, half_col, pb < 0 ? -1 : pb, policy);
+      if (between) {
+        ok = __all_sync(0xffffffffu, tile_wait(bar, land_phase));
+        land_phase ^= 1u;
+        if (!ok) break;
+        if (is_v) zero_between(smem + slot_off(slot), token_of(tile));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[slot]);
+      }
       slot += T::kProducers;
       if (slot >= slots) {
         slot -= slots;

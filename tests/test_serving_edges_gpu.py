@@ -5,6 +5,7 @@ import torch
 
 import paged_kv_gqa_decode_gb300 as pa
 import workloads
+from oracle import serving
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,84 @@ def test_no_groups_in_a_captured_stream():
     torch.cuda.synchronize()
     assert torch.equal(out, pa.paged_attn_decode_mods(w.q, w.k_cache, w.v_cache, w.block_tables,
                                                       w.seq_lens, w.scale))
+
+
+def f64(t):
+    return serving.bf16_to_f64(t)
+
+
+def within(out, res):
+    got = f64(out)
+    assert np.isfinite(got).all()
+    err = np.abs(got - res.out)
+    over = np.divide(err, res.tol, out=np.where(err > 0, np.inf, 0.0), where=res.tol > 0)
+    assert over.max() <= 1.0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+# ---- documents that begin behind a query (a blanked or padding row of a packed chunk)
+def check_documents(lens, qlens, H_q, H_kv, D, BS, docs, seed, causal=True, softcap=0.0,
+                    alibi=False, window=0, prefix=None):
+    """docs: one start per query row, anywhere.  K and V rows that no query of the sequence
+    sees are NaN."""
+    w = workloads.make(workloads.custom_spec("docs", len(lens), H_q, H_kv, D, BS, lens), seed=seed,
+                       device="cuda", poison="nan")
+    qo = np.concatenate([[0], np.cumsum(qlens)])
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(int(qo[-1]), H_q, D, generator=g).to(torch.bfloat16).cuda()
+    docs = np.asarray(docs, dtype=np.int64)
+    bt = w.block_tables.cpu().numpy()
+    hidden = 0
+    for s, (n, m) in enumerate(zip(lens, qlens)):
+        seen = serving.visible(n - m + np.arange(m), n, causal, window,
+                               0 if prefix is None else prefix[s], docs[qo[s]:qo[s + 1]])
+        for t in np.nonzero(~seen.any(axis=0))[0]:
+            for c in (w.k_cache, w.v_cache):
+                c[int(bt[s, t // BS]), :, t % BS] = float("nan")
+            hidden += 1
+    slopes = np.array([2.0 ** (-8.0 * (h + 1) / H_q) for h in range(H_q)], dtype=np.float32)
+    out = pa.paged_attn_decode_multi_mods(
+        q, w.k_cache, w.v_cache, i32(qo), w.block_tables, w.seq_lens, w.scale, causal=causal,
+        softcap=softcap, alibi_slopes=torch.tensor(slopes).cuda() if alibi else None,
+        window=window, prefix_lens=None if prefix is None else i32(prefix), doc_starts=i32(docs))
+    torch.cuda.synchronize()
+    within(out, serving.attend(f64(q), f64(w.k_cache), f64(w.v_cache), qo, bt, lens,
+                               float(np.float32(w.scale)), causal=causal, softcap=softcap,
+                               slopes=slopes.astype(np.float64) if alibi else None, window=window,
+                               prefix_lens=prefix, doc_starts=docs))
+    return hidden
+
+
+def test_tokens_between_the_documents_that_nobody_sees():
+    # rows 1 to 9 of a chunk see nothing, and nobody sees their tokens
+    assert check_documents([21], [11], 4, 2, 128, 16, [0] + [21] * 9 + [20], 1) == 9
+    # one blanked row in the middle of a prompt, the next document behind it
+    docs = [0] * 50 + [100] + [51] * 49
+    assert check_documents([100], [100], 4, 2, 128, 16, docs, 2) == 1
+    assert check_documents([100], [100], 4, 2, 128, 16, docs, 3, prefix=[51]) == 0
+    # a row that sees nothing before rows whose own document begins earlier: seen by those
+    assert check_documents([100], [100], 4, 2, 128, 16, [0] * 50 + [100] + [7] * 49, 4) == 0
+
+
+@pytest.mark.parametrize("D,BS,H_q,H_kv", [(64, 16, 4, 2), (128, 32, 6, 2), (256, 16, 2, 2),
+                                           (64, 32, 32, 8), (128, 16, 32, 8)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0), dict(alibi=True), dict(window=7),
+                                dict(prefix=[3, 0, 40, 33]), dict(causal=False)])
+def test_documents_that_begin_anywhere(D, BS, H_q, H_kv, kw):
+    lens, qlens = [300, 33, 170, 700], [300, 20, 129, 257]
+    rng = np.random.default_rng(D + BS + H_q)
+    docs = []
+    for n, m in zip(lens, qlens):
+        pos = n - m + np.arange(m)
+        start = np.maximum(0, pos - rng.integers(0, 40, size=m))
+        blank = rng.random(m) < 0.4
+        docs.append(np.where(blank, rng.integers(pos + 1, n + 5), start))
+    hidden = check_documents(lens, qlens, H_q, H_kv, D, BS, np.concatenate(docs), 5, **kw)
+    assert hidden > 20 or kw.get("causal") is False
+
+
+def test_hidden_tokens_of_a_range_in_parts():
+    docs = np.zeros(40, dtype=int)
+    docs[5:30] = 2 ** 31 - 1
+    docs[30:] = 8991
+    check_documents([9001], [40], 2, 1, 128, 16, docs, 6)
+    check_documents([9001], [40], 2, 1, 256, 32, docs, 7, window=5000)
