@@ -1368,9 +1368,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
       if (v >= R * (D / 4)) continue;
       const int r = v / (D / 4), d4 = v - r * (D / 4);
       float m_new = m_acc[k];
+      bool nan = l_acc[k] != l_acc[k];
 #pragma unroll 4
-      for (int j = 0; j < nc; ++j) m_new = fmaxf(m_new, parts[(j * R + r) * kPartialRow]);
-      if (m_new == -INFINITY) continue;
+      for (int j = 0; j < nc; ++j) {
+        const float m = parts[(j * R + r) * kPartialRow];
+        m_new = fmaxf(m_new, m);
+        nan = nan || m != m;
+      }
+      if (m_new == -INFINITY && !nan) continue;
       const float sc = m_acc[k] == -INFINITY ? 0.f : fast_exp2(m_acc[k] - m_new);
       float4 a = make_float4(acc[k].x * sc, acc[k].y * sc, acc[k].z * sc, acc[k].w * sc);
       float l = l_acc[k] * sc;
@@ -1404,7 +1409,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
         if (p.state != nullptr) {
           float* st = p.state + (size_t)qr * kPartialRow;
           *reinterpret_cast<float4*>(st + 4 + 4 * d4) = acc[k];
-          if (d4 == 0) *reinterpret_cast<float2*>(st) = make_float2(m_acc[k], l_acc[k]);
+          const float l = l_acc[k], M = l != l ? l : m_acc[k];
+          if (d4 == 0) *reinterpret_cast<float2*>(st) = make_float2(M, l);
           continue;
         }
       }
@@ -1502,7 +1508,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int h = 8 * nh + 2 * quad + e;
-          sm_m[warp * 16 + h] = m_run[nh][e];
+          // (a NaN score counts in the sum, not in the maximum: the maximum takes it
+          // over, so that the state is not taken for an empty one)
+          sm_m[warp * 16 + h] = l_run[nh][e] != l_run[nh][e] ? l_run[nh][e] : m_run[nh][e];
           sm_l[warp * 16 + h] = l_run[nh][e];
         }
     }
@@ -1546,6 +1554,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
         acc.z += v.z * f;
         acc.w += v.w * f;
       }
+      if (lsum != lsum) M = lsum;
       if (dst == nullptr) {
         const long long qr = qrow(s, g, r);
         if (qr < 0) continue;

@@ -34,7 +34,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const Mer
   float M = fmaxf(ml.x, own.x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  // (empty states, m = -inf, weigh nothing; what they hold is not read)
+  // (empty states, m = -inf, weigh nothing; what they hold is not read.  States that hold a
+  // NaN have m = NaN.)
   const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - M);
   const float w_own = own.x == -INFINITY ? 0.f : fast_exp2(own.x - M);
   float l = ml.x == -INFINITY ? 0.f : ml.y * w;

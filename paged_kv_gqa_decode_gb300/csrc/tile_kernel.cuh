@@ -889,6 +889,9 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       named_barrier(pair_bar, 64);
       l = half == 0 ? l + exchange[128 + r128] : exchange[r128] + l;
     }
+    // a NaN score counts in the sum, not in the maximum: the maximum takes it over, so that
+    // the state is not taken for an empty one
+    if (l != l) m = l;
     // ---- one row tile: the second team hands its state over through the ring (idle
     // once both have seen their last product), [D][128] floats, then (m, l)
     const bool merge = stride == 2 && n > 1;
@@ -914,8 +917,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         const float top = fmaxf(m, y.x);
         f_own = m == -INFINITY ? 0.f : fast_exp2(m - top);
         f_other = y.x == -INFINITY ? 0.f : fast_exp2(y.x - top);
-        l = l * f_own + (f_other > 0.f ? y.y * f_other : 0.f);
-        m = top;
+        l = l * f_own + (f_other != 0.f ? y.y * f_other : 0.f);
+        m = l != l ? l : top;
       }
     }
     if (both || team == 0) {
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           if (merge)
-            o[i] = o[i] * f_own + (f_other > 0.f ? sm_o[(c + i) * 128 + r128] * f_other : 0.f);
+            o[i] = o[i] * f_own + (f_other != 0.f ? sm_o[(c + i) * 128 + r128] * f_other : 0.f);
           o[i] *= inv;
         }
         if (valid) {

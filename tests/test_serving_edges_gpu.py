@@ -123,3 +123,91 @@ def test_hidden_tokens_of_a_range_in_parts():
     docs[30:] = 8991
     check_documents([9001], [40], 2, 1, 128, 16, docs, 6)
     check_documents([9001], [40], 2, 1, 256, 32, docs, 7, window=5000)
+
+
+# ---- a NaN in a query or in a token that it sees reaches the output, however the work is cut
+def nan_rows(out):
+    """[rows, heads]: all NaN or all finite, true for NaN."""
+    bad = torch.isnan(out)
+    assert torch.equal(bad.all(-1), bad.any(-1))
+    return bad.all(-1).cpu().numpy()
+
+
+LONG = [7, 20000, 1, 40]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[7, 30, 1, 40], LONG])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(window=15000)])
+def test_a_nan_query_of_a_decode(D, lens, kw):
+    w = workloads.make(workloads.custom_spec("nanq", 4, 8, 2, D, 16, lens), device="cuda")
+    w.q[1, 2] = float("nan")
+    w.q[2] = float("nan")
+    expect = np.zeros((4, 8), dtype=bool)
+    expect[1, 2] = expect[2] = True
+    args = (w.k_cache, w.v_cache, w.block_tables, w.seq_lens, w.scale)
+    assert np.array_equal(nan_rows(pa.paged_attn_decode_mods(w.q, *args, **kw)), expect)
+    if not kw:
+        assert np.array_equal(nan_rows(pa.paged_attn_decode(w.q, *args)), expect)
+    if D > 64:
+        f = workloads.to_fp8(w)
+        a8 = (w.q, f.k8, f.v8, f.k_scale, f.v_scale, w.block_tables, w.seq_lens, w.scale)
+        assert np.array_equal(nan_rows(pa.paged_attn_decode_fp8_mods(*a8, **kw)), expect)
+        if not kw:
+            assert np.array_equal(nan_rows(pa.paged_attn_decode_fp8(*a8)), expect)
+
+
+@pytest.mark.parametrize("D,H_q,H_kv", [(64, 8, 2), (128, 8, 2), (256, 8, 2), (64, 64, 32),
+                                        (128, 64, 32)])
+@pytest.mark.parametrize("lens", [[7, 300, 1, 40], LONG])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=30.0), dict(window=15000), dict(alibi=True)])
+def test_a_nan_query_among_many(D, H_q, H_kv, lens, kw):
+    w = workloads.make(workloads.custom_spec("nanm", 4, H_q, H_kv, D, 16, lens), device="cuda")
+    qo = np.cumsum([0, 3, 9, 1, 40])
+    q = torch.randn(53, H_q, D, device="cuda").to(torch.bfloat16)
+    q[5, 2] = float("nan")
+    q[12] = float("nan")
+    expect = np.zeros((53, H_q), dtype=bool)
+    expect[5, 2] = expect[12] = True
+    kw = dict(kw)
+    if kw.pop("alibi", False):
+        kw["alibi_slopes"] = torch.full((H_q,), 2.0 ** -6, device="cuda")
+    args = (q, w.k_cache, w.v_cache, i32(qo), w.block_tables, w.seq_lens, w.scale)
+    assert np.array_equal(nan_rows(pa.paged_attn_decode_multi_mods(*args, **kw)), expect)
+    if not kw and H_q == 8:
+        assert np.array_equal(nan_rows(pa.paged_attn_decode_multi(*args, 40)), expect)
+    # a blanked query sees nothing: a zero row whatever it holds
+    docs = np.zeros(53, dtype=int)
+    docs[12] = 2 ** 31 - 1
+    out = pa.paged_attn_decode_multi_mods(*args, **kw, doc_starts=i32(docs))
+    expect[12] = False
+    assert np.array_equal(nan_rows(out), expect) and torch.count_nonzero(out[12]) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("own", [[0, 5, 700, 40], [3, 9000, 1, 0]])
+def test_a_nan_query_over_a_shared_prefix(D, own):
+    w = workloads.make(workloads.custom_spec("nans", 5, 8, 2, D, 16, own + [5000]), device="cuda")
+    w.q[1, 2] = float("nan")
+    w.q[3] = float("nan")
+    expect = np.zeros((4, 8), dtype=bool)
+    expect[1, 2] = expect[3] = True
+    out = pa.paged_attn_decode_shared(w.q[:4].contiguous(), w.k_cache, w.v_cache, i32([0, 4]),
+                                      w.block_tables[4:].clone(), i32([5000]),
+                                      w.block_tables[:4].clone(), i32(own), w.scale)
+    assert np.array_equal(nan_rows(out), expect)
+
+
+def test_a_nan_token_reaches_those_who_see_it():
+    w = workloads.make(workloads.custom_spec("nank", 2, 8, 2, 128, 16, [20000, 50]), device="cuda")
+    w.k_cache[int(w.block_tables[0, 19000 // 16]), 1, 19000 % 16] = float("nan")
+    expect = np.zeros((2, 8), dtype=bool)
+    expect[0, 4:] = True
+    args = (w.k_cache, w.v_cache, w.block_tables, w.seq_lens, w.scale)
+    assert np.array_equal(nan_rows(pa.paged_attn_decode(w.q, *args)), expect)
+    assert np.array_equal(nan_rows(pa.paged_attn_decode_mods(w.q, *args)), expect)
+    assert not nan_rows(pa.paged_attn_decode_mods(w.q, *args, window=999)).any()
+    q = torch.randn(8, 8, 128, device="cuda").to(torch.bfloat16)
+    out = pa.paged_attn_decode_multi_mods(q, w.k_cache, w.v_cache, i32([0, 6, 8]), *args[2:],
+                                          softcap=5.0)
+    assert np.array_equal(nan_rows(out), np.repeat(expect, [6, 2], axis=0))
