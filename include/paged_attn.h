@@ -652,8 +652,12 @@ PAGED_ATTN_API const char* paged_attn_status_string(int status);
  * word.  In a layer-by-layer decode loop the kernel just before attention
  * typically writes q, and with paged_attn_append_decode the new K/V rows too,
  * but not the caches, tables or lengths.  With the caller's own
- * paged_kv_append (or any other write of the caches) just before, the flag
- * must stay off.  The append-and-decode entry points never let their own
+ * paged_kv_append or paged_kv_append_slots (or any other write of the caches)
+ * just before, the flag must stay off.  Further back such a write is safe: every
+ * launch of this library lets the next one begin only when the work ahead of its
+ * call is complete, so a decode with the flag finds the call just ahead running
+ * at most.  (A caller's kernel that begins its own dependents before its wait does
+ * not keep to that: behind it any launch still running counts.)  The append-and-decode entry points never let their own
  * append break the guarantee: where the append is a launch of its own, the
  * decode after it is a plain launch whatever the flag says.  Results are
  * those of the plain launch.

@@ -483,12 +483,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     atomicOr(p.status, bits);
   };
 
-  // ---- 0. Programmatic dependent launch: let the next kernel in the stream be
-  // scheduled as this grid's CTAs retire, and wait for the previous kernel
-  // (which may write any of the inputs) to complete before touching global
-  // memory; with the early prologue only the consumers wait (below).  Both are
+  // ---- 0. Programmatic dependent launch: wait for the previous kernel (which may
+  // write any of the inputs) to complete before touching global memory, then let
+  // the next kernel in the stream be scheduled as this grid's CTAs retire; with the
+  // early prologue only the consumers wait (below).  In this order the next launch
+  // begins when all work ahead of this one is complete, so what it may find running
+  // is this launch alone: with the early prologue it reads caches without waiting,
+  // and a launch further back may have written them (a cache append).  Both are
   // no-ops for a launch without the programmatic attribute.
-  griddep_launch_dependents();
   // Start the cold fetches that only depend on the arguments: the tensor maps
   // (kernel parameters, safe before the wait; needed by the first tensor copy)
   // and, spread over the grid, the block table (read right after the prefix
@@ -497,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  if (!p.early && !(MOD && p.independent)) griddep_wait();
+  if (!p.early) {
+    if (!(MOD && p.independent)) griddep_wait();
+    griddep_launch_dependents();
+  }
   {
     const size_t bt_bytes = (size_t)N * p.maxb * sizeof(int32_t);
     if (bt_bytes <= kBlockTablePrefetchBytes) {
@@ -790,6 +795,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
   int first_old = -1;    // thread 0: counter value its first piece's arrival saw
   if (p.early) {  // the producer went ahead; q, out and the workspace wait for the previous work
     griddep_wait();
+    griddep_launch_dependents();
     zero_empty(C, ctid, kConsumerThreads);
   }
 

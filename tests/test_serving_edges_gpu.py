@@ -211,3 +211,35 @@ def test_a_nan_token_reaches_those_who_see_it():
     out = pa.paged_attn_decode_multi_mods(q, w.k_cache, w.v_cache, i32([0, 6, 8]), *args[2:],
                                           softcap=5.0)
     assert np.array_equal(nan_rows(out), np.repeat(expect, [6, 2], axis=0))
+
+
+# ---- the early prologue begins when all but the launch just ahead is complete
+@pytest.mark.parametrize("between", ["decode", "mods", "early"])
+def test_early_prologue_two_launches_behind_an_append(between):
+    """An append, a decode of other caches, then with the early prologue a decode that
+    reads the appended rows: it may find the launch just ahead running, not the append."""
+    sp = workloads.custom_spec("chain", 64, 8, 8, 128, 16, [256] * 64)
+    w = workloads.make(sp, device="cuda")
+    other = workloads.make(workloads.custom_spec("other", 1, 8, 8, 128, 16, [20]), device="cuda")
+    bt = w.block_tables.long()
+    t = torch.arange(256, device="cuda")
+    slots = (bt[:, t // 16] * 16 + t % 16).reshape(-1).contiguous()
+
+    def decode(x, fn=pa.paged_attn_decode):
+        return fn(x.q, x.k_cache, x.v_cache, x.block_tables, x.seq_lens, x.scale)
+
+    decode(w), decode(other, pa.paged_attn_decode_mods)
+    for i in range(20):
+        rows = torch.randn(2, slots.numel(), 8, 128, device="cuda").to(torch.bfloat16)
+        torch.cuda.synchronize()
+        try:
+            if between == "early":
+                pa.paged_attn_set_launch_flags(pa.FLAG_EARLY_PROLOGUE)
+            pa.paged_kv_append_slots(rows[0], rows[1], w.k_cache, w.v_cache, slots)
+            decode(other, pa.paged_attn_decode_mods if between == "mods" else pa.paged_attn_decode)
+            pa.paged_attn_set_launch_flags(pa.FLAG_EARLY_PROLOGUE)
+            out = decode(w)
+        finally:
+            pa.paged_attn_set_launch_flags(0)
+        torch.cuda.synchronize()
+        assert torch.equal(out, decode(w)), i
