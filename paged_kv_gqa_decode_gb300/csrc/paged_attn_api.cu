@@ -70,7 +70,7 @@ struct OwnedWorkspace {
   size_t bytes = 0;
 };
 
-// Per-device state, indexed by device ordinal (guarded by g_mu).
+// Per-device state, indexed by device ordinal (guarded by g_mu; g_ws by g_ws_mu).
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DeviceInfo g_info[kMaxDevices];
@@ -592,13 +592,19 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
   return PAGED_ATTN_OK;
 }
 
+// Guards the library-owned workspaces.  A call that uses one holds it until its launches
+// are enqueued: another host thread's larger call releases the buffer in stream order,
+// which must come after them.
+std::mutex g_ws_mu;
+using WorkspaceHold = std::unique_lock<std::mutex>;
+
 // The library-owned workspace of the current device, grown to at least `bytes`.
-int owned_workspace(size_t bytes, cudaStream_t stream, void** out) {
+int owned_workspace(size_t bytes, cudaStream_t stream, void** out, WorkspaceHold* hold) {
   int dev = 0;
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
   cudaError_t e;
-  std::lock_guard<std::mutex> lk(g_mu);
+  *hold = WorkspaceHold(g_ws_mu);
   OwnedWorkspace& w = g_ws[dev];
   if (w.bytes < bytes) {
     if (w.ptr) {
@@ -628,10 +634,10 @@ int owned_workspace(size_t bytes, cudaStream_t stream, void** out) {
 // buffer captured graphs of the other entry points may hold).  A stream being
 // captured must bring its own: a graph must not keep a buffer that a later,
 // larger call releases.
-OwnedWorkspace g_opt_ws[kMaxDevices];  // guarded by g_mu
+OwnedWorkspace g_opt_ws[kMaxDevices];  // guarded by g_ws_mu
 
 int optional_workspace(void* workspace, size_t workspace_bytes, size_t need, cudaStream_t stream,
-                       void** out) {
+                       void** out, WorkspaceHold* hold) {
   if (workspace != nullptr) {
     if ((reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0 || workspace_bytes < need)
       return PAGED_ATTN_ERR_WORKSPACE;
@@ -645,7 +651,7 @@ int optional_workspace(void* workspace, size_t workspace_bytes, size_t need, cud
   int dev = 0;
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
-  std::lock_guard<std::mutex> lk(g_mu);
+  *hold = WorkspaceHold(g_ws_mu);
   OwnedWorkspace& w = g_opt_ws[dev];
   if (w.bytes < need) {
     if (w.ptr) {
@@ -733,7 +739,8 @@ int plan_and_run(Operands& o, int head_dim, int block_size, bool fp8, bool xp, i
                    qchunks);
   if (rc != PAGED_ATTN_OK) return rc;
   pl.xp = xp;  // same shared-memory plan as the bf16 layout
-  if (o.ws == nullptr && (rc = owned_workspace(pl.ws_bytes, st, &o.ws)) != PAGED_ATTN_OK)
+  WorkspaceHold hold;
+  if (o.ws == nullptr && (rc = owned_workspace(pl.ws_bytes, st, &o.ws, &hold)) != PAGED_ATTN_OK)
     return rc;
   return run(pl, o, st);
 }
@@ -766,7 +773,8 @@ int decode_mods_impl(Operands& o, int head_dim, int block_size, bool fp8, void* 
   Plan pl;
   rc = cached_plan(o.num_seqs, o.H_q, o.H_kv, head_dim, block_size, dev, di, &pl, fp8, 0, 0, true);
   if (rc != PAGED_ATTN_OK) return rc;
-  rc = optional_workspace(workspace, workspace_bytes, pl.ws_bytes, st, &o.ws);
+  WorkspaceHold hold;
+  rc = optional_workspace(workspace, workspace_bytes, pl.ws_bytes, st, &o.ws, &hold);
   if (rc != PAGED_ATTN_OK) return rc;
   return run(pl, o, st);
 }
@@ -1058,7 +1066,8 @@ int paged_attn_append_decode(const void* q, const void* k_new, const void* v_new
   Operands o = operands(q, k_cache, v_cache, out, block_tables, seq_lens, num_seqs, H_q, H_kv,
                         max_blocks_per_seq, scale);
   apply_checks(&o);
-  if ((rc = owned_workspace(pl.ws_bytes, st, &o.ws)) != PAGED_ATTN_OK) return rc;
+  WorkspaceHold hold;
+  if ((rc = owned_workspace(pl.ws_bytes, st, &o.ws, &hold)) != PAGED_ATTN_OK) return rc;
   // Fused, the warp that reads a piece's last page patches the new rows into it,
   // a small cost per piece on that CTA's path.  When CTAs average kAppendApartPieces
   // or more (s, g) pieces, the CTA crossing the most short sequences sets the
@@ -1196,7 +1205,8 @@ int paged_attn_append_decode_fp8(const void* q, const void* k_new, const void* v
   o.k_scale = k_scale;
   o.v_scale = v_scale;
   apply_checks(&o);
-  if ((rc = owned_workspace(pl.ws_bytes, st, &o.ws)) != PAGED_ATTN_OK) return rc;
+  WorkspaceHold hold;
+  if ((rc = owned_workspace(pl.ws_bytes, st, &o.ws, &hold)) != PAGED_ATTN_OK) return rc;
   // As for bf16 caches: fused (each piece's last page quantized and patched in
   // shared memory, then stored) unless CTAs average kAppendApartPieces or more
   // pieces, when the append runs as its own launch and the decode after it is
@@ -1318,7 +1328,8 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   t.single = t.splits == 1 ? 1 : 0;
   const size_t parts = t.single ? 0 : tile_part_bytes(head_dim, total_q, H_q, t.splits);
   void* ws = nullptr;
-  rc = optional_workspace(workspace, workspace_bytes, counters_end(di) + parts, st, &ws);
+  WorkspaceHold hold;
+  rc = optional_workspace(workspace, workspace_bytes, counters_end(di) + parts, st, &ws, &hold);
   if (rc != PAGED_ATTN_OK) return rc;
   t.status = g_check_blocks > 0 ? g_check_status : static_cast<int32_t*>(ws);
   if (!t.single) set_parts(&t, static_cast<uint8_t*>(ws) + counters_end(di));
@@ -1426,7 +1437,8 @@ int paged_attn_decode_shared(const void* q, const void* k_cache, const void* v_c
   DeviceInfo di;
   if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  rc = optional_workspace(workspace, workspace_bytes, sp.bytes, st, &o.ws);
+  WorkspaceHold hold;
+  rc = optional_workspace(workspace, workspace_bytes, sp.bytes, st, &o.ws, &hold);
   if (rc != PAGED_ATTN_OK) return rc;
   apply_checks(&o);
   uint8_t* base = static_cast<uint8_t*>(o.ws);
@@ -1683,7 +1695,7 @@ int paged_attn_reset_workspace(void* stream) {
   int dev = 0;
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
-  std::lock_guard<std::mutex> lk(g_mu);
+  std::lock_guard<std::mutex> lk(g_ws_mu);
   for (const OwnedWorkspace* w : {&g_ws[dev], &g_opt_ws[dev]}) {
     if (w->ptr == nullptr) continue;
     cudaError_t e = cudaMemsetAsync(w->ptr, 0, w->bytes, static_cast<cudaStream_t>(stream));

@@ -200,3 +200,76 @@ int main() {
   return bad != 0;
 }
 """)
+
+
+# Calls through each entry point that may use a library-owned workspace; `big`: sizes that
+# need a larger one than any call before.  check_live: a launch names a buffer that is
+# allocated at that place in the order of its stream.
+CALLS = r"""
+static int call(int kind, bool big, cudaStream_t st) {
+  void* p = at<void>(256);
+  const int32_t* i = at<int32_t>(256);
+  float* f = at<float>(256);
+  const int n = big ? 400 : 2, H = big ? 32 : 2, D = big ? 256 : 128;
+  switch (kind) {
+    case 0: return paged_attn_decode(p, p, p, p, i, i, n, H, 2, D, 8, 16, 0.1f, st);
+    case 1: return paged_attn_append_decode(p, p, p, p, p, p, i, i, n, H, 2, D, 8, 16, 0.1f, st);
+    case 2: return paged_attn_append_decode_fp8(p, p, p, p, p, f, f, p, i, i, n, H, 2, D, 8, 16, 0.1f, st);
+    case 3: return paged_attn_decode_multi(p, p, p, p, i, i, i, n, 2 * n, 2, H, 2, D, 8, 16, 0.1f, st);
+    case 4: return paged_attn_decode_mods(p, p, p, p, i, i, n, H, 2, D, 8, 16, 0.1f, 0.f, nullptr,
+                                          0, nullptr, nullptr, nullptr, 0, st);
+    case 5: return paged_attn_decode_multi_mods(p, p, p, p, i, i, i, big ? 9 : 1, big ? 60 : 3, H, 2, D,
+                                                8, 16, 0.1f, 1, 0.f, nullptr, 0, nullptr, nullptr,
+                                                nullptr, 0, st);
+    default: return paged_attn_decode_shared(p, p, p, p, i, i, i, 1, 8, i, i, n, H, 2, D, 8, 16, 0.1f,
+                                             0.f, nullptr, nullptr, 0, st);
+  }
+}
+constexpr int kKinds = 7;
+
+static void check_live() {
+  std::map<const void*, bool> live;
+  for (const Event& e : events) {
+    if (e.what == "malloc") live[e.at] = true;
+    else if (e.what == "free") live[e.at] = false;
+    else if (e.at != nullptr && e.what != "zero")
+      CHECK(live[e.at]);
+  }
+}
+"""
+
+
+def test_two_host_threads_on_one_stream(run):
+    """While one thread is between taking the library's workspace and launching, another
+    thread's larger call must not release that buffer ahead of the launch."""
+    run("threads", CALLS + r"""
+int main() {
+  for (int kind = 0; kind < kKinds; ++kind) {
+    std::atomic<bool> entered{false};
+    std::atomic<int> launches{0};
+    const size_t from = events.size();
+    before_launch = [&](const char*) {
+      if (launches++ > 0) return;
+      entered = true;
+      std::unique_lock<std::mutex> lk(ev_mu);  // as long as a release takes to come, if it may
+      ev_cv.wait_for(lk, std::chrono::milliseconds(300), [&] {
+        for (size_t k = from; k < events.size(); ++k)
+          if (events[k].what == "free") return true;
+        return false;
+      });
+    };
+    std::thread a([&] { CHECK(call(kind, false, nullptr) == PAGED_ATTN_OK); });
+    while (!entered) std::this_thread::yield();
+    std::thread b([&] { CHECK(call(kind, true, nullptr) == PAGED_ATTN_OK); });
+    a.join();
+    b.join();
+    check_live();
+    before_launch = nullptr;
+    // (the next kind begins with its small buffer again)
+    for (auto& w : g_ws) w = OwnedWorkspace();
+    for (auto& w : g_opt_ws) w = OwnedWorkspace();
+  }
+  std::printf(bad ? "FAIL\n" : "OK\n");
+  return bad != 0;
+}
+""")
