@@ -454,10 +454,13 @@ PAGED_ATTN_API int paged_attn_append_decode_fp8(const void* q, const void* k_new
  * workspace: at least paged_attn_mods_workspace_bytes(...) bytes, 256-byte
  * aligned, zero-filled before its first use, not shared by calls that may
  * overlap (one workspace serves any calls of the _mods and _shared entry points
- * on a device, in any order); or null, for a workspace the library owns, as
- * paged_attn_decode's (its own one, so calls of the two kinds may overlap).  A stream that is
- * being captured must pass one: with a null workspace the call returns
- * PAGED_ATTN_ERR_WORKSPACE there.  Launch flags do not apply.
+ * on a device, in any order); or null, for a workspace that the library keeps for
+ * the call's stream, apart from paged_attn_decode's: calls on different streams, and
+ * of the two kinds, may overlap.  It is allocated and grown as paged_attn_decode's;
+ * past 64 streams a device the least recently used stream's is given up, after a
+ * cudaDeviceSynchronize.  A stream that is being captured must pass one: with a
+ * null workspace the call returns PAGED_ATTN_ERR_WORKSPACE there.  Launch flags do
+ * not apply.
  */
 PAGED_ATTN_API int paged_attn_decode_mods(const void* q, const void* k_cache,
                                           const void* v_cache, void* out,
@@ -665,8 +668,9 @@ PAGED_ATTN_API const char* paged_attn_status_string(int status);
 PAGED_ATTN_API int paged_attn_set_launch_flags(int flags);
 
 /*
- * Zero-fills the library-owned workspaces of the current device on `stream`
- * (nothing to do when none exists yet).  Needed only after a call reported a
+ * Zero-fills the library-owned workspaces of the current device, those of other
+ * streams too, on `stream` (nothing to do when none exists yet); no call that uses
+ * one may overlap it.  Needed only after a call reported a
  * combine wait that ran out (status bit 2), which can leave split counters set.
  */
 PAGED_ATTN_API int paged_attn_reset_workspace(void* stream);

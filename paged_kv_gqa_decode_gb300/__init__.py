@@ -607,8 +607,9 @@ def paged_attn_decode_mods(q, k_cache, v_cache, block_tables, seq_lens, scale: f
     paged_attn.h): a query at position L - 1 sees token t when t < prefix_lens[s], or
     when t >= doc_starts[s] and t > L - 1 - window (window 0: none), with the score
     softcap * tanh(scale * q.k / softcap) - alibi_slopes[h] * (L - 1 - t).
-    ``workspace``: a zero-initialised uint8 tensor of paged_attn_mods_workspace_bytes,
-    needed while a stream is being captured."""
+    ``workspace``: a zero-initialised uint8 tensor of paged_attn_mods_workspace_bytes for
+    calls that do not overlap, needed while a stream is being captured; without it the
+    library keeps one for each stream."""
     import torch
 
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
@@ -656,7 +657,8 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     """Attention of any number of query tokens per sequence with score options (see
     paged_attn.h): q [total_q, H_q, D], sequence s owning rows qo_indptr[s] ..
     qo_indptr[s+1] - 1 (its last tokens, already in the cache); doc_starts is
-    [total_q], one per query row; the other options as paged_attn_decode_mods."""
+    [total_q], one per query row; the other options as paged_attn_decode_mods
+    (``workspace``: paged_attn_multi_mods_workspace_bytes)."""
     import torch
 
     total_q, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
@@ -687,7 +689,8 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
     """Decode of sequences that share prefixes, each prefix read once (see paged_attn.h):
     sequences group_indptr[g] .. group_indptr[g+1] - 1 begin with the prefix_lens[g]
     tokens of prefix_tables[g] (int32 [num_groups, prefix_max_blocks]); block_tables and
-    seq_lens are those of the sequences' own tokens."""
+    seq_lens are those of the sequences' own tokens.  ``workspace``: as
+    paged_attn_decode_mods, of paged_attn_shared_workspace_bytes."""
     import torch
 
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(

@@ -598,43 +598,84 @@ int run(const Plan& pl, const Operands& o, cudaStream_t stream) {
 std::mutex g_ws_mu;
 using WorkspaceHold = std::unique_lock<std::mutex>;
 
-// The library-owned workspace of the current device, grown to at least `bytes`.
+// Grows a workspace to at least `bytes`, zero-filled.  Earlier calls on this stream may
+// still use the old buffer: it is released in stream order, and the new one is made so
+// (the device's default pool).  No device-wide sync.
+int grow(OwnedWorkspace* w, size_t bytes, cudaStream_t stream) {
+  if (w->bytes >= bytes) return PAGED_ATTN_OK;
+  cudaError_t e;
+  if (w->ptr) {
+    if ((e = cudaFreeAsync(w->ptr, stream)) != cudaSuccess) return cuda_fail(e);
+    *w = OwnedWorkspace();
+  }
+  void* p = nullptr;
+  if ((e = cudaMallocAsync(&p, bytes, stream)) != cudaSuccess) return cuda_fail(e);
+  if ((e = cudaMemsetAsync(p, 0, bytes, stream)) != cudaSuccess) {
+    cudaFreeAsync(p, stream);
+    return cuda_fail(e);
+  }
+  w->ptr = p;
+  w->bytes = bytes;
+  return PAGED_ATTN_OK;
+}
+
+// The library-owned workspace of the current device, grown to at least `bytes` (calls on
+// other streams overlapping this one race on it, as the header says).
 int owned_workspace(size_t bytes, cudaStream_t stream, void** out, WorkspaceHold* hold) {
   int dev = 0;
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
-  cudaError_t e;
   *hold = WorkspaceHold(g_ws_mu);
-  OwnedWorkspace& w = g_ws[dev];
-  if (w.bytes < bytes) {
-    if (w.ptr) {
-      // Earlier calls on this stream may still use the old buffer: free it in
-      // stream order (calls on other streams overlapping this one race on the
-      // shared workspace anyway, as the header says).  No device-wide sync.
-      if ((e = cudaFreeAsync(w.ptr, stream)) != cudaSuccess) return cuda_fail(e);
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    void* p = nullptr;
-    // stream-ordered, like the release of the old one (the device's default pool)
-    if ((e = cudaMallocAsync(&p, bytes, stream)) != cudaSuccess) return cuda_fail(e);
-    if ((e = cudaMemsetAsync(p, 0, bytes, stream)) != cudaSuccess) {
-      cudaFreeAsync(p, stream);
-      return cuda_fail(e);
-    }
-    w.ptr = p;
-    w.bytes = bytes;
-  }
-  *out = w.ptr;
+  if ((rc = grow(&g_ws[dev], bytes, stream)) != PAGED_ATTN_OK) return rc;
+  *out = g_ws[dev].ptr;
   return PAGED_ATTN_OK;
 }
 
-// The workspace of a call that takes an optional one: the caller's, or the
-// library's own for these entry points (kept apart from owned_workspace, whose
-// buffer captured graphs of the other entry points may hold).  A stream being
-// captured must bring its own: a graph must not keep a buffer that a later,
-// larger call releases.
-OwnedWorkspace g_opt_ws[kMaxDevices];  // guarded by g_ws_mu
+// The workspace of a call that takes an optional one: the caller's, or one that the
+// library keeps for the call's stream (apart from owned_workspace, whose buffer captured
+// graphs of the other entry points may hold), so that calls on different streams need
+// nothing of each other.  A stream being captured must bring its own: a graph must not
+// keep a buffer that a later, larger call releases.
+// Streams are told apart by their id, which is never given out twice (a handle may be).
+struct StreamWorkspace {
+  unsigned long long stream;
+  unsigned long long last_use;
+  OwnedWorkspace w;
+};
+constexpr int kStreamWorkspaces = 64;
+struct StreamWorkspaces {
+  int count = 0;
+  unsigned long long uses = 0;
+  StreamWorkspace entry[kStreamWorkspaces];
+};
+StreamWorkspaces g_opt_ws[kMaxDevices];  // guarded by g_ws_mu
+
+// The entry of a stream, made where there is none: past kStreamWorkspaces streams the
+// least recently used one's is taken over, once the device has finished all work.
+int stream_workspace(StreamWorkspaces& all, unsigned long long id, cudaStream_t stream,
+                     OwnedWorkspace** out) {
+  StreamWorkspace* x = nullptr;
+  for (int k = 0; k < all.count && x == nullptr; ++k)
+    if (all.entry[k].stream == id) x = &all.entry[k];
+  if (x == nullptr && all.count < kStreamWorkspaces) {
+    x = &all.entry[all.count++];
+    *x = StreamWorkspace();
+    x->stream = id;
+  }
+  if (x == nullptr) {
+    x = &all.entry[0];
+    for (StreamWorkspace& y : all.entry)
+      if (y.last_use < x->last_use) x = &y;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e == cudaSuccess && x->w.ptr) e = cudaFreeAsync(x->w.ptr, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    *x = StreamWorkspace();
+    x->stream = id;
+  }
+  x->last_use = ++all.uses;
+  *out = &x->w;
+  return PAGED_ATTN_OK;
+}
 
 int optional_workspace(void* workspace, size_t workspace_bytes, size_t need, cudaStream_t stream,
                        void** out, WorkspaceHold* hold) {
@@ -651,24 +692,13 @@ int optional_workspace(void* workspace, size_t workspace_bytes, size_t need, cud
   int dev = 0;
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
+  unsigned long long id = 0;
+  if ((e = cudaStreamGetId(stream, &id)) != cudaSuccess) return cuda_fail(e);
   *hold = WorkspaceHold(g_ws_mu);
-  OwnedWorkspace& w = g_opt_ws[dev];
-  if (w.bytes < need) {
-    if (w.ptr) {
-      if ((e = cudaFreeAsync(w.ptr, stream)) != cudaSuccess) return cuda_fail(e);
-      w.ptr = nullptr;
-      w.bytes = 0;
-    }
-    void* p = nullptr;
-    if ((e = cudaMallocAsync(&p, need, stream)) != cudaSuccess) return cuda_fail(e);
-    if ((e = cudaMemsetAsync(p, 0, need, stream)) != cudaSuccess) {
-      cudaFreeAsync(p, stream);
-      return cuda_fail(e);
-    }
-    w.ptr = p;
-    w.bytes = need;
-  }
-  *out = w.ptr;
+  OwnedWorkspace* w = nullptr;
+  if ((rc = stream_workspace(g_opt_ws[dev], id, stream, &w)) != PAGED_ATTN_OK) return rc;
+  if ((rc = grow(w, need, stream)) != PAGED_ATTN_OK) return rc;
+  *out = w->ptr;
   return PAGED_ATTN_OK;
 }
 
@@ -1696,12 +1726,15 @@ int paged_attn_reset_workspace(void* stream) {
   int rc = current_device(&dev);
   if (rc != PAGED_ATTN_OK) return rc;
   std::lock_guard<std::mutex> lk(g_ws_mu);
-  for (const OwnedWorkspace* w : {&g_ws[dev], &g_opt_ws[dev]}) {
-    if (w->ptr == nullptr) continue;
-    cudaError_t e = cudaMemsetAsync(w->ptr, 0, w->bytes, static_cast<cudaStream_t>(stream));
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
-  return PAGED_ATTN_OK;
+  auto zero = [&](const OwnedWorkspace& w) -> int {
+    if (w.ptr == nullptr) return PAGED_ATTN_OK;
+    cudaError_t e = cudaMemsetAsync(w.ptr, 0, w.bytes, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PAGED_ATTN_OK : cuda_fail(e);
+  };
+  rc = zero(g_ws[dev]);
+  for (int k = 0; k < g_opt_ws[dev].count && rc == PAGED_ATTN_OK; ++k)
+    rc = zero(g_opt_ws[dev].entry[k].w);
+  return rc;
 }
 
 int paged_attn_last_cuda_error(void) { return g_last_cuda_error; }

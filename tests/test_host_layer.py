@@ -267,8 +267,58 @@ int main() {
     before_launch = nullptr;
     // (the next kind begins with its small buffer again)
     for (auto& w : g_ws) w = OwnedWorkspace();
-    for (auto& w : g_opt_ws) w = OwnedWorkspace();
+    for (auto& w : g_opt_ws) w = StreamWorkspaces();
   }
+  std::printf(bad ? "FAIL\n" : "OK\n");
+  return bad != 0;
+}
+""")
+
+
+def test_streams_have_their_own_workspaces(run):
+    """The score-option and shared-prefix calls without a workspace of the caller's: one
+    per stream, kept while its stream needs it, released in its stream's order; past the
+    number the library keeps, only after the device has finished."""
+    run("streams", CALLS + r"""
+int main() {
+  std::map<cudaStream_t, const void*> of;
+  for (int kind = 4; kind < kKinds; ++kind) {
+    for (int round = 0; round < 2; ++round)
+      for (int i = 0; i < 5; ++i) {
+        const size_t from = events.size();
+        CHECK(call(kind, round == 1 && i == 3, stream_of(i)) == PAGED_ATTN_OK);
+        const void* ws = nullptr;
+        for (size_t k = from; k < events.size(); ++k) {
+          const Event& e = events[k];
+          CHECK(e.stream == stream_of(i));
+          if (e.what == "free") CHECK(of[stream_of(i)] == e.at);
+          if (ws == nullptr && e.what != "malloc" && e.what != "zero" && e.what != "free") ws = e.at;
+        }
+        CHECK(ws != nullptr);
+        for (auto& [st, w] : of) CHECK((st == stream_of(i)) || w != ws);
+        of[stream_of(i)] = ws;
+      }
+  }
+  check_live();
+  // as many streams as come: what is taken over is idle
+  for (int i = 5; i < 200; ++i) {
+    const size_t from = events.size();
+    CHECK(call(4, false, stream_of(i)) == PAGED_ATTN_OK);
+    bool synced = false;
+    for (size_t k = from; k < events.size(); ++k) {
+      if (events[k].what == "sync") synced = true;
+      if (events[k].what == "free") CHECK(synced);
+    }
+    CHECK(synced == (i >= kStreamWorkspaces));
+    const size_t again = events.size();
+    CHECK(call(4, false, stream_of(i)) == PAGED_ATTN_OK);
+    CHECK(events.size() == again + 1);  // the launch alone
+  }
+  check_live();
+  // a reset reaches every buffer that is kept
+  const size_t from = events.size();
+  CHECK(paged_attn_reset_workspace(stream_of(1)) == PAGED_ATTN_OK);
+  CHECK(events.size() - from == (size_t)kStreamWorkspaces);
   std::printf(bad ? "FAIL\n" : "OK\n");
   return bad != 0;
 }

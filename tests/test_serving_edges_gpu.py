@@ -243,3 +243,37 @@ def test_early_prologue_two_launches_behind_an_append(between):
             pa.paged_attn_set_launch_flags(0)
         torch.cuda.synchronize()
         assert torch.equal(out, decode(w)), i
+
+
+# ---- the library's own workspaces
+def test_streams_side_by_side_without_workspaces():
+    """Split work of every entry point on several streams at once, and grown buffers."""
+    ws = [workloads.make(workloads.custom_spec("side", 3, 8, 2, 128, 16, lens), seed=i,
+                         device="cuda") for i, lens in enumerate(([9000, 5, 300], [20, 8000, 7000],
+                                                                  [4000, 4000, 4000]))]
+    qo = i32([0, 4, 5, 9])
+
+    def calls(w):
+        g = torch.Generator(device="cuda").manual_seed(w.seed)
+        q = torch.randn(9, 8, 128, generator=g, device="cuda").to(torch.bfloat16)
+        args = (w.k_cache, w.v_cache)
+        rest = (w.block_tables, w.seq_lens, w.scale)
+        lone = (i32([0, 3]), w.block_tables[:1].clone(), w.seq_lens[:1].clone())
+        return [lambda: pa.paged_attn_decode_mods(w.q, *args, *rest, softcap=30.0),
+                lambda: pa.paged_attn_decode_multi_mods(q, *args, qo, *rest),
+                lambda: pa.paged_attn_decode_shared(w.q, *args, *lone, *rest)]
+
+    work = [calls(w) for w in ws]
+    torch.cuda.synchronize()
+    expect = [[c() for c in cs] for cs in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = [[] for _ in work]
+    for i in range(12):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append((work[k][(i + k) % 3](), (i + k) % 3))
+    torch.cuda.synchronize()
+    for k, outs in enumerate(got):
+        for out, which in outs:
+            assert torch.equal(out, expect[k][which])
