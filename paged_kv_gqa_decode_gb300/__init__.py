@@ -546,6 +546,22 @@ def _need(name, t, dtype, shape) -> None:
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
+def _int32(name, x) -> int:
+    """An int argument of the C ABI (whose conversion would drop the upper bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit 32 bits, got {x}")
+    return x
+
+
+def _softcap(x) -> float:
+    """The cap as the C ABI takes it: one below float32's range is not taken for none."""
+    x = float(x)
+    if x != 0.0 and ctypes.c_float(x).value == 0.0:
+        raise ValueError(f"softcap must be 0 or in [1e-30, 1e30], got {x}")
+    return x
+
+
 def _raw_stream(stream, device) -> int:
     """The stream's handle: the one given, or the device's current one."""
     if stream is not None:
@@ -612,13 +628,14 @@ def paged_attn_decode_mods(q, k_cache, v_cache, block_tables, seq_lens, scale: f
     library keeps one for each stream."""
     import torch
 
+    softcap, window = _softcap(softcap), _int32("window", window)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
         workspace, torch.bfloat16)
     _check((_lib or load()).paged_attn_decode_mods(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
-        float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens), _ptr(doc_starts),
+        softcap, _ptr(alibi_slopes), window, _ptr(prefix_lens), _ptr(doc_starts),
         _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
     return out
 
@@ -630,6 +647,7 @@ def paged_attn_decode_fp8_mods(q, k8, v8, k_scale, v_scale, block_tables, seq_le
     """paged_attn_decode_mods over FP8 caches (as paged_attn_decode_fp8; head_dim 128 or 256)."""
     import torch
 
+    softcap, window = _softcap(softcap), _int32("window", window)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k8, v8, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts, workspace,
         torch.uint8)
@@ -639,7 +657,7 @@ def paged_attn_decode_fp8_mods(q, k8, v8, k_scale, v_scale, block_tables, seq_le
     _check((_lib or load()).paged_attn_decode_fp8_mods(
         q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         out.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS,
-        float(scale), float(softcap), _ptr(alibi_slopes), int(window), _ptr(prefix_lens),
+        float(scale), softcap, _ptr(alibi_slopes), window, _ptr(prefix_lens),
         _ptr(doc_starts), _ptr(workspace), _bytes(workspace), _raw_stream(stream, dev)))
     return out
 
@@ -661,6 +679,7 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     (``workspace``: paged_attn_multi_mods_workspace_bytes)."""
     import torch
 
+    softcap, window = _softcap(softcap), _int32("window", window)
     total_q, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
         workspace, torch.bfloat16, rows="many")
@@ -669,8 +688,8 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     _check((_lib or load()).paged_attn_decode_multi_mods(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         qo_indptr.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), n, total_q, H_q, H_kv,
-        D, maxb, BS, float(scale), 1 if causal else 0, float(softcap), _ptr(alibi_slopes),
-        int(window), _ptr(prefix_lens), _ptr(doc_starts), _ptr(workspace), _bytes(workspace),
+        D, maxb, BS, float(scale), 1 if causal else 0, softcap, _ptr(alibi_slopes),
+        window, _ptr(prefix_lens), _ptr(doc_starts), _ptr(workspace), _bytes(workspace),
         _raw_stream(stream, dev)))
     return out
 
@@ -693,6 +712,7 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
     paged_attn_decode_mods, of paged_attn_shared_workspace_bytes."""
     import torch
 
+    softcap = _softcap(softcap)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, None, None, workspace,
         torch.bfloat16)
@@ -707,7 +727,7 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         group_indptr.data_ptr(), prefix_tables.data_ptr(), prefix_lens.data_ptr(), groups, pmax,
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
-        float(softcap), _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace),
+        softcap, _ptr(alibi_slopes), _ptr(workspace), _bytes(workspace),
         _raw_stream(stream, dev)))
     return out
 
@@ -732,6 +752,8 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
     tensor of one element that receives the number of sequences refused."""
     import torch
 
+    block_size, max_new = _int32("block_size", block_size), _int32("max_new", max_new)
+    n_free = _int32("free_blocks' length", free_blocks.numel())
     n = seq_lens.shape[0]
     i32 = torch.int32
     _need("seq_lens", seq_lens, i32, (n,))
@@ -766,7 +788,7 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
         seq_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(),
         free_blocks.data_ptr(), free_count.data_ptr(), seq_lens_out.data_ptr(),
         qo_indptr.data_ptr(), slot_map.data_ptr(), free_count_out.data_ptr(), _ptr(refused), n,
-        block_tables.shape[1], int(block_size), free_blocks.numel(), int(max_new),
+        block_tables.shape[1], block_size, n_free, max_new,
         _raw_stream(stream, dev)))
     return seq_lens_out, qo_indptr, slot_map, free_count_out
 
