@@ -277,3 +277,67 @@ def test_streams_side_by_side_without_workspaces():
     for k, outs in enumerate(got):
         for out, which in outs:
             assert torch.equal(out, expect[k][which])
+
+
+# ---- block ids outside the pool, with checks on: reported, and read as pages of zeros
+def with_checks(num_blocks, call):
+    status = i32([0])
+    pa.paged_attn_set_checks(num_blocks, status)
+    try:
+        out = call()
+        torch.cuda.synchronize()
+    finally:
+        pa.paged_attn_set_checks(0, None)
+    return out, int(status)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_bad_page_is_a_page_of_zeros(D):
+    lens, qlens = [100, 40], [20, 3]
+    w = workloads.make(workloads.custom_spec("bad", 2, 8, 2, D, 16, lens), device="cuda")
+    qo = np.cumsum([0] + qlens)
+    q = torch.randn(23, 8, D, device="cuda").to(torch.bfloat16)
+    bt = w.block_tables.cpu().numpy()
+    scale = float(np.float32(w.scale))
+    bad = w.block_tables.clone()
+    bad[0, 5] = w.num_blocks + 3
+    skipped = w.block_tables.clone()
+    skipped[0, 0] = -9                      # ahead of the window
+    k0, v0 = w.k_cache.clone(), w.v_cache.clone()
+    k0[int(bt[0, 5])] = 0
+    v0[int(bt[0, 5])] = 0
+    for window, tables, k, v, bits in ((0, bad, k0, v0, 1), (60, bad, k0, v0, 1),
+                                       (60, skipped, w.k_cache, w.v_cache, 0)):
+        out, status = with_checks(w.num_blocks, lambda: pa.paged_attn_decode_mods(
+            w.q, w.k_cache, w.v_cache, tables, w.seq_lens, w.scale, window=window))
+        assert status == bits
+        within(out, serving.attend(f64(w.q), f64(k), f64(v), None, bt, lens, scale, window=window))
+        out, status = with_checks(w.num_blocks, lambda: pa.paged_attn_decode_multi_mods(
+            q, w.k_cache, w.v_cache, i32(qo), tables, w.seq_lens, w.scale, window=window))
+        assert status == bits
+        within(out, serving.attend(f64(q), f64(k), f64(v), qo, bt, lens, scale, window=window))
+    # a prefix's page
+    out, status = with_checks(w.num_blocks, lambda: pa.paged_attn_decode_shared(
+        w.q[1:].contiguous(), w.k_cache, w.v_cache, i32([0, 1]), bad[:1].clone(), i32([100]),
+        w.block_tables[1:].clone(), i32([40]), w.scale))
+    assert status == 1
+    within(out, serving.attend_shared(f64(w.q[1:]), f64(k0), f64(v0), [0, 1], bt[:1], [100], bt[1:],
+                                      [40], scale))
+
+
+def test_a_bad_fp8_page_is_a_page_of_zeros():
+    lens = [100, 40]
+    w = workloads.make(workloads.custom_spec("bad8", 2, 8, 2, 128, 16, lens), device="cuda")
+    f = workloads.to_fp8(w)
+    bt = w.block_tables.cpu().numpy()
+    bad = w.block_tables.clone()
+    bad[0, 5] = w.num_blocks + 3
+    out, status = with_checks(w.num_blocks, lambda: pa.paged_attn_decode_fp8_mods(
+        w.q, f.k8, f.v8, f.k_scale, f.v_scale, bad, w.seq_lens, w.scale))
+    assert status == 1
+    k = f.k8.view(torch.float8_e4m3fn).double() * f.k_scale.double()[..., None]
+    v = f.v8.view(torch.float8_e4m3fn).double() * f.v_scale.double()[..., None]
+    k[int(bt[0, 5])] = 0
+    v[int(bt[0, 5])] = 0
+    within(out, serving.attend(f64(w.q), k.cpu().numpy(), v.cpu().numpy(), None, bt, lens,
+                               float(np.float32(w.scale)), eps_p=serving.F16_STEP, f16=True))
