@@ -501,11 +501,18 @@ PAGED_ATTN_API size_t paged_attn_mods_workspace_bytes(int num_seqs, int H_q, int
  * with the scores of paged_attn_decode_mods, |pos - t'| the distance of the
  * bias.  q, out, qo_indptr and total_q as paged_attn_decode_multi, except that
  * doc_starts is [total_q] (one per row) and there is no max_q_len.  Rows that
- * see no token are zero; rows of q no sequence owns are not written.  Tiles of
- * 128 tokens (64 for head_dim 256) that no row of a 256-row (128-row) piece
- * sees are not read, and cache rows that no query of the sequence sees may
- * hold anything, NaN included; a cache row that only some of a sequence's
- * queries see must be finite for the others' sake.
+ * see no token are zero; rows of q no sequence owns are not written.
+ *
+ * Without causality (is_causal = 0) the window and the document bound a query's view
+ * on the left only: it sees everything from there to the sequence's end, later
+ * documents included.  A bidirectional document mask over a packed sequence
+ * is therefore not among these options.
+ *
+ * The query rows of a KV head are worked on in pieces of consecutive rows (up to 128 or
+ * 256, as a call's sizes have it).  Pages ahead of all that a piece's rows see (its
+ * prefix aside) and behind it are not read, nor their table entries.  Cache rows
+ * that no query of the sequence sees may hold anything, NaN included; a cache row that
+ * only some of a sequence's queries see must be finite for the others' sake.
  *
  * The products run on the 5th-generation tensor cores (bf16 operands, the
  * weights rounded to bf16, fp32 accumulation).  workspace: as

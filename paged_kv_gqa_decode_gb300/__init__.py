@@ -675,7 +675,8 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     """Attention of any number of query tokens per sequence with score options (see
     paged_attn.h): q [total_q, H_q, D], sequence s owning rows qo_indptr[s] ..
     qo_indptr[s+1] - 1 (its last tokens, already in the cache); doc_starts is
-    [total_q], one per query row; the other options as paged_attn_decode_mods
+    [total_q], one per query row; with ``causal=False`` a window or a document bounds the
+    view on the left only, later documents are seen; the other options as paged_attn_decode_mods
     (``workspace``: paged_attn_multi_mods_workspace_bytes)."""
     import torch
 

@@ -15,9 +15,9 @@
 // Every CTA scans all the lengths into per-thread sums in shared memory and fills
 // its part of the slot map from them.  When the new lengths or the free count go
 // over the old ones, all those reads have to come before the writes: the grid is
-// then one thread-block cluster (a single CTA for a decode step, eight for prompts),
-// whose barrier separates them without a workspace; else it is as large as the
-// rows ask for.
+// then one thread-block cluster (of one, two, four or eight CTAs by the rows there may
+// be, one up to 4096), whose barrier separates them without a workspace; else it is as
+// large as the rows ask for, up to 128 CTAs.
 #include "assign.h"
 
 namespace pagedattn {

@@ -934,8 +934,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, G16, BS, KV == kKvFp8
     return valid < BS || (MOD && tb < mod_lo && tb + BS > mod_pre);
   };
   // Score of token t (log2 domain) from the dot product, for slope `slope`.  The
-  // cap: the series where every score of the warp is small next to the cap,
-  // which is the ordinary case and costs no MUFU operation.
+  // cap: the series where every score of the warp is small next to the cap, which costs
+  // no MUFU operation; else both forms (scores of deviation 50 under a cap of 50 in a window
+  // of 1024 tokens 29.7 us, of deviation 1 29.3: memory bounds both).
   auto mod_score = [&](float dot, float factor, int t, float slope) -> float {
     float x;
     if (p.cap_log2 > 0.f) {

@@ -821,14 +821,13 @@ long long tile_bound(int total_q, int num_seqs, int G, int teams) {
 // for CTAs (two on an SM for the one-team kernels of head_dim 64 and 128), else as many as
 // make 1.75 CTAs a place, so that the longest parts end near the others (fewer
 // leave SMs idle behind a long sequence, more pay each CTA's 4 us of start and end:
-// verification of five tokens, 272 pieces, 1 / 2 / 3 / 6 parts 100 / 81 / 78 / 87 us;
-// 64 chats over three prompts, 40 pieces, one pass after the other, 4 / 8 / 12 / 24
-// parts 64 / 58 / 56 / 69 us; where pieces fill the places parts only cost: a chunk of
-// 1200 tokens, 160 pieces, 1 / 2 / 3 parts 88 / 118 / 140 us, two head_dim 256 chunks,
-// 156 pieces, 134 / 143 / 170 us).
+// verification of five tokens, 272 pieces, 1 / 2 / 3 / 6 parts 64 / 51 / 57 / 75 us;
+// where pieces fill the places parts only cost: a chunk of 1200 tokens, 160 pieces,
+// 1 / 2 / 3 parts 70 / 102 / 124 us, two head_dim 256 chunks, 156 pieces, 127 / 140 /
+// 167 us).
 // `beside`: another launch runs at the same time (shared prefixes: the sequences'
-// own tokens), for which SMs are left: 1.25 CTAs an SM (the same 40 pieces 4 / 5 / 6 /
-// 12 parts 47.9 / 46.8 / 47.5 / 52.7 us).
+// own tokens), for which SMs are left: 1.25 CTAs an SM (64 chats over three prompts, 40
+// pieces, 2 / 3 / 4 / 5 / 6 / 8 / 12 parts 71 / 55 / 46 / 47.5 / 51 / 47 / 45.6 us).
 // The part count bounds what the kernel uses (it never makes parts of fewer than
 // two tiles).  num_seqs > 0, so there is at least one piece.
 int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,

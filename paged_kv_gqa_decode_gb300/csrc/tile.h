@@ -13,9 +13,13 @@ namespace pagedattn {
 // Softmax teams of a CTA, each with a tile of 128 query rows.  Two for head_dim 64
 // and 128, where a sequence has more than 128 rows for a KV head on average and the
 // pieces of 256 rows fill the SMs (a K/V tile then serves both: four capped prompt
-// chunks 552 us, 594 with one); else one, in CTAs of which two run on an SM (64, 128),
-// as their starts and ends then overlap (chunks of 40 to 64 tokens 57 us, 71 with two);
-// one for 256, whose accumulators take half the tensor memory.
+// chunks 476 us, 543 with one; plain 401 / 450; of head_dim 64 441 / 478 and 334 /
+// 367); else one, in CTAs of which two run on an SM (64, 128), as their starts and ends
+// then overlap (eight chunks of 40 to 64 tokens 41.9 us, 46.8 with two; verification of
+// five tokens 50.3 / 56.6); one for 256, whose accumulators take half the tensor memory.
+// (Just past the border two teams are not yet the better choice: twelve chunks of 40 to
+// 64 tokens 64.1 us, 50.3 with one, eight of 200 to 400 tokens 95.0 / 88.5; at 500 tokens
+// it is 194.8 / 206.)
 constexpr int tile_teams(int D, long long total_rows, long long num_seqs, int H_kv, int sms) {
   return D < 256 && total_rows > 128 * num_seqs &&
                  (total_rows / 256 + num_seqs) * H_kv >= sms

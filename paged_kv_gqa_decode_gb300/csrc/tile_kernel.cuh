@@ -24,10 +24,12 @@
 // on an SM, while the accumulators of 256 take half the tensor memory.
 //
 // What bounds it.  On four prompt chunks (1500 to 2048 tokens each before up to 8192,
-// window 4096, 32 query and 8 KV heads of 128, 472 GFLOP) it takes 482 us with capped
-// scores and 400 without, 979 and 1180 TFLOP/s (0.51 and 0.61 of the measured peak):
+// window 4096, 32 query and 8 KV heads of 128, 472 GFLOP) it takes 476 us with capped
+// scores and 401 without, 992 and 1177 TFLOP/s (0.51 and 0.61 of the measured peak):
 // a team's weights and its products follow each other, since its one score buffer
-// holds both, and the other team's products fill half of that.  For 64 tokens of
+// holds both, and the other team's products fill half of that.  Capped scores that come
+// near the cap (deviation 4 and more under a cap of 50) take 870 to 900 us, the slow form
+// of cap_score below.  For 64 tokens of
 // head_dim 128 the two products take 620 cycles back to back; what keeps them apart is
 // latency, of the tensor-memory loads, of the barrier operations behind the other
 // warps' arithmetic, and of the 4 cycles a warp's 32 exponentials take.
@@ -37,8 +39,8 @@
 // for the product, as relative accuracy is what counts there, and summed in fp32.
 //
 // Masks: a query at position pos sees [lo, hi] and the prefix [0, pre).  Token
-// tiles that no row of the piece sees are not walked, their pages not read; in
-// the few tiles where an interval ends the scores are selected, and V rows that no
+// tiles outside the prefix and the hull of the rows' intervals are not walked, pages
+// outside them not read; in the few tiles where an interval ends the scores are selected, and V rows that no
 // row of the piece sees, which may hold anything, are zeroed in shared memory
 // before the product.  Those are the rows outside the hull of the rows' intervals and, where
 // a row sees nothing, its own token if no later row sees it.
@@ -56,7 +58,8 @@ constexpr int kTileStatusBadBlock = 1, kTileStatusBadLength = 2, kTileStatusTime
               kTileStatusConfig = 8;
 constexpr float kTileLazyMax = 8.f;
 // Batches up to this many sequences start with the longest ones (a loop over all of
-// them in every CTA): verification of five tokens, 512 to 4096 tokens, 71 -> 52 us.
+// them in every CTA): verification of five tokens, 32 sequences of 512 to 4096 tokens,
+// 67.5 -> 50.5 us, two head_dim 256 chunks 185 -> 127.
 constexpr int kRankedSeqs = 128;
 
 template <int D, int TEAMS>
@@ -110,8 +113,9 @@ __device__ __forceinline__ uint32_t bits_from(long long n) {
 }
 
 // cap tanh(s c) - m for raw scores s, c = scale / cap, as the weights' exponent:
-// where |s c| < kTanhSeries for every score of the warp, which is the ordinary
-// case, from a polynomial with the powers of c and the cap folded into its
+// where |s c| < kTanhSeries for every score of the warp (2048 of them, or 1024: under a
+// cap of 50 nearly all tiles of scores of deviation 1 or 2, hardly one of deviation 4)
+// from a polynomial with the powers of c and the cap folded into its
 // coefficients, s (a0 + s^2 (a1 + s^2 a2)): four operations a score with the
 // subtraction, and no MUFU operation.  tanh(y) / y = 1 - z / 3 + 2 z^2 / 15 -
 // 17 z^3 / 315 + ..., z = y^2; on [0, h], h = kTanhSeries^2, z^3 differs by h^3 / 32 at
@@ -132,6 +136,9 @@ __device__ __forceinline__ CapSeries cap_series(float c, float cap_log2) {
   t.reach = isfinite(t.a2) ? kTanhSeries / c : 0.f;  // (c > 0)
   return t;
 }
+// Any score: both forms and a selection, three MUFU operations a score in place of one
+// with the weight's.  Four capped prompt chunks of scores of deviation 1 / 2 / 4 / 10 / 50,
+// cap 50: 476 / 482 / 879 / 896 / 870 us.
 __device__ __forceinline__ float cap_score(float s, float c, float cap_log2) {
   const float y = s * c;
   return cap_log2 * (fabsf(y) < kTanhSeries ? tanh_series(y) : tanh_exp(y));
