@@ -125,6 +125,16 @@ def test_hidden_tokens_of_a_range_in_parts():
     check_documents([9001], [40], 2, 1, 256, 32, docs, 7, window=5000)
 
 
+@pytest.mark.parametrize("H_q,H_kv", [(2, 1), (32, 16)])
+def test_hidden_tokens_of_many_sequences(H_q, H_kv):
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 120, size=300)
+    qlens = np.minimum(rng.integers(0, 60, size=300), lens)
+    docs = np.concatenate([np.where(rng.random(m) < 0.5, n, np.maximum(0, n - m + np.arange(m) - 2))
+                           for n, m in zip(lens, qlens)])
+    assert check_documents(list(lens), list(qlens), H_q, H_kv, 64, 16, docs, 8) > 100
+
+
 # ---- a NaN in a query or in a token that it sees reaches the output, however the work is cut
 def nan_rows(out):
     """[rows, heads]: all NaN or all finite, true for NaN."""
@@ -192,10 +202,14 @@ def test_a_nan_query_over_a_shared_prefix(D, own):
     w.q[3] = float("nan")
     expect = np.zeros((4, 8), dtype=bool)
     expect[1, 2] = expect[3] = True
-    out = pa.paged_attn_decode_shared(w.q[:4].contiguous(), w.k_cache, w.v_cache, i32([0, 4]),
-                                      w.block_tables[4:].clone(), i32([5000]),
-                                      w.block_tables[:4].clone(), i32(own), w.scale)
-    assert np.array_equal(nan_rows(out), expect)
+    for members in (4, 2):  # the others have no prefix
+        out = pa.paged_attn_decode_shared(w.q[:4].contiguous(), w.k_cache, w.v_cache,
+                                          i32([0, members]), w.block_tables[4:].clone(),
+                                          i32([5000]), w.block_tables[:4].clone(), i32(own),
+                                          w.scale)
+        if members == 2:
+            expect[3] = own[3] > 0  # without a token a zero row
+        assert np.array_equal(nan_rows(out), expect)
 
 
 def test_a_nan_token_reaches_those_who_see_it():
