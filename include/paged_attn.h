@@ -83,6 +83,7 @@ extern "C" {
 #define PAGED_ATTN_ERR_STATIC_SCRATCH (-9) /* sizes exceed paged_attn_decode_static's scratch */
 #define PAGED_ATTN_ERR_FLAGS (-10)     /* unknown bits in paged_attn_set_launch_flags */
 #define PAGED_ATTN_ERR_MODS (-11)      /* softcap not 0 and outside [1e-30, 1e30] (or scale / softcap past 1e30), or window < 0 */
+#define PAGED_ATTN_ERR_ROPE (-12)      /* rotary_dim, num_axes, max_positions or eps out of range */
 
 /* Launch flags (paged_attn_set_launch_flags). */
 #define PAGED_ATTN_FLAG_EARLY_PROLOGUE 1
@@ -532,6 +533,41 @@ PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int to
                                                             int block_size);
 
 /*
+ * Attention of a tree of drafted tokens (speculative decoding with several
+ * continuations at once): sequence s owns the rows t = qo_indptr[s] + i, its last q_len =
+ * qo_indptr[s+1] - qo_indptr[s] tokens, which are already in the cache, and ctx =
+ * seq_lens[s] - q_len tokens stand before the tree.  Row i sees
+ *
+ *       the cached tokens t' < ctx  with  t' < prefix_lens[s]  or
+ *                                         (window == 0 or t' > pos - window)
+ *       the drafted token j of its sequence (token ctx + j) where bit j % 32 of
+ *       tree_mask[t, j / 32] is set
+ *
+ * and stands at pos = ctx + n - 1, n the drafted tokens it sees: in a tree, whose nodes see
+ * themselves and their ancestors, as deep as the node is.  The scores are those of
+ * paged_attn_decode_mods; the distance of the bias is |pos - t'| for a cached token and
+ * the difference of the two rows' positions for a drafted one.  A mask without bits
+ * leaves the cached tokens (a padding node; pos = ctx - 1); a row that sees nothing is zero.
+ *
+ *   tree_mask   [total_q, mask_words]  int32 (read; 16-byte aligned): any bits, those
+ *               from q_len on are not used
+ *   mask_words  1 .. 8: a drafted token from 32 * mask_words on has no bit and is seen by no
+ *               row (with paged_attn_set_checks on, it sets bit 1 of the status word)
+ *
+ * Cache rows that no row sees, those of padding nodes too, may hold anything, NaN
+ * included; a row that only some of a sequence's rows see must be finite for the others'
+ * sake.  Everything else, workspace and its size too, as paged_attn_decode_multi_mods.
+ * Returns PAGED_ATTN_ERR_SIZES for mask_words out of range.
+ */
+PAGED_ATTN_API int paged_attn_decode_tree(
+    const void* q, const void* k_cache, const void* v_cache, void* out,
+    const int32_t* qo_indptr, const int32_t* tree_mask, int mask_words,
+    const int32_t* block_tables, const int32_t* seq_lens, int num_seqs, int total_q, int H_q,
+    int H_kv, int head_dim, int max_blocks_per_seq, int block_size, float scale, float softcap,
+    const float* alibi_slopes, int window, const int32_t* prefix_lens, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/*
  * Decode of a batch whose sequences share long prefixes (system prompts, a
  * document that many questions are about), each prefix read once for all its
  * sequences.  Sequences group_indptr[g] .. group_indptr[g+1] - 1 form group g
@@ -641,6 +677,151 @@ PAGED_ATTN_API int paged_kv_append_slots(const void* k_new, const void* v_new,
                                          void* v_cache, const int64_t* slot_map, int rows,
                                          int H_kv, int head_dim, int block_size,
                                          long long num_blocks, void* stream);
+
+/*
+ * What comes between a layer's projection and its attention, in one pass: the norm of
+ * each query and key head, their rotation by position, and the append of the K and V rows
+ * by slot.  For row r and every head, in float32 up to the one rounding at the end:
+ *
+ *   y = x / sqrt(mean_d(x[d]^2) + eps) * norm[d]      (norm null: y = x)
+ *   for the pairs i < rotary_dim / 2, (a, b) = (i, i + rotary_dim / 2), or (2i, 2i + 1)
+ *   with interleaved != 0, p = positions[axis(i), r]:
+ *     z[a] = y[a] cos_sin[p, i] - y[b] cos_sin[p, rotary_dim / 2 + i]
+ *     z[b] = y[b] cos_sin[p, i] + y[a] cos_sin[p, rotary_dim / 2 + i]
+ *   z[d] = y[d]  for d >= rotary_dim
+ *
+ *   q_out[r, h, :] = bf16(z of q[r, h, :])
+ *   the cache rows at slot_map[r], as paged_kv_append_slots: bf16(z of k_new[r, g, :]) and
+ *   v_new[r, g, :]; with k_scale and v_scale the caches are FP8 and z and v_new are
+ *   quantized as paged_kv_append_fp8 does (z from its float32 values)
+ *
+ *   q, k_new, v_new  rows at their strides as paged_kv_append_slots (slices of one fused
+ *                 projection need no copy)
+ *   q_out         [rows, H_q, head_dim]  bf16 (written); may be q where q_stride = H_q *
+ *                 head_dim, else apart from all inputs
+ *   k_scale, v_scale  [num_blocks, H_kv, block_size]  float32 (written), or both null; with
+ *                 them head_dim is 128 or 256
+ *   slot_map      [rows]  int64.  A slot outside [0, num_blocks * block_size) writes no K
+ *                 and V (-1: a padding row); q_out is written all the same
+ *   positions     [num_axes, rows]  int32, clamped to [0, max_positions).  One axis for
+ *                 text; time, height and width for images and video
+ *   freq_axis     [rotary_dim / 2]  int32, 16-byte aligned: the axis of each pair, clamped
+ *                 to [0, num_axes), or null (axis 0)
+ *   cos_sin       [max_positions, rotary_dim]  float32: cosines, then sines, of each
+ *                 position's angles (any frequencies, any scaling of them)
+ *   q_norm, k_norm  [head_dim]  float32, or null
+ *
+ * rotary_dim is a multiple of 16 up to head_dim, or 0 (no rotation; positions and
+ * cos_sin may be null then).  PAGED_ATTN_ERR_ROPE for other values, for num_axes or
+ * max_positions below 1 and for an eps that is negative or not finite.  The slots of a
+ * call must be distinct.  With paged_attn_set_checks on, a slot past the pool sets bit 0 of
+ * the status word and a position outside the table bit 1.  Strides, other sizes and
+ * errors as paged_kv_append_slots.  One launch; asynchronous; allocates nothing.
+ */
+PAGED_ATTN_API int paged_kv_rope_append_slots(
+    const void* q, const void* k_new, const void* v_new, long long q_stride, long long k_stride,
+    long long v_stride, void* q_out, void* k_cache, void* v_cache, float* k_scale,
+    float* v_scale, const int64_t* slot_map, const int32_t* positions, int num_axes,
+    const int32_t* freq_axis, const float* cos_sin, int max_positions, int rotary_dim,
+    int interleaved, const float* q_norm, const float* k_norm, float eps, int rows, int H_q,
+    int H_kv, int head_dim, int block_size, long long num_blocks, void* stream);
+
+/*
+ * After the verification of drafted tokens: the rows of the accepted ones move together.
+ * The tree of sequence s are its last q_len tokens, ctx = seq_lens[s] - q_len stand before
+ * it (as paged_attn_decode_tree), and for every KV head, K and V (and the row floats of
+ * FP8 caches, with k_scale and v_scale not null):
+ *
+ *   row of token ctx + i  =  old row of token ctx + accepted[s, i]     i < n
+ *   seq_lens_out[s] = ctx + n
+ *
+ *   accepted      [num_seqs, max_accept]  int32 (read): drafted tokens in rising order,
+ *                 padded with -1.  n is the place of the first entry that is not past
+ *                 the one before it or not below q_len (max_accept where there is none)
+ *   seq_lens_out  [num_seqs]  int32 (written), not seq_lens: paged_kv_release takes both to
+ *                 give back the pages behind
+ *
+ * The cache rows behind the new length keep what they hold.  No block with tokens of a tree
+ * may be in two sequences.  Block ids outside [0, num_blocks) move nothing (bit 0 of the
+ * status word with checks on).  Sizes and errors as paged_kv_append_slots (PAGED_ATTN_ERR_SIZES
+ * for max_accept outside [0, 2^30]).  One launch; asynchronous; allocates nothing.
+ */
+PAGED_ATTN_API int paged_kv_compact(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                    const int32_t* qo_indptr, const int32_t* accepted,
+                                    const int32_t* block_tables, const int32_t* seq_lens,
+                                    int32_t* seq_lens_out, int num_seqs, int max_accept, int H_kv,
+                                    int head_dim, int max_blocks_per_seq, int block_size,
+                                    long long num_blocks, void* stream);
+
+/*
+ * Sequences that continue another one (parallel samples, beams): table row children[i]
+ * takes over the tokens of table row parents[i].  Whole pages are shared, a partly filled
+ * last page is copied to a fresh block, so that both may append:
+ *
+ *   L = seq_lens[parents[i]], full = L / block_size
+ *   block_tables[children[i], j] = block_tables[parents[i], j]  and its block_refs + 1,  j < full
+ *   L % block_size > 0:  block_tables[children[i], full] = free_blocks[free_count - 1 - k], to
+ *       which the rows of the L % block_size tokens are copied (K, V and FP8 row floats),
+ *       k counting the forks before i with such a page
+ *   seq_lens[children[i]] = L
+ *
+ *   block_tables  [num_rows, max_blocks_per_seq]  int32: the children's entries are written
+ *   seq_lens      [num_rows]  int32: the children's are written
+ *   parents, children  [num_forks]  int32.  The children of a call are distinct and none is
+ *                 a parent of it; a parent may have any number of them
+ *   block_refs    [num_blocks]  int32: the table rows that hold a block, less one (zero for
+ *                 blocks fresh from paged_kv_assign and for free ones); paged_kv_release
+ *                 counts it down
+ *   free_blocks, free_count, free_count_out  as paged_kv_assign (free_count_out may be free_count,
+ *                 at the cost of a second launch)
+ *   refused       [1]  int32, or null: forks refused
+ *
+ * A fork is refused, its child left empty, when its block is not in the free stack or
+ * a row is outside [0, num_rows).  With checks on, a block id outside [0, num_blocks) sets
+ * bit 0 of the status word (it is handed on, not copied), an invalid row or length bit 1.
+ * k_scale, v_scale, sizes and errors as paged_kv_compact.  Asynchronous; allocates nothing.
+ */
+PAGED_ATTN_API int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                 int32_t* block_tables, int32_t* seq_lens,
+                                 const int32_t* parents, const int32_t* children,
+                                 int32_t* block_refs, const int32_t* free_blocks,
+                                 const int32_t* free_count, int32_t* free_count_out,
+                                 int32_t* refused, int num_forks, int num_rows, int H_kv,
+                                 int head_dim, int max_blocks_per_seq, int block_size,
+                                 int free_capacity, long long num_blocks, void* stream);
+
+/*
+ * Pages given back: sequence s keeps its first keep_lens[s] tokens (0: it has ended).  The
+ * table entries past the page of the last kept token, up to the page of token seq_lens[s] -
+ * 1, lose a holder, in the order of the sequences and of their pages:
+ *
+ *   block_refs[b] > 0 still counts other holders: it falls by one
+ *   else the block is free: free_blocks[free_count + k] = b, k counting the blocks freed
+ *   before it; a block that several entries of the call hold is freed once, in the place of
+ *   the first of them, when all its holders are among them
+ *   seq_lens_out[s] = min(keep_lens[s], seq_lens[s])
+ *
+ *   keep_lens     [num_seqs]  int32 (read), clamped to [0, seq_lens[s]]
+ *   block_refs    [num_blocks]  int32 as paged_kv_fork, or null: no block is shared (num_blocks is
+ *                 not used then)
+ *   free_blocks   [free_capacity]  int32: written past the old count.  Room for the whole
+ *                 pool is enough; a block that finds none is lost (bit 1 of the status word)
+ *   free_count    [1] int32; free_count_out [1] int32 may be free_count
+ *   seq_lens_out  [num_seqs]  may be seq_lens or keep_lens
+ *
+ * The table entries keep their values.  Entries outside [0, num_blocks) (without
+ * block_refs: below 0) are passed over (bit 0 with checks on).  The result does not depend
+ * on the order in which the GPU works.  num_seqs * max_blocks_per_seq below 2^31
+ * (PAGED_ATTN_ERR_SIZES); other sizes, pointers and errors as paged_kv_assign.  One launch; no
+ * workspace; asynchronous on `stream`.
+ */
+PAGED_ATTN_API int paged_kv_release(const int32_t* block_tables, const int32_t* seq_lens,
+                                    const int32_t* keep_lens, int32_t* block_refs,
+                                    long long num_blocks, int32_t* free_blocks,
+                                    const int32_t* free_count, int32_t* seq_lens_out,
+                                    int32_t* free_count_out, int num_seqs,
+                                    int max_blocks_per_seq, int block_size, int free_capacity,
+                                    void* stream);
 
 /* Human-readable text for a PAGED_ATTN_* code (static storage). */
 PAGED_ATTN_API const char* paged_attn_status_string(int status);

@@ -41,13 +41,15 @@ def rows_of(cache, table, n):
     return pages.transpose(0, 2, 1, 3).reshape(-1, cache.shape[1], cache.shape[3])[:n]
 
 
-def _sequence(q, K, V, pos, seen, scale, softcap, slopes, eps_p, f16):
-    """One sequence: q [r, H_q, D], K, V [n, H_kv, D], pos [r], seen [r, n]."""
+def _sequence(q, K, V, pos, seen, scale, softcap, slopes, eps_p, f16, at=None):
+    """One sequence: q [r, H_q, D], K, V [n, H_kv, D], pos [r], seen [r, n]; at [n]: the tokens'
+    positions (None: 0, 1, ...)."""
     r, H, D = q.shape
     G = H // K.shape[1]
     out, tol = np.zeros((r, H, D)), np.zeros((r, H, D))
     some = seen.any(axis=0)  # rows nobody sees may hold anything: they take no part
     K, V, seen, t = K[some], V[some], seen[:, some], np.nonzero(some)[0]
+    t = t if at is None else np.asarray(at)[t]
     dist = np.abs(pos[:, None] - t[None, :])
     for h in range(H):
         k, v = K[:, h // G], V[:, h // G]

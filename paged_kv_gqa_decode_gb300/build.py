@@ -26,7 +26,9 @@ SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d64.cu", "deco
            "decode_xp_d128.cu", "decode_xp_d256.cu", "decode_multi_d64.cu",
            "decode_multi_d128.cu", "decode_multi_d256.cu", "decode_mod_d64.cu",
            "decode_mod_d128.cu", "decode_mod_d256.cu", "decode_fp8_mod_d128.cu",
-           "decode_fp8_mod_d256.cu", "tile_d64.cu", "tile_d128.cu", "tile_d256.cu", "merge.cu"]
+           "decode_fp8_mod_d256.cu", "tile_d64.cu", "tile_d128.cu", "tile_d256.cu",
+           "tile_tree_d64.cu", "tile_tree_d128.cu", "tile_tree_d256.cu", "merge.cu", "pages_api.cu",
+           "rope.cu", "pages.cu"]
 
 
 def nvcc() -> str:
@@ -101,7 +103,8 @@ def build(verbose: bool = False, force: bool = False) -> str:
 # a wait run out (a ring slot left without its copy, a combiner waiting for one
 # more published part than exists).  Never loaded by the product path.
 WAIT_TEST_LIB = os.path.join(LIB_DIR, "libpaged_kv_gqa_decode_waittest.so")
-WAIT_TEST_SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d128.cu"]
+WAIT_TEST_SOURCES = ["paged_attn_api.cu", "append.cu", "assign.cu", "decode_d128.cu",
+                     "pages_api.cu", "rope.cu", "pages.cu"]
 WAIT_TEST_DEFINES = ["-DPAGED_ATTN_WAIT_TEST", "-DPAGED_ATTN_MBAR_SLEEPS=(1u<<14)",
                      "-DPAGED_ATTN_PUBLISH_POLLS=(1u<<15)"]
 

@@ -10,6 +10,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "api_common.h"
 #include "append.h"
 #include "assign.h"
 #include "launch.h"
@@ -914,6 +915,34 @@ void set_parts(TileParams* t, uint8_t* base) {
   t->part_o = reinterpret_cast<float*>(base + round_up(rows * 8, kWsAlign));
 }
 
+// A row-tile launch of whole sequences (everything of `t` set but its parts and status
+// word), and the merge where the token ranges are split.
+int run_row_tiles(int D, const DeviceInfo& di, TileParams& t, const void* k_cache,
+                  const void* v_cache, void* workspace, size_t workspace_bytes, cudaStream_t st) {
+  t.splits = tile_splits(D, t.total_q, t.num_seqs, t.H_q, t.H_kv, di.sms);
+  t.single = t.splits == 1 ? 1 : 0;
+  const size_t parts = t.single ? 0 : tile_part_bytes(D, t.total_q, t.H_q, t.splits);
+  void* ws = nullptr;
+  WorkspaceHold hold;
+  int rc = optional_workspace(workspace, workspace_bytes, counters_end(di) + parts, st, &ws, &hold);
+  if (rc != PAGED_ATTN_OK) return rc;
+  t.status = g_check_blocks > 0 ? g_check_status : static_cast<int32_t*>(ws);
+  if (!t.single) set_parts(&t, static_cast<uint8_t*>(ws) + counters_end(di));
+  if ((rc = launch_tiles(D, t, k_cache, v_cache, st)) != PAGED_ATTN_OK) return rc;
+  if (t.single) return PAGED_ATTN_OK;
+  MergeParams m = {};
+  m.part_o = t.part_o;
+  m.part_ml = t.part_ml;
+  m.splits = t.splits;
+  m.qo_indptr = t.qo_indptr;
+  m.num_seqs = t.num_seqs;
+  m.total_q = t.total_q;
+  m.H_q = t.H_q;
+  m.D = D;
+  m.out = t.out;
+  return launch_merge_parts(m, st);
+}
+
 AppendParams append_params(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                            const int32_t* bt, const int32_t* sl, int num_seqs, int H_kv,
                            int head_dim, int max_blocks_per_seq, int block_size) {
@@ -996,6 +1025,15 @@ int fp8_checks(const void* q, const void* k8, const void* v8, const void* k_scal
 }
 
 }  // namespace
+
+int api_validate_sizes(int num_seqs, int H_q, int H_kv, int head_dim, int max_blocks_per_seq,
+                       int block_size) {
+  return validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size);
+}
+int api_cuda_fail(int err) { return cuda_fail(err); }
+int api_sms(int* sms) { return sms_of_device(sms); }
+int32_t* api_check_status() { return g_check_blocks > 0 ? g_check_status : nullptr; }
+
 }  // namespace pagedattn
 
 using namespace pagedattn;
@@ -1346,35 +1384,46 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   if (!aligned16(qo_indptr)) return PAGED_ATTN_ERR_POINTER;
   DeviceInfo di;
   if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   TileParams t = tile_params(head_dim, di.sms, q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
                              H_kv, max_blocks_per_seq, block_size, scale, softcap, alibi_slopes);
   t.causal = is_causal ? 1 : 0;
   t.window = window;
   t.prefix_lens = prefix_lens;
   t.doc_starts = doc_starts;
-  t.splits = tile_splits(head_dim, total_q, num_seqs, H_q, H_kv, di.sms);
-  t.single = t.splits == 1 ? 1 : 0;
-  const size_t parts = t.single ? 0 : tile_part_bytes(head_dim, total_q, H_q, t.splits);
-  void* ws = nullptr;
-  WorkspaceHold hold;
-  rc = optional_workspace(workspace, workspace_bytes, counters_end(di) + parts, st, &ws, &hold);
+  return run_row_tiles(head_dim, di, t, k_cache, v_cache, workspace, workspace_bytes,
+                       static_cast<cudaStream_t>(stream));
+}
+
+int paged_attn_decode_tree(const void* q, const void* k_cache, const void* v_cache, void* out,
+                           const int32_t* qo_indptr, const int32_t* tree_mask, int mask_words,
+                           const int32_t* block_tables, const int32_t* seq_lens, int num_seqs,
+                           int total_q, int H_q, int H_kv, int head_dim, int max_blocks_per_seq,
+                           int block_size, float scale, float softcap, const float* alibi_slopes,
+                           int window, const int32_t* prefix_lens, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  int rc = validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size);
   if (rc != PAGED_ATTN_OK) return rc;
-  t.status = g_check_blocks > 0 ? g_check_status : static_cast<int32_t*>(ws);
-  if (!t.single) set_parts(&t, static_cast<uint8_t*>(ws) + counters_end(di));
-  if ((rc = launch_tiles(head_dim, t, k_cache, v_cache, st)) != PAGED_ATTN_OK) return rc;
-  if (t.single) return PAGED_ATTN_OK;
-  MergeParams m = {};
-  m.part_o = t.part_o;
-  m.part_ml = t.part_ml;
-  m.splits = t.splits;
-  m.qo_indptr = qo_indptr;
-  m.num_seqs = num_seqs;
-  m.total_q = total_q;
-  m.H_q = H_q;
-  m.D = head_dim;
-  m.out = t.out;
-  return launch_merge_parts(m, st);
+  if (!std::isfinite(scale)) return PAGED_ATTN_ERR_SCALE;
+  if (total_q < 0 || mask_words < 1 || mask_words > kTreeWords ||
+      !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
+    return PAGED_ATTN_ERR_SIZES;
+  rc = mods_checks(scale, (long long)max_blocks_per_seq * block_size, softcap, alibi_slopes,
+                   window, prefix_lens, nullptr);
+  if (rc != PAGED_ATTN_OK || num_seqs == 0 || total_q == 0) return rc;
+  rc = check_pointers(q, k_cache, v_cache, out, block_tables, seq_lens);
+  if (rc != PAGED_ATTN_OK) return rc;
+  if (!aligned16(qo_indptr) || !aligned16(tree_mask)) return PAGED_ATTN_ERR_POINTER;
+  DeviceInfo di;
+  if ((rc = device_info(&di)) != PAGED_ATTN_OK) return rc;
+  TileParams t = tile_params(head_dim, di.sms, q, out, block_tables, seq_lens, qo_indptr, num_seqs, total_q, H_q,
+                             H_kv, max_blocks_per_seq, block_size, scale, softcap, alibi_slopes);
+  t.causal = 1;
+  t.window = window;
+  t.prefix_lens = prefix_lens;
+  t.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  t.mask_words = mask_words;
+  return run_row_tiles(head_dim, di, t, k_cache, v_cache, workspace, workspace_bytes,
+                       static_cast<cudaStream_t>(stream));
 }
 
 // Shared prefixes: the rows of a group's members over its prefix (row tiles),
@@ -1696,6 +1745,9 @@ const char* paged_attn_status_string(int status) {
       return "sizes need more scratch than paged_attn_decode_static's fixed 4 MiB array";
     case PAGED_ATTN_ERR_FLAGS: return "unknown launch flag bits";
     case PAGED_ATTN_ERR_MODS: return "softcap must be 0 or in [1e-30, 1e30], window >= 0";
+    case PAGED_ATTN_ERR_ROPE:
+      return "rotary_dim must be a multiple of 16 up to head_dim, num_axes and max_positions "
+             "positive, eps finite and not negative";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,494 @@
+// Compaction, forks and release of the pages of a cache (include/paged_attn.h:
+// paged_kv_compact, paged_kv_fork, paged_kv_release).
+//
+// All three move little: rows of a few accepted tokens, the last pages of forked
+// sequences, four bytes a page.  What bounds them is latency, of dependent reads (a length,
+// then a table entry, then rows) and of the steps that have to follow one another, so
+// each is one launch that keeps several reads of a thread in flight.
+#include <climits>
+#include <cstdint>
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "pages.h"
+#include "ptx.cuh"
+
+namespace pagedattn {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kBadBlock = 1, kBadLength = 2;
+
+__device__ __forceinline__ void report(int32_t* status, int bits) {
+  if (status != nullptr) atomicOr(status, bits);
+}
+
+__device__ __forceinline__ int clamped_length(int L, int maxb, int BS, int32_t* status) {
+  const long long cap = (long long)maxb * BS;
+  if (L < 0 || L > cap) report(status, kBadLength);
+  return (int)min(max((long long)L, 0LL), cap);
+}
+
+// Exclusive sum over the block's threads; the block's total in every thread.  `warp_sums`
+// is of 32 ints and is free again after the call.
+template <int THREADS>
+__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int w = lane < THREADS / 32 ? warp_sums[lane] : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += u;
+  }
+  *total = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
+  const int before = warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0;
+  __syncthreads();
+  return before + inc - v;
+}
+
+// ------------------------------------------------------------------ compaction
+//
+// Entry i of the list of sequence s moves the row of token ctx + accepted[i] to token ctx
+// + i, ctx = L - q_len.  The list rises, so a row moves towards the front or stays, and
+// accepted[j] >= j: rows written by one pass of a CTA lie before every row that a later
+// pass reads, and within a pass all reads come before the writes.  A CTA has one KV head
+// of a sequence, K and V.
+constexpr int kCompactThreads = 256;
+constexpr int kCompactUnroll = 4;
+
+__global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const CompactParams p) {
+  __shared__ int sm_n;
+  griddep_wait();
+  griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
+  const int s = blockIdx.x / p.cache.H_kv, g = blockIdx.x - s * p.cache.H_kv;
+  const int tid = threadIdx.x, BS = p.cache.BS;
+  const int a = p.qo_indptr[s], b = p.qo_indptr[s + 1];
+  const int q_len = (int)min(max((long long)b - a, 0LL), 0x7fffffffLL);
+  const int len = clamped_length(p.seq_lens[s], p.maxb, BS, tid == 0 && g == 0 ? p.status : nullptr);
+  const int ctx = len - q_len;
+  const int32_t* list = p.accepted + (size_t)s * p.max_accept;
+  if (tid == 0) sm_n = p.max_accept;
+  __syncthreads();
+  // the list ends at its first entry that is not past the one before or not in the tree
+  for (int i = tid; i < p.max_accept; i += kCompactThreads) {
+    const int x = list[i], before = i > 0 ? list[i - 1] : -1;
+    if (x <= before || x >= q_len) {
+      atomicMin(&sm_n, i);
+      break;
+    }
+  }
+  __syncthreads();
+  const int n = sm_n;
+  if (g == 0 && tid == 0) p.seq_lens_out[s] = max(ctx + n, 0);
+  const int32_t* table = p.block_tables + (size_t)s * p.maxb;
+  // the cache row of a token, -1: there is none
+  auto row_of = [&](int t) -> long long {
+    if (t < 0) return -1;
+    const int block = table[t / BS];
+    if (block < 0 || block >= p.cache.num_blocks) {
+      report(p.status, kBadBlock);
+      return -1;
+    }
+    return ((long long)block * p.cache.H_kv + g) * BS + t % BS;
+  };
+  const int chunks = p.cache.row_bytes / 16;       // 4 .. 32, a power of two
+  const int rows = kCompactThreads / (2 * chunks); // rows of K and V in one step
+  const int c = tid % chunks, kv = tid / chunks & 1, r = tid / (2 * chunks);
+  uint8_t* cache = kv ? p.cache.v : p.cache.k;
+  float* floats = kv ? p.cache.v_scale : p.cache.k_scale;
+  for (int i0 = 0; i0 < n; i0 += rows * kCompactUnroll) {
+    uint4 x[kCompactUnroll];
+    float f[kCompactUnroll];
+    long long to[kCompactUnroll];
+#pragma unroll
+    for (int u = 0; u < kCompactUnroll; ++u) {
+      const int i = i0 + u * rows + r;
+      to[u] = -1;
+      f[u] = 0.f;
+      if (i >= n) continue;
+      const int from = list[i];
+      if (from == i) continue;  // in its place
+      const long long src = row_of(ctx + from), dst = row_of(ctx + i);
+      if (src < 0 || dst < 0) continue;
+      to[u] = dst;
+      x[u] = *(reinterpret_cast<const uint4*>(cache + src * p.cache.row_bytes) + c);
+      if (floats != nullptr && c == 0) f[u] = floats[src];
+    }
+    __syncthreads();  // every row of this pass is read
+#pragma unroll
+    for (int u = 0; u < kCompactUnroll; ++u) {
+      if (to[u] < 0) continue;
+      *(reinterpret_cast<uint4*>(cache + to[u] * p.cache.row_bytes) + c) = x[u];
+      if (floats != nullptr && c == 0) floats[to[u]] = f[u];
+    }
+  }
+}
+
+// ------------------------------------------------------------------ forks
+//
+// Fork i needs a fresh block when its parent's last page is not full; R_i of the forks
+// before it do, and it takes the stack entry free_count - 1 - R_i.  Every CTA scans the
+// parents' lengths; the work of a fork (its table row, the counts of the shared blocks, the
+// rows of the last page) is cut into `parts` CTAs by KV heads, the first of which does
+// the table row.
+constexpr int kForkThreads = 256;
+constexpr int kForkUnroll = 8;
+
+struct Fork {
+  int parent, child, len, need;
+  bool valid;
+};
+
+__device__ __forceinline__ Fork load_fork(const ForkParams& p, int i) {
+  Fork f;
+  f.parent = p.parents[i];
+  f.child = p.children[i];
+  f.valid = f.parent >= 0 && f.parent < p.num_rows && f.child >= 0 && f.child < p.num_rows &&
+            f.parent != f.child;
+  f.len = f.valid ? clamped_length(p.seq_lens[f.parent], p.maxb, p.cache.BS, nullptr) : 0;
+  f.need = f.len % p.cache.BS != 0;
+  return f;
+}
+
+__global__ void __launch_bounds__(kForkThreads) paged_kv_fork_kernel(const ForkParams p, int parts,
+                                                                     int count_apart) {
+  __shared__ int before[kForkThreads];
+  __shared__ int warp_sums[32];
+  griddep_wait();
+  griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
+  const int tid = threadIdx.x, n = p.num_forks, BS = p.cache.BS;
+  const int free_count = min(max(*p.free_count, 0), p.free_capacity);
+  const int per = (n + kForkThreads - 1) / kForkThreads;  // forks that a thread sums
+  const int i0 = (int)min((long long)n, (long long)tid * per);
+  const int i1 = (int)min((long long)n, (long long)i0 + per);
+  int needs = 0, invalid = 0;
+  for (int i = i0; i < i1; ++i) {
+    const Fork f = load_fork(p, i);
+    needs += f.need;
+    invalid += !f.valid;
+  }
+  int total, bad = 0;
+  before[tid] = block_exclusive<kForkThreads>(needs, warp_sums, &total);
+  if (blockIdx.x == 0) block_exclusive<kForkThreads>(invalid, warp_sums, &bad);
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    if (!count_apart) *p.free_count_out = free_count - min(total, free_count);
+    if (p.refused != nullptr) *p.refused = bad + max(total - free_count, 0);
+  }
+  const long long units = (long long)n * parts;
+  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
+    const int i = (int)(unit / parts), part = (int)(unit - (long long)i * parts);
+    const Fork f = load_fork(p, i);
+    int rank = before[i / per];
+    for (int j = i / per * per; j < i; ++j) rank += load_fork(p, j).need;
+    const bool given = f.valid && (!f.need || rank < free_count);
+    if (!given) {
+      if (part == 0 && tid == 0) {
+        if (!f.valid) report(p.status, kBadLength);
+        if (f.child >= 0 && f.child < p.num_rows && f.child != f.parent) p.seq_lens[f.child] = 0;
+      }
+      continue;
+    }
+    const int full = f.len / BS, tail = f.len - full * BS;
+    const int32_t* from = p.block_tables + (size_t)f.parent * p.maxb;
+    int32_t* to = p.block_tables + (size_t)f.child * p.maxb;
+    const int fresh = f.need ? p.free_blocks[free_count - 1 - rank] : -1;
+    if (part == 0) {
+      for (int j = tid; j < full; j += kForkThreads) {
+        const int b = from[j];
+        to[j] = b;
+        if (b >= 0 && b < p.cache.num_blocks)
+          atomicAdd(p.block_refs + b, 1);
+        else
+          report(p.status, kBadBlock);
+      }
+      if (tid == 0) {
+        if (f.need) to[full] = fresh;
+        p.seq_lens[f.child] = f.len;
+        const int held = p.seq_lens[f.parent];
+        if (held != f.len) report(p.status, kBadLength);
+      }
+    }
+    if (!f.need) continue;
+    const int last = from[full];
+    if (last < 0 || last >= p.cache.num_blocks || fresh < 0 || fresh >= p.cache.num_blocks) {
+      if (tid == 0) report(p.status, kBadBlock);
+      continue;
+    }
+    // ---- the rows of the last page: of each tensor and KV head one run of `run` chunks
+    const int H = p.cache.H_kv, pairs = 2 * H;
+    const int a = (int)((long long)pairs * part / parts);
+    const int b = (int)((long long)pairs * (part + 1) / parts);
+    const uint32_t run = (uint32_t)tail * p.cache.row_bytes / 16;
+    const uint32_t most = (uint32_t)(b - a) * run;
+    const long long page = (long long)BS * p.cache.row_bytes;
+    for (uint32_t c0 = tid; c0 < most; c0 += kForkThreads * kForkUnroll) {
+      uint4 x[kForkUnroll];
+      uint4* dst[kForkUnroll];
+#pragma unroll
+      for (int u = 0; u < kForkUnroll; ++u) {
+        const uint32_t c = c0 + u * kForkThreads;
+        dst[u] = nullptr;
+        if (c >= most) continue;
+        const int pair = a + (int)(c / run), at = (int)(c % run);
+        uint8_t* cache = pair < H ? p.cache.k : p.cache.v;
+        const int h = pair < H ? pair : pair - H;
+        x[u] = *(reinterpret_cast<const uint4*>(cache + ((long long)last * H + h) * page) + at);
+        dst[u] = reinterpret_cast<uint4*>(cache + ((long long)fresh * H + h) * page) + at;
+      }
+#pragma unroll
+      for (int u = 0; u < kForkUnroll; ++u)
+        if (dst[u] != nullptr) *dst[u] = x[u];
+    }
+    if (p.cache.k_scale != nullptr) {
+      for (int c = tid; c < (b - a) * tail; c += kForkThreads) {
+        const int pair = a + c / tail, at = c % tail;
+        float* floats = pair < H ? p.cache.k_scale : p.cache.v_scale;
+        const int h = pair < H ? pair : pair - H;
+        floats[((long long)fresh * H + h) * BS + at] = floats[((long long)last * H + h) * BS + at];
+      }
+    }
+  }
+}
+
+// The free count where it is updated in place: the kernel above, whose CTAs all read the
+// old one, has completed.
+__global__ void __launch_bounds__(kForkThreads) paged_kv_fork_count_kernel(const ForkParams p) {
+  __shared__ int warp_sums[32];
+  griddep_wait();
+  griddep_launch_dependents();
+  int needs = 0, total;
+  for (int i = threadIdx.x; i < p.num_forks; i += kForkThreads) needs += load_fork(p, i).need;
+  block_exclusive<kForkThreads>(needs, warp_sums, &total);
+  if (threadIdx.x == 0) {
+    const int free_count = min(max(*p.free_count, 0), p.free_capacity);
+    *p.free_count_out = free_count - min(total, free_count);
+  }
+}
+
+// ------------------------------------------------------------------ release
+//
+// Entry (s, p) of the table is released when it lies past the page of the last kept token
+// and in the sequence; its key is e = s * maxb + p.  block_refs holds a block's holders past
+// the first, so with m of the released entries its count falls by m, and it is free when
+// the count is then below zero.  Which of its entries places it on the stack must not
+// hang on the order of atomics: it is the one of lowest key.  Steps, each one after all of
+// the one before:
+//
+//   1. refs[b] -= 1 for each entry
+//   2. where refs[b] < 0: refs[b] = min(refs[b], INT_MIN + e), so the lowest key remains
+//   3. entries with refs[b] == INT_MIN + e are counted, the counts summed
+//   4. those write their block to the stack at their rank and refs[b] = 0
+//
+// The grid is one thread-block cluster, whose barrier separates the steps (and all reads
+// of lengths and the free count from their writes in place).  A thread has a run of
+// consecutive entries, so ranks need one scan.
+constexpr int kReleaseThreads = 1024;
+constexpr int kReleaseCtas = 8;   // a portable cluster
+constexpr int kReleaseBatch = 8;  // entries of a thread in flight
+
+__global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const ReleaseParams p) {
+  __shared__ int before[kReleaseThreads];  // entries ahead of each thread's sequences
+  __shared__ int warp_sums[32];
+  __shared__ int sm_count;
+  griddep_wait();
+  griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, N = p.num_seqs;
+  const int ctas = (int)gridDim.x, cta = (int)blockIdx.x;
+  const int free_count = min(max(*p.free_count, 0), p.free_capacity);
+  const int per = (N + kReleaseThreads - 1) / kReleaseThreads;
+  const int s0 = (int)min((long long)N, (long long)tid * per);
+  const int s1 = (int)min((long long)N, (long long)s0 + per);
+  // first released page and the number of them
+  auto span = [&](int s, int& first) -> int {
+    const int len = clamped_length(p.seq_lens[s], p.maxb, p.BS, nullptr);
+    const int keep = min(max(p.keep_lens[s], 0), len);
+    first = (keep + p.BS - 1) / p.BS;
+    return (len + p.BS - 1) / p.BS - first;
+  };
+  int own = 0, all;
+  for (int s = s0; s < s1; ++s) {
+    int first;
+    own += span(s, first);
+    if (cta == 0) clamped_length(p.seq_lens[s], p.maxb, p.BS, p.status);
+  }
+  before[tid] = block_exclusive<kReleaseThreads>(own, warp_sums, &all);
+  __syncthreads();
+  // ---- this thread's run of entries [e0, e1) of all the released ones
+  const int run = (int)(((long long)all + ctas * kReleaseThreads - 1) / (ctas * kReleaseThreads));
+  const long long at = ((long long)cta * kReleaseThreads + tid) * run;
+  const int e0 = (int)min((long long)all, at), e1 = (int)min((long long)all, at + run);
+  int start_s = 0, start_p = 0, start_left = 0;  // sequence, page and pages left at e0
+  if (e0 < e1) {
+    int lo = 0, hi = kReleaseThreads - 1;  // the last group of sequences starting at or before e0
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] <= e0)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    int ahead = before[lo];
+    start_s = lo * per;
+    for (;;) {
+      int first;
+      const int n = span(start_s, first);
+      if (e0 < ahead + n || start_s + 1 >= N) {
+        start_p = first + (e0 - ahead);
+        start_left = ahead + n - e0;
+        break;
+      }
+      ahead += n;
+      ++start_s;
+    }
+  }
+  // f(key, block) for each entry of the run, kReleaseBatch of whose reads are in flight
+  // (`more`: a read for each block, all issued before the first f)
+  auto each = [&](auto&& more, auto&& f) {
+    int s = start_s, page = start_p, left = start_left;
+    for (int e = e0; e < e1; e += kReleaseBatch) {
+      int key[kReleaseBatch], block[kReleaseBatch], extra[kReleaseBatch];
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u) {
+        key[u] = -1;
+        if (e + u >= e1) continue;
+        while (left <= 0 && s + 1 < N) left = span(++s, page);
+        key[u] = s * p.maxb + page;
+        ++page;
+        --left;
+      }
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u)
+        block[u] = key[u] >= 0 ? p.block_tables[key[u]] : -1;
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u) {
+        // (a block that is none has no count and is not freed)
+        const bool bad = block[u] < 0 || (p.block_refs != nullptr && block[u] >= p.num_blocks);
+        if (bad && key[u] >= 0) report(p.status, kBadBlock);
+        if (bad) key[u] = -1;
+        extra[u] = key[u] >= 0 ? more(block[u]) : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u)
+        if (key[u] >= 0) f(key[u], block[u], extra[u]);
+    }
+  };
+  auto count_of = [&](int b) -> int { return p.block_refs ? __ldcg(p.block_refs + b) : 0; };
+  auto nothing = [](int) -> int { return 0; };
+  auto step_done = [&] {
+    __threadfence();
+    cluster.sync();
+  };
+  auto places = [&](int key, int refs) -> bool {
+    return p.block_refs == nullptr || refs == INT_MIN + key;
+  };
+  if (p.block_refs != nullptr) {
+    each(nothing, [&](int, int b, int) { atomicSub(p.block_refs + b, 1); });
+    step_done();
+    each(count_of, [&](int key, int b, int refs) {
+      if (refs < 0) atomicMin(p.block_refs + b, INT_MIN + key);
+    });
+    step_done();
+  }
+  int freed = 0, in_cta;
+  each(count_of, [&](int key, int, int refs) { freed += places(key, refs); });
+  int rank = block_exclusive<kReleaseThreads>(freed, warp_sums, &in_cta);
+  if (tid == 0) sm_count = in_cta;
+  step_done();
+  int total = 0;
+  for (int c = 0; c < ctas; ++c) {
+    const int n = *cluster.map_shared_rank(&sm_count, c);
+    if (c < cta) rank += n;
+    total += n;
+  }
+  each(count_of, [&](int key, int b, int refs) {
+    // (a block's other entries see the winner's key or the zero written over it: not theirs)
+    if (!places(key, refs)) return;
+    const long long to = (long long)free_count + rank++;
+    if (to < p.free_capacity)
+      p.free_blocks[to] = b;
+    else
+      report(p.status, kBadLength);
+    if (p.block_refs != nullptr) p.block_refs[b] = 0;
+  });
+  cluster.sync();  // every length, count and sum is read
+  for (int s = cta * kReleaseThreads + tid; s < N; s += ctas * kReleaseThreads) {
+    const int len = clamped_length(p.seq_lens[s], p.maxb, p.BS, nullptr);
+    p.seq_lens_out[s] = min(max(p.keep_lens[s], 0), len);
+  }
+  if (cta == 0 && tid == 0)
+    *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
+}
+
+cudaLaunchAttribute dependent_launch() {  // may be scheduled while the kernel before it ends
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  const long long ctas = (long long)p.num_seqs * p.cache.H_kv;
+  if (ctas == 0) return cudaSuccess;
+  if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kCompactThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_kv_compact_kernel, p);
+}
+
+cudaError_t launch_fork(const ForkParams& p, int sms, cudaStream_t stream) {
+  // parts of a fork: a power of two, until the CTAs are about four an SM
+  int parts = 1;
+  while (parts < 2 * p.cache.H_kv && (long long)p.num_forks * parts * 2 <= 4LL * sms) parts *= 2;
+  const long long units = (long long)p.num_forks * parts, most = 8LL * sms;
+  const int apart = p.free_count_out == p.free_count;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units < most ? units : most));
+  cfg.blockDim = dim3(kForkThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1] = {dependent_launch()};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_kv_fork_kernel, p, parts, apart);
+  if (e != cudaSuccess || !apart) return e;
+  cfg.gridDim = dim3(1);
+  return cudaLaunchKernelEx(&cfg, paged_kv_fork_count_kernel, p);
+}
+
+cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream) {
+  const long long entries = (long long)p.num_seqs * p.maxb;
+  int ctas = 1;  // by the entries there may be
+  while (ctas < kReleaseCtas && (long long)ctas * 4 * kReleaseThreads < entries) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kReleaseThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {dependent_launch(), {}};
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, paged_kv_release_kernel, p);
+}
+
+}  // namespace pagedattn

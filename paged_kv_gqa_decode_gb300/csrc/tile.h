@@ -27,6 +27,9 @@ constexpr int tile_teams(int D, long long total_rows, long long num_seqs, int H_
              : 1;
 }
 
+// Words of a drafted token's mask at most: trees of up to 256 tokens.
+constexpr int kTreeWords = 8;
+
 struct TileParams {
   const __nv_bfloat16* q;       // [total_q, H_q, D]
   __nv_bfloat16* out;           // [total_q, H_q, D]
@@ -44,6 +47,10 @@ struct TileParams {
   // (the prefix's) last one (null: the rows are the sequence's last tokens).
   const int32_t* tail_lens;     // [total_q] or null
   int tail_cap;                 // largest value tail_lens is clamped to
+  // A tree of drafted tokens (null: none): the sequence's last tokens see one another by
+  // these bits, [total_q][mask_words], and all but the masked-out tokens before them.
+  const uint32_t* tree_mask;
+  int mask_words;               // 1 .. kTreeWords
   int teams;                    // tile_teams: picks the kernel
   int splits;                   // parts of each piece's token range
   int single;                   // 1: splits is 1 and the kernel writes the output itself
@@ -69,6 +76,13 @@ cudaError_t launch_tile_d128(const CUtensorMap& tk, const CUtensorMap& tv, const
                              cudaStream_t stream);
 cudaError_t launch_tile_d256(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                              cudaStream_t stream);
+// The same kernels with tree masks (tile_tree_d*.cu); the three above pass on to them.
+cudaError_t launch_tile_tree_d64(const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const TileParams& p, cudaStream_t stream);
+cudaError_t launch_tile_tree_d128(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const TileParams& p, cudaStream_t stream);
+cudaError_t launch_tile_tree_d256(const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const TileParams& p, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, cudaStream_t stream);
 
 }  // namespace pagedattn

@@ -44,6 +44,12 @@
 // row of the piece sees, which may hold anything, are zeroed in shared memory
 // before the product.  Those are the rows outside the hull of the rows' intervals and, where
 // a row sees nothing, its own token if no later row sees it.
+//
+// Trees (TREE; kernels of their own, so that the others stay as they are): a row is a
+// drafted token, sees the cached tokens before the tree as above and of the tree's tokens
+// those its mask has a bit for.  Only the one or two token tiles with drafted tokens look at
+// the bits, shifted to the tile's columns; there V rows without a bit in any row of the
+// piece (padding nodes) are zeroed too.
 #pragma once
 
 #include <atomic>
@@ -62,7 +68,7 @@ constexpr float kTileLazyMax = 8.f;
 // 67.5 -> 50.5 us, two head_dim 256 chunks 185 -> 127.
 constexpr int kRankedSeqs = 128;
 
-template <int D, int TEAMS>
+template <int D, int TEAMS, bool TREE = false>
 struct TileShape {
   static constexpr int kTeams = TEAMS;                    // softmax teams of 256 threads
   static constexpr int kRows = 128 * TEAMS;
@@ -97,7 +103,9 @@ struct TileShape {
   static constexpr int kRingOff = kTeams * kQTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
-  static constexpr int kSmem = kMaxOff + kTeams * kBufs * 2 * 128 * 4;
+  // (trees) depths of the drafted tokens, 16 bits each
+  static constexpr int kDepthOff = kMaxOff + kTeams * kBufs * 2 * 128 * 4;
+  static constexpr int kSmem = kDepthOff + (TREE ? 32 * kTreeWords * 2 : 0);
   static_assert((kSmem + 1024) * kCtas <= 228 * 1024 && (2 * kSlots + 14 + kProducers) * 8 <= 384,
                 "shared memory");
 };
@@ -144,11 +152,11 @@ __device__ __forceinline__ float cap_score(float s, float c, float cap_log2) {
   return cap_log2 * (fabsf(y) < kTanhSeries ? tanh_series(y) : tanh_exp(y));
 }
 
-template <int D, int TEAMS, int MOD>
+template <int D, int TEAMS, int MOD, bool TREE>
 __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TEAMS>::kCtas)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TileParams p) {
-  using T = TileShape<D, TEAMS>;
+  using T = TileShape<D, TEAMS, TREE>;
   constexpr int kTeams = T::kTeams, kRows = T::kRows, BN = T::BN, kHalves = T::kHalves;
   constexpr int kThreads = T::kThreads;
   extern __shared__ __align__(1024) uint8_t smem[];  // (no room for an alignment slack)
@@ -306,7 +314,20 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       len = (int)min(max((long long)len, 0LL), cap);
     }
   }
-  const int pre = p.prefix_lens != nullptr ? min(max(__ldg(p.prefix_lens + s), 0), len) : 0;
+  // (a tree's drafted tokens, from ctx on, are seen by their bits alone)
+  const int ctx = TREE ? len - q_len : 0;
+  const int pre = p.prefix_lens != nullptr
+                      ? min(max(__ldg(p.prefix_lens + s), 0), TREE ? max(ctx, 0) : len)
+                      : 0;
+  // Drafted tokens that there are bits for, and those of bits 32 w .. 32 w + 31 of drafted
+  // token qi's mask that are tokens of the sequence.
+  const int drafts = TREE ? min(q_len, 32 * p.mask_words) : 0;
+  if (TREE && q_len > drafts && p.num_blocks > 0 && tid == 0) report(kTileStatusBadLength);
+  auto mask_word = [&](int qi, int w) -> uint32_t {
+    if (w < 0 || w >= p.mask_words) return 0u;
+    return __ldg(p.tree_mask + (size_t)(qo + qi) * p.mask_words + w) &
+           ~bits_from((long long)drafts - 32 * w) & bits_from(-(long long)ctx - 32 * w);
+  };
   const int n_rows = (int)min((long long)kRows, (long long)q_len * G - row0);
   const bool both = kTeams == 2 && n_rows > 128;  // a row tile per warpgroup
 
@@ -330,6 +351,22 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       const int tail = min(max(__ldg(p.tail_lens + qo + qi), 0), p.tail_cap);
       pos = (int)min((long long)len - 1 + tail, 0x7fffffffLL);
       hi = len - 1;
+    } else if constexpr (TREE) {
+      // as deep in the tree as the drafted tokens it sees; [lo, hi] are cached tokens
+      int n = 0, from = -1, to = -1;
+      for (int w = 0; w < p.mask_words; ++w) {
+        const uint32_t word = mask_word(qi, w);
+        if (word == 0u) continue;
+        n += __popc(word);
+        if (from < 0) from = 32 * w + __ffs(word) - 1;
+        to = 32 * w + 31 - __clz(word);
+      }
+      pos = ctx + n - 1;
+      hi = ctx - 1;
+      if (from >= 0) {
+        atomicMin(&sm_i[3], ctx + from);
+        atomicMax(&sm_i[4], ctx + to);
+      }
     } else {
       pos = len - q_len + qi;
       hi = p.causal ? pos : len - 1;
@@ -339,7 +376,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     if (lo <= hi) {
       atomicMin(&sm_i[3], lo);
       atomicMax(&sm_i[4], hi);
-    } else if (p.causal) {
+    } else if (!TREE && p.causal) {
       sm_i[7] = 1;
     }
     atomicMax(&sm_i[5], lo);
@@ -364,6 +401,21 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     if (lane == 0) mbar_arrive(q_full);
   }
   if (tid < 8) sm_i[8 + tid] = 0;
+  // [drafts] drafted tokens that each of them sees
+  uint16_t* sm_depth = reinterpret_cast<uint16_t*>(smem + T::kDepthOff);
+  if constexpr (TREE) {
+    __syncthreads();
+    if (valid && half == 0)
+      for (int w = 0; w < p.mask_words; ++w) {
+        const uint32_t word = mask_word(qi, w);
+        if (word != 0u) atomicOr(&sm_i[8 + w], (int)word);
+      }
+    if (MOD == kTileGeneral && p.slopes != nullptr && tid < drafts) {
+      int n = 0;
+      for (int w = 0; w < p.mask_words; ++w) n += __popc(mask_word(tid, w));
+      sm_depth[tid] = (uint16_t)n;
+    }
+  }
   __syncthreads();
   const int min_lo = sm_i[3], max_hi = sm_i[4];
   // tiles beginning in [clean_lo, clean_hi] are seen whole by every row
@@ -650,6 +702,15 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         for (int b = 0; b < kBlocks; ++b)
           seen[b] = (bits_from(lo - c0 - 32 * b) & ~bits_from(hi + 1LL - c0 - 32 * b)) |
                     ~bits_from(pre - c0 - 32 * b);
+        if constexpr (TREE) {
+          if (c0 + kCols > ctx && valid) {  // drafted tokens: the bits from token c0 + 32 b on
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+              const int from = c0 + 32 * b - ctx, w = from >> 5;  // (rounded down)
+              seen[b] |= __funnelshift_r(mask_word(qi, w), mask_word(qi, w + 1), from & 31);
+            }
+          }
+        }
       };
       auto sees = [&](int b, int c) { return (seen[b] >> c & 1u) != 0; };
       // ---- this thread's scores (a timeout leaves what is there: the walk goes on
@@ -671,7 +732,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         const float d0 = (float)(pos - c0), base = -slope * d0;
         // -slope |pos - t| is linear over the columns where no token lies past the
         // query, which is everywhere but on a causal diagonal and beyond
-        const bool behind = __all_sync(0xffffffffu, pos >= c0 + kCols - 1 || slope == 0.f);
+        const bool behind = __all_sync(
+            0xffffffffu, (TREE ? ctx >= c0 + kCols : pos >= c0 + kCols - 1) || slope == 0.f);
         auto each_pair = [&](auto&& f) {  // column pairs (c, c + 1)
 #pragma unroll
           for (int c = 0; c < kCols; c += 2) {
@@ -719,8 +781,14 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         }
         if (!behind) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
-            x[c >> 5][c & 31] = fmaf(-slope, fabsf(d0 - (float)c), x[c >> 5][c & 31]);
+          for (int c = 0; c < kCols; ++c) {
+            float d = d0 - (float)c;
+            if constexpr (TREE) {  // a drafted token stands as deep as it is in the tree
+              const int j = c0 + c - ctx;
+              if (j >= 0 && j < drafts) d = (float)(pos + 1 - ctx - (int)sm_depth[j]);
+            }
+            x[c >> 5][c & 31] = fmaf(-slope, fabsf(d), x[c >> 5][c & 31]);
+          }
         }
       }
       find_seen();
@@ -863,13 +931,19 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       // ---- V rows of this tile that no row of the piece sees (the first step on a
       // tile zeroes them; the product of the other row tile comes after its own)
       if ((t0 < clean_lo || t0 > clean_hi) && (!both || team == 0) &&
-          (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre))) {
+          (t0 + BN - 1 > last_seen || (t0 < min_lo && t0 + BN > pre) ||
+           (TREE && t0 + BN > ctx))) {
         const int item = item_v(j);
         ok = ok && warp_wait(&full[item % slots], (uint32_t)((item / slots) & 1));
         uint8_t* v = smem + slot_off(item % slots);
         for (int c = half * 128 + r128; ok && c < BN * kHalves * 8; c += 256) {
           const int row = (c >> 3) % BN, t = t0 + row;
-          if (t > last_seen || (t < min_lo && t >= pre))
+          bool unseen = t > last_seen || (t < min_lo && t >= pre);
+          if constexpr (TREE) {
+            const int k = t - ctx;  // (t <= last_seen: a bit of the union below)
+            unseen = unseen || (k >= 0 && !(sm_i[8 + (k >> 5)] >> (k & 31) & 1));
+          }
+          if (unseen)
             *reinterpret_cast<uint4*>(v + (c >> 3) / BN * (BN * 128) + row * 128 +
                                       (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -972,12 +1046,12 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   }
 }
 
-template <int D, int TEAMS, int MOD>
+template <int D, int TEAMS, int MOD, bool TREE>
 cudaError_t launch_tile_as(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                            cudaStream_t stream) {
-  using T = TileShape<D, TEAMS>;
+  using T = TileShape<D, TEAMS, TREE>;
   static std::atomic<bool> limit_raised[64];
-  auto kernel = paged_tile_kernel<D, TEAMS, MOD>;
+  auto kernel = paged_tile_kernel<D, TEAMS, MOD, TREE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1002,13 +1076,13 @@ cudaError_t launch_tile_as(const CUtensorMap& tk, const CUtensorMap& tv, const T
   return cudaLaunchKernelEx(&cfg, kernel, tk, tv, p);
 }
 
-template <int D, int TEAMS>
+template <int D, int TEAMS, bool TREE = false>
 cudaError_t launch_tile(const CUtensorMap& tk, const CUtensorMap& tv, const TileParams& p,
                         cudaStream_t stream) {
   if (p.slopes != nullptr || !(p.scale_log2 > 0.f))
-    return launch_tile_as<D, TEAMS, kTileGeneral>(tk, tv, p, stream);
-  return p.cap_log2 > 0.f ? launch_tile_as<D, TEAMS, kTileCapped>(tk, tv, p, stream)
-                          : launch_tile_as<D, TEAMS, kTilePlain>(tk, tv, p, stream);
+    return launch_tile_as<D, TEAMS, kTileGeneral, TREE>(tk, tv, p, stream);
+  return p.cap_log2 > 0.f ? launch_tile_as<D, TEAMS, kTileCapped, TREE>(tk, tv, p, stream)
+                          : launch_tile_as<D, TEAMS, kTilePlain, TREE>(tk, tv, p, stream);
 }
 
 }  // namespace pagedattn
