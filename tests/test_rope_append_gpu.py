@@ -144,6 +144,23 @@ def test_several_axes(D, inter, fp8):
     run_case(20, 8, 2, D, 16, D, axes=2, sections=np.arange(half) - 3, inter=inter, fp8=fp8, seed=4)  # clamped
 
 
+# enough rows for the kernel that streams them
+@pytest.mark.parametrize("rows,H_q,H_kv,D,kw", [
+    (2601, 32, 8, 64, dict()), (2601, 40, 8, 64, dict(inter=True, axes=3)), (1501, 32, 8, 128, dict()),
+    (1501, 32, 8, 128, dict(inter=True, norm=False)), (1501, 20, 10, 128, dict(fp8=True)),
+    (1000, 32, 2, 128, dict(part=48, gap=8)), (1000, 33, 11, 128, dict(fp8=True, inter=True, part=64)),
+    (701, 24, 4, 256, dict(fp8=True, part=64)), (801, 24, 4, 256, dict(axes=3)),
+    (1501, 32, 8, 128, dict(axes=3, inter=False, mixed=True)), (1501, 32, 8, 128, dict(axes=2, fp8=True, mixed=True)),
+    (1501, 32, 8, 128, dict(dense=True, in_place=True)), (1501, 32, 8, 128, dict(part=0)),
+])
+def test_many_rows(rows, H_q, H_kv, D, kw):
+    kw = dict(kw)
+    R = kw.pop("part", D)
+    if kw.pop("mixed", False):
+        kw["sections"] = np.arange(R // 2) % kw["axes"]
+    run_case(rows, H_q, H_kv, D, 16, R, seed=rows, out_of_range=rows == 1000, **kw)
+
+
 def test_positions_outside_the_table_are_clamped():
     run_case(50, 8, 2, 128, 16, 128, out_of_range=True)
     run_case(50, 8, 2, 128, 16, 128, axes=3, out_of_range=True, sections=np.arange(64) % 3)
