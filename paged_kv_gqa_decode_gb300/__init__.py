@@ -4,7 +4,9 @@ A thin Python binding over the C ABI in ``include/paged_attn.h``: the
 functions here only marshal torch tensors into pointers, sizes and the
 current CUDA stream; every step of the computation runs in the library's
 CUDA kernels.  There is no fallback: if the compiled library is missing the
-calls raise.
+calls raise.  The entry points of speculative and parallel decoding (trees, rotation
+with the append, compaction, forks, release) are marshalled by a native module
+(``csrc/binding.cpp``), as an engine's step waits for the host in them.
 """
 from __future__ import annotations
 
@@ -98,8 +100,12 @@ EXPORTED_SYMBOLS = (
 # Launch flags (include/paged_attn.h).
 FLAG_EARLY_PROLOGUE = 1
 
+# The module that marshals the tree, rotation and page entry points (csrc/binding.cpp).
+NATIVE_PATH = os.path.join(_PKG, "lib", "_paged_native.so")
+
 _lock = threading.Lock()
 _lib = None
+_native = None
 
 
 class PagedAttnError(RuntimeError):
@@ -204,6 +210,33 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         if path is None:
             _lib = lib
         return lib
+
+
+def _load_native():
+    """Load the marshalling module and give it the library's entry points."""
+    global _native
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (the module links to it)
+
+    lib = load()
+    with _lock:
+        if _native is None:
+            if not os.path.exists(NATIVE_PATH):
+                raise RuntimeError(
+                    f"{NATIVE_PATH} is missing: build it with `python -m "
+                    "paged_kv_gqa_decode_gb300.build` (needs g++ and torch's headers)")
+            loader = importlib.machinery.ExtensionFileLoader("_paged_native", NATIVE_PATH)
+            mod = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_paged_native", NATIVE_PATH,
+                                                       loader=loader))
+            loader.exec_module(mod)
+            mod.init(_check, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.paged_attn_decode_tree, lib.paged_kv_rope_append_slots, lib.paged_kv_compact,
+                lib.paged_kv_fork, lib.paged_kv_release)))
+            _native = mod
+        return _native
 
 
 def paged_attn_status_string(status: int) -> str:
@@ -855,57 +888,9 @@ def paged_attn_decode_tree(q, k_cache, v_cache, qo_indptr, tree_mask, block_tabl
     of a tree: itself and its ancestors).  A row's position is the tokens before the tree
     plus the drafted ones it sees, less one; the other options as
     paged_attn_decode_multi_mods (``workspace``: paged_attn_multi_mods_workspace_bytes)."""
-    import torch
-
-    softcap, window = _softcap(softcap), _int32("window", window)
-    total_q, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
-        q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, None,
-        workspace, torch.bfloat16, rows="many")
-    _need("qo_indptr", qo_indptr, torch.int32, (n + 1,))
-    if tree_mask.dim() != 2:
-        raise ValueError("tree_mask must be [total_q, words]")
-    words = tree_mask.shape[1]
-    _need("tree_mask", tree_mask, torch.int32, (total_q, words))
-    _same_device(qo_indptr, tree_mask)
-    _check((_lib or load()).paged_attn_decode_tree(
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
-        qo_indptr.data_ptr(), tree_mask.data_ptr(), words, block_tables.data_ptr(),
-        seq_lens.data_ptr(), n, total_q, H_q, H_kv, D, maxb, BS, float(scale), softcap,
-        _ptr(alibi_slopes), window, _ptr(prefix_lens), _ptr(workspace), _bytes(workspace),
-        _raw_stream(stream, dev)))
-    return out
-
-
-def _caches(k_cache, v_cache, k_scale, v_scale):
-    """Checks a pair of caches, bf16 or (with both floats) FP8; returns their shape."""
-    import torch
-
-    if k_cache.dim() != 4:
-        raise ValueError("the caches must be [num_blocks, H_kv, block_size, D]")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale come together (FP8 caches) or not at all")
-    shape = k_cache.shape
-    dtype = torch.bfloat16 if k_scale is None else torch.uint8
-    _need("k_cache", k_cache, dtype, shape)
-    _need("v_cache", v_cache, dtype, shape)
-    if k_scale is not None:
-        _need("k_scale", k_scale, torch.float32, shape[:3])
-        _need("v_scale", v_scale, torch.float32, shape[:3])
-    return shape
-
-
-def _strided_rows(name, t, rows, heads, D) -> int:
-    """Checks bf16 rows [rows, heads, D], each contiguous; returns their stride."""
-    import torch
-
-    if t.dtype is not torch.bfloat16 or t.shape != (rows, heads, D):
-        raise ValueError(f"{name} must be bfloat16 [{rows}, {heads}, {D}]")
-    if rows == 0:
-        return heads * D
-    st = t.stride()
-    if st[2] != 1 or (heads > 1 and st[1] != D):
-        raise ValueError(f"the rows of {name} must be contiguous [heads, head_dim]")
-    return st[0] if rows > 1 else heads * D
+    return (_native or _load_native()).decode_tree(
+        q, k_cache, v_cache, qo_indptr, tree_mask, block_tables, seq_lens, scale, softcap,
+        alibi_slopes, window, prefix_lens, out, workspace, stream)
 
 
 def paged_kv_rope_append_slots(q, k_new, v_new, k_cache, v_cache, slot_map, positions, cos_sin,
@@ -923,41 +908,9 @@ def paged_kv_rope_append_slots(q, k_new, v_new, k_cache, v_cache, slot_map, posi
     naming the axis of each pair.  cos_sin: float32 [max_positions, rotary_dim], cosines
     then sines; the first rotary_dim elements of a head turn, in pairs (i, i + rotary_dim /
     2) or, ``interleaved``, (2 i, 2 i + 1).  q_norm, k_norm: float32 [D], or None (no norm)."""
-    import torch
-
-    nb, H_kv, BS, D = _caches(k_cache, v_cache, k_scale, v_scale)
-    if q.dim() != 3:
-        raise ValueError("q must be [rows, H_q, D]")
-    rows, H_q = q.shape[0], q.shape[1]
-    qs = _strided_rows("q", q, rows, H_q, D)
-    ks = _strided_rows("k_new", k_new, rows, H_kv, D)
-    vs = _strided_rows("v_new", v_new, rows, H_kv, D)
-    _need("slot_map", slot_map, torch.int64, (rows,))
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _need("positions", positions, torch.int32, (axes, rows) if positions.dim() == 2 else (rows,))
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_positions, rotary_dim]")
-    most, rot = cos_sin.shape
-    _need("cos_sin", cos_sin, torch.float32, (most, rot))
-    if freq_axis is not None:
-        _need("freq_axis", freq_axis, torch.int32, (rot // 2,))
-    if q_norm is not None:
-        _need("q_norm", q_norm, torch.float32, (D,))
-    if k_norm is not None:
-        _need("k_norm", k_norm, torch.float32, (D,))
-    if out is None:
-        out = torch.empty((rows, H_q, D), dtype=torch.bfloat16, device=q.device)
-    else:
-        _need("out", out, torch.bfloat16, (rows, H_q, D))
-    dev = _same_device(q, k_new, v_new, k_cache, v_cache, slot_map, positions, cos_sin, freq_axis,
-                       q_norm, k_norm, k_scale, v_scale, out)
-    _check((_lib or load()).paged_kv_rope_append_slots(
-        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, out.data_ptr(),
-        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale), slot_map.data_ptr(),
-        positions.data_ptr(), axes, _ptr(freq_axis), cos_sin.data_ptr(), most, rot,
-        1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), float(eps), rows, H_q, H_kv, D, BS,
-        nb, _raw_stream(stream, dev)))
-    return out
+    return (_native or _load_native()).rope_append_slots(
+        q, k_new, v_new, k_cache, v_cache, slot_map, positions, cos_sin, interleaved, freq_axis,
+        q_norm, k_norm, eps, k_scale, v_scale, out, stream)
 
 
 def paged_kv_compact(k_cache, v_cache, qo_indptr, accepted, block_tables, seq_lens, *,
@@ -967,30 +920,9 @@ def paged_kv_compact(k_cache, v_cache, qo_indptr, accepted, block_tables, seq_le
     max_accept], the kept ones' places in the draft in rising order, padded with -1.
     Returns the new lengths (``seq_lens_out``, other memory than seq_lens, which
     paged_kv_release takes beside them)."""
-    import torch
-
-    nb, H_kv, BS, D = _caches(k_cache, v_cache, k_scale, v_scale)
-    i32 = torch.int32
-    n = seq_lens.shape[0]
-    if accepted.dim() != 2 or block_tables.dim() != 2:
-        raise ValueError("accepted must be [num_seqs, max_accept], block_tables [num_seqs, "
-                         "max_blocks]")
-    most, maxb = accepted.shape[1], block_tables.shape[1]
-    _need("seq_lens", seq_lens, i32, (n,))
-    _need("qo_indptr", qo_indptr, i32, (n + 1,))
-    _need("accepted", accepted, i32, (n, most))
-    _need("block_tables", block_tables, i32, (n, maxb))
-    if seq_lens_out is None:
-        seq_lens_out = torch.empty_like(seq_lens)
-    else:
-        _need("seq_lens_out", seq_lens_out, i32, (n,))
-    dev = _same_device(k_cache, v_cache, qo_indptr, accepted, block_tables, seq_lens, k_scale,
-                       v_scale, seq_lens_out)
-    _check((_lib or load()).paged_kv_compact(
-        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-        qo_indptr.data_ptr(), accepted.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-        seq_lens_out.data_ptr(), n, most, H_kv, D, maxb, BS, nb, _raw_stream(stream, dev)))
-    return seq_lens_out
+    return (_native or _load_native()).compact(
+        k_cache, v_cache, qo_indptr, accepted, block_tables, seq_lens, k_scale, v_scale,
+        seq_lens_out, stream)
 
 
 def paged_kv_fork(k_cache, v_cache, block_tables, seq_lens, parents, children, block_refs,
@@ -1003,37 +935,9 @@ def paged_kv_fork(k_cache, v_cache, block_tables, seq_lens, parents, children, b
     a parent.  Returns the free count (``free_count_out``, which may be free_count);
     ``refused``: an int32 tensor of one element that receives the number of forks for
     which there was no block."""
-    import torch
-
-    nb, H_kv, BS, D = _caches(k_cache, v_cache, k_scale, v_scale)
-    i32 = torch.int32
-    n_free = _int32("free_blocks' length", free_blocks.numel())
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [rows, max_blocks]")
-    rows, maxb = block_tables.shape
-    forks = parents.shape[0]
-    _need("block_tables", block_tables, i32, (rows, maxb))
-    _need("seq_lens", seq_lens, i32, (rows,))
-    _need("parents", parents, i32, (forks,))
-    _need("children", children, i32, (forks,))
-    _need("block_refs", block_refs, i32, (nb,))
-    _need("free_blocks", free_blocks, i32, (n_free,))
-    _need("free_count", free_count, i32, (1,))
-    if free_count_out is None:
-        free_count_out = torch.empty_like(free_count)
-    else:
-        _need("free_count_out", free_count_out, i32, (1,))
-    if refused is not None:
-        _need("refused", refused, i32, (1,))
-    dev = _same_device(k_cache, v_cache, block_tables, seq_lens, parents, children, block_refs,
-                       free_blocks, free_count, k_scale, v_scale, free_count_out, refused)
-    _check((_lib or load()).paged_kv_fork(
-        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
-        block_tables.data_ptr(), seq_lens.data_ptr(), parents.data_ptr(), children.data_ptr(),
-        block_refs.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
-        free_count_out.data_ptr(), _ptr(refused), forks, rows, H_kv, D, maxb, BS, n_free, nb,
-        _raw_stream(stream, dev)))
-    return free_count_out
+    return (_native or _load_native()).fork(
+        k_cache, v_cache, block_tables, seq_lens, parents, children, block_refs, free_blocks,
+        free_count, k_scale, v_scale, free_count_out, refused, stream)
 
 
 def paged_kv_release(block_tables, seq_lens, keep_lens, free_blocks, free_count, block_size: int,
@@ -1044,36 +948,6 @@ def paged_kv_release(block_tables, seq_lens, keep_lens, free_blocks, free_count,
     the order of the sequences and pages.  Returns (seq_lens_out, free_count_out), made here
     unless passed; they may be seq_lens (or keep_lens) and free_count, to update them in
     place.  free_blocks and block_refs are updated in place."""
-    import torch
-
-    block_size = _int32("block_size", block_size)
-    n_free = _int32("free_blocks' length", free_blocks.numel())
-    i32 = torch.int32
-    n = seq_lens.shape[0]
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    maxb = block_tables.shape[1]
-    _need("block_tables", block_tables, i32, (n, maxb))
-    _need("seq_lens", seq_lens, i32, (n,))
-    _need("keep_lens", keep_lens, i32, (n,))
-    _need("free_blocks", free_blocks, i32, (n_free,))
-    _need("free_count", free_count, i32, (1,))
-    nb = 0
-    if block_refs is not None:
-        nb = block_refs.numel()
-        _need("block_refs", block_refs, i32, (nb,))
-    if seq_lens_out is None:
-        seq_lens_out = torch.empty_like(seq_lens)
-    else:
-        _need("seq_lens_out", seq_lens_out, i32, (n,))
-    if free_count_out is None:
-        free_count_out = torch.empty_like(free_count)
-    else:
-        _need("free_count_out", free_count_out, i32, (1,))
-    dev = _same_device(block_tables, seq_lens, keep_lens, free_blocks, free_count, block_refs,
-                       seq_lens_out, free_count_out)
-    _check((_lib or load()).paged_kv_release(
-        block_tables.data_ptr(), seq_lens.data_ptr(), keep_lens.data_ptr(), _ptr(block_refs), nb,
-        free_blocks.data_ptr(), free_count.data_ptr(), seq_lens_out.data_ptr(),
-        free_count_out.data_ptr(), n, maxb, block_size, n_free, _raw_stream(stream, dev)))
-    return seq_lens_out, free_count_out
+    return (_native or _load_native()).release(
+        block_tables, seq_lens, keep_lens, free_blocks, free_count, block_size, block_refs,
+        seq_lens_out, free_count_out, stream)

@@ -60,7 +60,56 @@ def source_digest() -> str:
     return h.hexdigest()
 
 
+# The Python module that marshals some entry points: plain C++ against torch's headers.
+NATIVE_SOURCE = os.path.join(CSRC, "binding.cpp")
+NATIVE_PATH = os.path.join(LIB_DIR, "_paged_native.so")
+
+
+def build_native(force: bool = False) -> str:
+    import sysconfig
+
+    import torch
+
+    os.makedirs(LIB_DIR, exist_ok=True)
+    where = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden"]
+    for inc in (INCLUDE, os.path.join(where, "include"),
+                os.path.join(where, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda, "include")):
+        cmd += ["-I", inc]
+    libs = ["-L", os.path.join(where, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python"]
+    h = hashlib.sha256(" ".join(cmd + libs + [torch.__version__, sys.version]).encode())
+    for path in (NATIVE_SOURCE, os.path.join(INCLUDE, "paged_attn.h")):
+        with open(path, "rb") as f:
+            h.update(f.read())
+    digest = h.hexdigest()
+    stamp = os.path.join(LIB_DIR, "build_native.sha256")
+    if not force and os.path.exists(NATIVE_PATH) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == digest:
+                return NATIVE_PATH
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    r = subprocess.run(cmd + [NATIVE_SOURCE, "-o", tmp] + libs, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {NATIVE_SOURCE}:\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
+    with open(stamp, "w") as f:
+        f.write(digest + "\n")
+    return NATIVE_PATH
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the kernels
+        native = ex.submit(build_native, force)
+        path = build_library(verbose, force)
+        native.result()
+    return path
+
+
+def build_library(verbose: bool = False, force: bool = False) -> str:
     os.makedirs(LIB_DIR, exist_ok=True)
     obj_dir = os.path.join(LIB_DIR, "obj")
     os.makedirs(obj_dir, exist_ok=True)

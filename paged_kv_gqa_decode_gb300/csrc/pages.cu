@@ -5,6 +5,7 @@
 // sequences, four bytes a page.  What bounds them is latency, of dependent reads (a length,
 // then a table entry, then rows) and of the steps that have to follow one another, so
 // each is one launch that keeps several reads of a thread in flight.
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -60,23 +61,37 @@ __device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total
 //
 // Entry i of the list of sequence s moves the row of token ctx + accepted[i] to token ctx
 // + i, ctx = L - q_len.  The list rises, so a row moves towards the front or stays, and
-// accepted[j] >= j: rows written by one pass of a CTA lie before every row that a later
-// pass reads, and within a pass all reads come before the writes.  A CTA has one KV head
-// of a sequence, K and V.
-constexpr int kCompactThreads = 256;
+// accepted[j] >= j: rows written by one pass of a warp lie before every row that a later
+// pass reads, and within a pass all reads come before the writes.  A warp has K or V of one KV
+// head of a sequence; its CTA looks the rows' places up once for eight of them.
+constexpr int kCompactThreads = 256, kCompactWarps = kCompactThreads / 32;
 constexpr int kCompactUnroll = 4;
 
-__global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const CompactParams p,
+                                                                           int ctas_per_seq) {
   __shared__ int sm_n;
+  __shared__ longlong2 sm_move[kCompactThreads];  // (from, to): cache rows of KV head 0
   griddep_wait();
   griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
-  const int s = blockIdx.x / p.cache.H_kv, g = blockIdx.x - s * p.cache.H_kv;
-  const int tid = threadIdx.x, BS = p.cache.BS;
+  const int s = blockIdx.x / ctas_per_seq, part = blockIdx.x - s * ctas_per_seq;
+  const int tid = threadIdx.x, BS = p.cache.BS, H = p.cache.H_kv;
   const int a = p.qo_indptr[s], b = p.qo_indptr[s + 1];
   const int q_len = (int)min(max((long long)b - a, 0LL), 0x7fffffffLL);
-  const int len = clamped_length(p.seq_lens[s], p.maxb, BS, tid == 0 && g == 0 ? p.status : nullptr);
+  const int len =
+      clamped_length(p.seq_lens[s], p.maxb, BS, tid == 0 && part == 0 ? p.status : nullptr);
   const int ctx = len - q_len;
   const int32_t* list = p.accepted + (size_t)s * p.max_accept;
+  const int32_t* table = p.block_tables + (size_t)s * p.maxb;
+  // the cache row of a token and KV head 0, -1: there is none
+  auto row_of = [&](int t) -> long long {
+    if (t < 0) return -1;
+    const int block = table[t / BS];
+    if (block < 0 || block >= p.cache.num_blocks) {
+      report(p.status, kBadBlock);
+      return -1;
+    }
+    return (long long)block * H * BS + t % BS;
+  };
   if (tid == 0) sm_n = p.max_accept;
   __syncthreads();
   // the list ends at its first entry that is not past the one before or not in the tree
@@ -89,47 +104,52 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
   }
   __syncthreads();
   const int n = sm_n;
-  if (g == 0 && tid == 0) p.seq_lens_out[s] = max(ctx + n, 0);
-  const int32_t* table = p.block_tables + (size_t)s * p.maxb;
-  // the cache row of a token, -1: there is none
-  auto row_of = [&](int t) -> long long {
-    if (t < 0) return -1;
-    const int block = table[t / BS];
-    if (block < 0 || block >= p.cache.num_blocks) {
-      report(p.status, kBadBlock);
-      return -1;
+  if (part == 0 && tid == 0) p.seq_lens_out[s] = max(ctx + n, 0);
+  const int pair = part * kCompactWarps + (tid >> 5);  // K of each KV head, then V
+  const int g = pair < H ? pair : pair - H;
+  uint8_t* cache = pair < H ? p.cache.k : p.cache.v;
+  float* floats = pair < H ? p.cache.k_scale : p.cache.v_scale;
+  const int chunks = p.cache.row_bytes / 16;  // 4 .. 32, a power of two
+  const int rows = 32 / chunks, lane = tid & 31, c = lane % chunks, r = lane / chunks;
+  for (int base = 0; base < n; base += kCompactThreads) {
+    const int m = min(kCompactThreads, n - base);
+    if (base > 0) __syncthreads();  // (every warp is done with the places before)
+    if (tid < m) {
+      const int i = base + tid, from = list[i];
+      longlong2 mv = make_longlong2(-1, -1);
+      if (from != i) {  // (else it is in its place)
+        mv.x = row_of(ctx + from);
+        mv.y = row_of(ctx + i);
+      }
+      sm_move[tid] = mv;
     }
-    return ((long long)block * p.cache.H_kv + g) * BS + t % BS;
-  };
-  const int chunks = p.cache.row_bytes / 16;       // 4 .. 32, a power of two
-  const int rows = kCompactThreads / (2 * chunks); // rows of K and V in one step
-  const int c = tid % chunks, kv = tid / chunks & 1, r = tid / (2 * chunks);
-  uint8_t* cache = kv ? p.cache.v : p.cache.k;
-  float* floats = kv ? p.cache.v_scale : p.cache.k_scale;
-  for (int i0 = 0; i0 < n; i0 += rows * kCompactUnroll) {
-    uint4 x[kCompactUnroll];
-    float f[kCompactUnroll];
-    long long to[kCompactUnroll];
+    __syncthreads();
+    if (pair >= 2 * H) continue;
+    for (int i0 = 0; i0 < m; i0 += rows * kCompactUnroll) {
+      uint4 x[kCompactUnroll];
+      float f[kCompactUnroll];
+      long long to[kCompactUnroll];
 #pragma unroll
-    for (int u = 0; u < kCompactUnroll; ++u) {
-      const int i = i0 + u * rows + r;
-      to[u] = -1;
-      f[u] = 0.f;
-      if (i >= n) continue;
-      const int from = list[i];
-      if (from == i) continue;  // in its place
-      const long long src = row_of(ctx + from), dst = row_of(ctx + i);
-      if (src < 0 || dst < 0) continue;
-      to[u] = dst;
-      x[u] = *(reinterpret_cast<const uint4*>(cache + src * p.cache.row_bytes) + c);
-      if (floats != nullptr && c == 0) f[u] = floats[src];
-    }
-    __syncthreads();  // every row of this pass is read
+      for (int u = 0; u < kCompactUnroll; ++u) {
+        const int i = i0 + u * rows + r;
+        to[u] = -1;
+        f[u] = 0.f;
+        if (i >= m) continue;
+        const longlong2 mv = sm_move[i];
+        if (mv.x < 0 || mv.y < 0) continue;
+        const long long src = mv.x + (long long)g * BS;
+        to[u] = mv.y + (long long)g * BS;
+        x[u] = *(reinterpret_cast<const uint4*>(cache + src * p.cache.row_bytes) + c);
+        if (floats != nullptr && c == 0) f[u] = floats[src];
+      }
+      __syncwarp();  // every row of this pass is read
 #pragma unroll
-    for (int u = 0; u < kCompactUnroll; ++u) {
-      if (to[u] < 0) continue;
-      *(reinterpret_cast<uint4*>(cache + to[u] * p.cache.row_bytes) + c) = x[u];
-      if (floats != nullptr && c == 0) floats[to[u]] = f[u];
+      for (int u = 0; u < kCompactUnroll; ++u) {
+        if (to[u] < 0) continue;
+        *(reinterpret_cast<uint4*>(cache + to[u] * p.cache.row_bytes) + c) = x[u];
+        if (floats != nullptr && c == 0) floats[to[u]] = f[u];
+      }
+      __syncwarp();
     }
   }
 }
@@ -142,7 +162,7 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
 // rows of the last page) is cut into `parts` CTAs by KV heads, the first of which does
 // the table row.
 constexpr int kForkThreads = 256;
-constexpr int kForkUnroll = 8;
+constexpr int kForkUnroll = 4;
 
 struct Fork {
   int parent, child, len, need;
@@ -160,7 +180,7 @@ __device__ __forceinline__ Fork load_fork(const ForkParams& p, int i) {
   return f;
 }
 
-__global__ void __launch_bounds__(kForkThreads) paged_kv_fork_kernel(const ForkParams p, int parts,
+__global__ void __launch_bounds__(kForkThreads, 5) paged_kv_fork_kernel(const ForkParams p, int parts,
                                                                      int count_apart) {
   __shared__ int before[kForkThreads];
   __shared__ int warp_sums[32];
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(kForkThreads) paged_kv_fork_count_kernel(const
 // of lengths and the free count from their writes in place).  A thread has a run of
 // consecutive entries, so ranks need one scan.
 constexpr int kReleaseThreads = 1024;
-constexpr int kReleaseCtas = 8;   // a portable cluster
+constexpr int kReleaseCtas = 16, kPortableCtas = 8;  // the largest cluster, where the device has room
 constexpr int kReleaseBatch = 8;  // entries of a thread in flight
 
 __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const ReleaseParams p) {
@@ -353,79 +373,101 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
       ++start_s;
     }
   }
-  // f(key, block) for each entry of the run, kReleaseBatch of whose reads are in flight
-  // (`more`: a read for each block, all issued before the first f)
-  auto each = [&](auto&& more, auto&& f) {
-    int s = start_s, page = start_p, left = start_left;
-    for (int e = e0; e < e1; e += kReleaseBatch) {
-      int key[kReleaseBatch], block[kReleaseBatch], extra[kReleaseBatch];
+  // The entries of a batch: keys (-1: none) and blocks.  A run of one batch, the usual one, is
+  // looked up once; a longer one in every step.
+  int key[kReleaseBatch], block[kReleaseBatch];
+  int s = start_s, page = start_p, left = start_left;
+  auto look_up = [&](int e) {
 #pragma unroll
-      for (int u = 0; u < kReleaseBatch; ++u) {
+    for (int u = 0; u < kReleaseBatch; ++u) {
+      key[u] = -1;
+      if (e + u >= e1) continue;
+      while (left <= 0 && s + 1 < N) left = span(++s, page);
+      key[u] = s * p.maxb + page;
+      ++page;
+      --left;
+    }
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u) block[u] = key[u] >= 0 ? p.block_tables[key[u]] : -1;
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u) {
+      // (a block that is none has no count and is not freed)
+      if (key[u] < 0) continue;
+      if (block[u] < 0 || (p.block_refs != nullptr && block[u] >= p.num_blocks)) {
+        report(p.status, kBadBlock);
         key[u] = -1;
-        if (e + u >= e1) continue;
-        while (left <= 0 && s + 1 < N) left = span(++s, page);
-        key[u] = s * p.maxb + page;
-        ++page;
-        --left;
       }
-#pragma unroll
-      for (int u = 0; u < kReleaseBatch; ++u)
-        block[u] = key[u] >= 0 ? p.block_tables[key[u]] : -1;
-#pragma unroll
-      for (int u = 0; u < kReleaseBatch; ++u) {
-        // (a block that is none has no count and is not freed)
-        const bool bad = block[u] < 0 || (p.block_refs != nullptr && block[u] >= p.num_blocks);
-        if (bad && key[u] >= 0) report(p.status, kBadBlock);
-        if (bad) key[u] = -1;
-        extra[u] = key[u] >= 0 ? more(block[u]) : 0;
-      }
-#pragma unroll
-      for (int u = 0; u < kReleaseBatch; ++u)
-        if (key[u] >= 0) f(key[u], block[u], extra[u]);
     }
   };
-  auto count_of = [&](int b) -> int { return p.block_refs ? __ldcg(p.block_refs + b) : 0; };
-  auto nothing = [](int) -> int { return 0; };
-  auto step_done = [&] {
-    __threadfence();
-    cluster.sync();
+  const bool once = run <= kReleaseBatch;
+  if (once) look_up(e0);
+  auto each_batch = [&](auto&& f) {
+    s = start_s;
+    page = start_p;
+    left = start_left;
+    for (int e = e0; e < e1; e += kReleaseBatch) {
+      if (!once) look_up(e);
+      f();
+    }
   };
-  auto places = [&](int key, int refs) -> bool {
-    return p.block_refs == nullptr || refs == INT_MIN + key;
+  int refs[kReleaseBatch];
+  auto counts = [&] {  // (written by other SMs: not from the L1)
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u)
+      refs[u] = key[u] >= 0 && p.block_refs != nullptr ? __ldcg(p.block_refs + block[u]) : 0;
+  };
+  auto places = [&](int u) -> bool {
+    return key[u] >= 0 && (p.block_refs == nullptr || refs[u] == INT_MIN + key[u]);
   };
   if (p.block_refs != nullptr) {
-    each(nothing, [&](int, int b, int) { atomicSub(p.block_refs + b, 1); });
-    step_done();
-    each(count_of, [&](int key, int b, int refs) {
-      if (refs < 0) atomicMin(p.block_refs + b, INT_MIN + key);
+    each_batch([&] {
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u)
+        if (key[u] >= 0) atomicSub(p.block_refs + block[u], 1);
     });
-    step_done();
+    cluster.sync();
+    each_batch([&] {
+      counts();
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u)
+        if (refs[u] < 0) atomicMin(p.block_refs + block[u], INT_MIN + key[u]);
+    });
+    cluster.sync();
   }
   int freed = 0, in_cta;
-  each(count_of, [&](int key, int, int refs) { freed += places(key, refs); });
+  each_batch([&] {
+    counts();
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u) freed += places(u);
+  });
   int rank = block_exclusive<kReleaseThreads>(freed, warp_sums, &in_cta);
   if (tid == 0) sm_count = in_cta;
-  step_done();
+  cluster.sync();
   int total = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const int n = *cluster.map_shared_rank(&sm_count, c);
-    if (c < cta) rank += n;
-    total += n;
+  {
+    const int n = tid % 32 < ctas ? *cluster.map_shared_rank(&sm_count, tid % 32) : 0;
+    total = __reduce_add_sync(0xffffffffu, n);
+    rank += __reduce_add_sync(0xffffffffu, tid % 32 < cta ? n : 0);
   }
-  each(count_of, [&](int key, int b, int refs) {
-    // (a block's other entries see the winner's key or the zero written over it: not theirs)
-    if (!places(key, refs)) return;
-    const long long to = (long long)free_count + rank++;
-    if (to < p.free_capacity)
-      p.free_blocks[to] = b;
-    else
-      report(p.status, kBadLength);
-    if (p.block_refs != nullptr) p.block_refs[b] = 0;
+  each_batch([&] {
+    // (looked up again, a block's other entries see the winner's key or the zero written over
+    // it: not theirs)
+    if (!once) counts();
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u) {
+      if (!places(u)) continue;
+      const long long to = (long long)free_count + rank++;
+      if (to < p.free_capacity)
+        p.free_blocks[to] = block[u];
+      else
+        report(p.status, kBadLength);
+      if (p.block_refs != nullptr) p.block_refs[block[u]] = 0;
+    }
   });
   cluster.sync();  // every length, count and sum is read
-  for (int s = cta * kReleaseThreads + tid; s < N; s += ctas * kReleaseThreads) {
-    const int len = clamped_length(p.seq_lens[s], p.maxb, p.BS, nullptr);
-    p.seq_lens_out[s] = min(max(p.keep_lens[s], 0), len);
+  for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
+    const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
+    p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
   }
   if (cta == 0 && tid == 0)
     *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
@@ -441,7 +483,8 @@ cudaLaunchAttribute dependent_launch() {  // may be scheduled while the kernel b
 }  // namespace
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  const long long ctas = (long long)p.num_seqs * p.cache.H_kv;
+  const int per_seq = (2 * p.cache.H_kv + kCompactWarps - 1) / kCompactWarps;
+  const long long ctas = (long long)p.num_seqs * per_seq;
   if (ctas == 0) return cudaSuccess;
   if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
@@ -451,7 +494,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1] = {dependent_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_kv_compact_kernel, p);
+  return cudaLaunchKernelEx(&cfg, paged_kv_compact_kernel, p, per_seq);
 }
 
 cudaError_t launch_fork(const ForkParams& p, int sms, cudaStream_t stream) {
@@ -474,19 +517,39 @@ cudaError_t launch_fork(const ForkParams& p, int sms, cudaStream_t stream) {
 }
 
 cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream) {
-  const long long entries = (long long)p.num_seqs * p.maxb;
-  int ctas = 1;  // by the entries there may be
-  while (ctas < kReleaseCtas && (long long)ctas * 4 * kReleaseThreads < entries) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kReleaseThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2] = {dependent_launch(), {}};
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2] = {{}, dependent_launch()};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
+  auto set_ctas = [&](int n) {
+    cfg.gridDim = dim3((unsigned)n);
+    attr[0].val.clusterDim.x = (unsigned)n;
+  };
+  static std::atomic<int> most[64];  // CTAs of a cluster that this device takes
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int limit = dev >= 0 && dev < 64 ? most[dev].load(std::memory_order_acquire) : 0;
+  if (limit == 0) {
+    e = cudaFuncSetAttribute(paged_kv_release_kernel,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    int clusters = 0;
+    set_ctas(kReleaseCtas);
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&clusters, paged_kv_release_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    limit = clusters > 0 ? kReleaseCtas : kPortableCtas;
+    if (dev >= 0 && dev < 64) most[dev].store(limit, std::memory_order_release);
+  }
+  const long long entries = (long long)p.num_seqs * p.maxb;
+  int ctas = 1;  // by the entries there may be
+  while (ctas < limit && (long long)ctas * 4 * kReleaseThreads < entries) ctas *= 2;
+  set_ctas(ctas);
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, paged_kv_release_kernel, p);
 }
