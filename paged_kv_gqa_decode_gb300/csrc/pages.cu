@@ -20,7 +20,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kBadBlock = 1, kBadLength = 2;
+constexpr int kBadBlock = 1, kBadLength = 2, kTimeout = 4;
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status != nullptr) atomicOr(status, bits);
@@ -30,6 +30,14 @@ __device__ __forceinline__ int clamped_length(int L, int maxb, int BS, int32_t* 
   const long long cap = (long long)maxb * BS;
   if (L < 0 || L > cap) report(status, kBadLength);
   return (int)min(max((long long)L, 0LL), cap);
+}
+
+// The two halves of the cluster's barrier.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Exclusive sum over the block's threads; the block's total in every thread.  `warp_sums`
@@ -157,12 +165,16 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
 // ------------------------------------------------------------------ forks
 //
 // Fork i needs a fresh block when its parent's last page is not full; R_i of the forks
-// before it do, and it takes the stack entry free_count - 1 - R_i.  Every CTA scans the
-// parents' lengths; the work of a fork (its table row, the counts of the shared blocks, the
-// rows of the last page) is cut into `parts` CTAs by KV heads, the first of which does
-// the table row.
-constexpr int kForkThreads = 256;
-constexpr int kForkUnroll = 4;
+// before it do, and it takes the stack entry free_count - 1 - R_i.  The runs to copy, one for
+// each fork, tensor and KV head, are dealt to one CTA an SM in equal consecutive shares.  A
+// CTA scans the parents' lengths once and looks all its forks up at once, a thread each; then each
+// warp moves pieces of 4 KB by bulk copies into its place in shared memory and out of it,
+// with no dependent read in between (512 forks of 64 prompts, 33 MB written: copied
+// through registers, eight 16-byte chunks a thread in flight, 17 us).  The CTA with a fork's
+// first run does its table row and the counts of its blocks.
+constexpr int kForkThreads = 512, kForkWarps = kForkThreads / 32;
+constexpr int kForkPiece = 4096;
+constexpr size_t kForkSmem = (size_t)kForkWarps * (kForkPiece + 8);
 
 struct Fork {
   int parent, child, len, need;
@@ -180,18 +192,29 @@ __device__ __forceinline__ Fork load_fork(const ForkParams& p, int i) {
   return f;
 }
 
-__global__ void __launch_bounds__(kForkThreads, 5) paged_kv_fork_kernel(const ForkParams p, int parts,
-                                                                     int count_apart) {
+__global__ void __launch_bounds__(kForkThreads, 1)
+    paged_kv_fork_kernel(const ForkParams p, int share, int count_apart) {
+  extern __shared__ __align__(128) uint8_t fork_smem[];
   __shared__ int before[kForkThreads];
   __shared__ int warp_sums[32];
+  // forks of a batch: blocks copied from and to (-1: no copy) and the tokens of the last page
+  __shared__ int sm_from[kForkThreads], sm_to[kForkThreads], sm_tail[kForkThreads];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* place = fork_smem + warp * kForkPiece;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(fork_smem + kForkWarps * kForkPiece) + warp;
+  if (lane == 0) {
+    mbar_init(full_bar, 1);
+    fence_barrier_init();
+  }
   griddep_wait();
   griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
-  const int tid = threadIdx.x, n = p.num_forks, BS = p.cache.BS;
+  const int n = p.num_forks, BS = p.cache.BS;
   const int free_count = min(max(*p.free_count, 0), p.free_capacity);
   const int per = (n + kForkThreads - 1) / kForkThreads;  // forks that a thread sums
   const int i0 = (int)min((long long)n, (long long)tid * per);
   const int i1 = (int)min((long long)n, (long long)i0 + per);
   int needs = 0, invalid = 0;
+#pragma unroll 4
   for (int i = i0; i < i1; ++i) {
     const Fork f = load_fork(p, i);
     needs += f.need;
@@ -199,91 +222,141 @@ __global__ void __launch_bounds__(kForkThreads, 5) paged_kv_fork_kernel(const Fo
   }
   int total, bad = 0;
   before[tid] = block_exclusive<kForkThreads>(needs, warp_sums, &total);
-  if (blockIdx.x == 0) block_exclusive<kForkThreads>(invalid, warp_sums, &bad);
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0) {
-    if (!count_apart) *p.free_count_out = free_count - min(total, free_count);
-    if (p.refused != nullptr) *p.refused = bad + max(total - free_count, 0);
-  }
-  const long long units = (long long)n * parts;
-  for (long long unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int i = (int)(unit / parts), part = (int)(unit - (long long)i * parts);
-    const Fork f = load_fork(p, i);
-    int rank = before[i / per];
-    for (int j = i / per * per; j < i; ++j) rank += load_fork(p, j).need;
-    const bool given = f.valid && (!f.need || rank < free_count);
-    if (!given) {
-      if (part == 0 && tid == 0) {
-        if (!f.valid) report(p.status, kBadLength);
-        if (f.child >= 0 && f.child < p.num_rows && f.child != f.parent) p.seq_lens[f.child] = 0;
-      }
-      continue;
+  if (blockIdx.x == 0) {
+    block_exclusive<kForkThreads>(invalid, warp_sums, &bad);
+    if (tid == 0) {
+      if (!count_apart) *p.free_count_out = free_count - min(total, free_count);
+      if (p.refused != nullptr) *p.refused = bad + max(total - free_count, 0);
     }
-    const int full = f.len / BS, tail = f.len - full * BS;
-    const int32_t* from = p.block_tables + (size_t)f.parent * p.maxb;
-    int32_t* to = p.block_tables + (size_t)f.child * p.maxb;
-    const int fresh = f.need ? p.free_blocks[free_count - 1 - rank] : -1;
-    if (part == 0) {
-      for (int j = tid; j < full; j += kForkThreads) {
-        const int b = from[j];
-        to[j] = b;
-        if (b >= 0 && b < p.cache.num_blocks)
-          atomicAdd(p.block_refs + b, 1);
+  }
+  // ---- this CTA's runs: run r is fork r / pairs, tensor and KV head r % pairs
+  const int H = p.cache.H_kv, pairs = 2 * H;
+  const int runs = n * pairs;  // (the host has seen to it that it fits)
+  const int first = (int)min((long long)runs, (long long)blockIdx.x * share);
+  const int last = (int)min((long long)runs, (long long)first + share);
+  const long long page = (long long)BS * p.cache.row_bytes;
+  const int pieces = max(1, (int)page / kForkPiece);  // of a run at most: 1, 2 or 4
+  const int shift = pieces == 4 ? 2 : pieces - 1;
+  uint32_t phase = 0;
+  for (int f0 = first / pairs; (long long)f0 * pairs < last; f0 += kForkThreads) {
+    const int r0 = max(first, f0 * pairs);  // this batch's runs
+    const int r1 = (int)min((long long)last, ((long long)f0 + kForkThreads) * pairs);
+    __syncthreads();  // (`before` is written; the batch before is done with)
+    if (((long long)f0 + tid) * pairs < last) {
+      const int i = f0 + tid;
+      const Fork f = load_fork(p, i);
+      int rank = before[i / per];
+      for (int j = i / per * per; j < i; ++j) rank += load_fork(p, j).need;
+      const bool given = f.valid && (!f.need || rank < free_count);
+      const int full = f.len / BS;
+      int from = -1, to = -1;
+      if (given && f.need) {
+        from = p.block_tables[(size_t)f.parent * p.maxb + full];
+        to = p.free_blocks[free_count - 1 - rank];
+      }
+      if (i * pairs >= first) {  // the fork's first run is this CTA's
+        if (given) {
+          if (f.need) p.block_tables[(size_t)f.child * p.maxb + full] = to;
+          if (p.seq_lens[f.parent] != f.len) report(p.status, kBadLength);
+        } else if (!f.valid) {
+          report(p.status, kBadLength);
+        }
+        if (f.child >= 0 && f.child < p.num_rows && f.child != f.parent)
+          p.seq_lens[f.child] = given ? f.len : 0;
+      }
+      if (given && f.need &&
+          (from < 0 || from >= p.cache.num_blocks || to < 0 || to >= p.cache.num_blocks)) {
+        report(p.status, kBadBlock);
+        from = -1;
+      }
+      sm_from[tid] = from;
+      sm_to[tid] = to;
+      sm_tail[tid] = given ? f.len - full * BS : -1;  // (-1: no table row either)
+    }
+    __syncthreads();
+    // ---- the rows of the last pages: a warp's first piece is under way while it works on
+    // the table rows
+    struct Piece {
+      long long from, to;  // KV head pages
+      uint8_t* cache;
+      float* floats;
+      int at, bytes, tail;
+    };
+    const long long most = (long long)(r1 - r0) * pieces;
+    auto find = [&](long long& q, Piece& x) -> bool {  // this warp's next one from place q on
+      for (; q < most; q += kForkWarps) {
+        // (pieces is a power of two, at most four)
+        const int r = r0 + (int)(q >> shift), piece = (int)q & (pieces - 1);
+        const int k = (int)((uint32_t)r / (uint32_t)pairs) - f0, pair = r - (k + f0) * pairs;
+        x.tail = sm_tail[k];
+        x.at = piece * kForkPiece;
+        x.bytes = min(kForkPiece, x.tail * p.cache.row_bytes - x.at);
+        if (sm_from[k] < 0 || x.bytes <= 0) continue;
+        const int h = pair < H ? pair : pair - H;
+        x.cache = pair < H ? p.cache.k : p.cache.v;
+        x.floats = pair < H ? p.cache.k_scale : p.cache.v_scale;
+        x.from = (long long)sm_from[k] * H + h;
+        x.to = (long long)sm_to[k] * H + h;
+        return true;
+      }
+      return false;
+    };
+    auto load = [&](const Piece& x) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(full_bar, (uint32_t)x.bytes);
+        bulk_load(place, x.cache + x.from * page + x.at, (uint32_t)x.bytes, full_bar);
+      }
+      if (x.floats != nullptr && x.at == 0 && lane < x.tail)
+        x.floats[x.to * BS + lane] = x.floats[x.from * BS + lane];
+    };
+    long long q = warp;
+    Piece x;
+    bool some = find(q, x);
+    if (some) load(x);
+    // ---- the table rows and the counts of the blocks in them: the warps shared out among the
+    // forks whose first run is this CTA's
+    const int own = max(f0, first / pairs + (first % pairs != 0));
+    const int end = min(last / pairs + (last % pairs != 0), f0 + kForkThreads);
+    const int forks = max(0, end - own);
+    const int each = max(1, kForkWarps / max(forks, 1));  // warps of a fork
+    for (int k = warp / each; k < forks; k += kForkWarps / each) {
+      if (sm_tail[own - f0 + k] < 0) continue;
+      const Fork f = load_fork(p, own + k);
+      const int32_t* from = p.block_tables + (size_t)f.parent * p.maxb;
+      int32_t* to = p.block_tables + (size_t)f.child * p.maxb;
+#pragma unroll 4
+      for (int j = warp % each * 32 + lane; j < f.len / BS; j += each * 32) {
+        const int block = from[j];
+        to[j] = block;
+        if (block >= 0 && block < p.cache.num_blocks)
+          atomicAdd(p.block_refs + block, 1);
         else
           report(p.status, kBadBlock);
       }
-      if (tid == 0) {
-        if (f.need) to[full] = fresh;
-        p.seq_lens[f.child] = f.len;
-        const int held = p.seq_lens[f.parent];
-        if (held != f.len) report(p.status, kBadLength);
-      }
     }
-    if (!f.need) continue;
-    const int last = from[full];
-    if (last < 0 || last >= p.cache.num_blocks || fresh < 0 || fresh >= p.cache.num_blocks) {
-      if (tid == 0) report(p.status, kBadBlock);
-      continue;
-    }
-    // ---- the rows of the last page: of each tensor and KV head one run of `run` chunks
-    const int H = p.cache.H_kv, pairs = 2 * H;
-    const int a = (int)((long long)pairs * part / parts);
-    const int b = (int)((long long)pairs * (part + 1) / parts);
-    const uint32_t run = (uint32_t)tail * p.cache.row_bytes / 16;
-    const uint32_t most = (uint32_t)(b - a) * run;
-    const long long page = (long long)BS * p.cache.row_bytes;
-    for (uint32_t c0 = tid; c0 < most; c0 += kForkThreads * kForkUnroll) {
-      uint4 x[kForkUnroll];
-      uint4* dst[kForkUnroll];
-#pragma unroll
-      for (int u = 0; u < kForkUnroll; ++u) {
-        const uint32_t c = c0 + u * kForkThreads;
-        dst[u] = nullptr;
-        if (c >= most) continue;
-        const int pair = a + (int)(c / run), at = (int)(c % run);
-        uint8_t* cache = pair < H ? p.cache.k : p.cache.v;
-        const int h = pair < H ? pair : pair - H;
-        x[u] = *(reinterpret_cast<const uint4*>(cache + ((long long)last * H + h) * page) + at);
-        dst[u] = reinterpret_cast<uint4*>(cache + ((long long)fresh * H + h) * page) + at;
+    while (some) {
+      if (lane == 0) {
+        if (mbar_wait(full_bar, phase)) {
+          bulk_store(x.cache + x.to * page + x.at, place, (uint32_t)x.bytes);
+        } else {  // never expected: a copy that may still land
+          report(p.status, kTimeout);
+          mbar_wait(full_bar, phase);
+        }
+        bulk_store_read();  // the place is free again
       }
-#pragma unroll
-      for (int u = 0; u < kForkUnroll; ++u)
-        if (dst[u] != nullptr) *dst[u] = x[u];
-    }
-    if (p.cache.k_scale != nullptr) {
-      for (int c = tid; c < (b - a) * tail; c += kForkThreads) {
-        const int pair = a + c / tail, at = c % tail;
-        float* floats = pair < H ? p.cache.k_scale : p.cache.v_scale;
-        const int h = pair < H ? pair : pair - H;
-        floats[((long long)fresh * H + h) * BS + at] = floats[((long long)last * H + h) * BS + at];
-      }
+      phase ^= 1u;
+      __syncwarp();
+      q += kForkWarps;
+      some = find(q, x);
+      if (some) load(x);
     }
   }
+  if (lane == 0) bulk_store_done();
 }
 
 // The free count where it is updated in place: the kernel above, whose CTAs all read the
 // old one, has completed.
-__global__ void __launch_bounds__(kForkThreads) paged_kv_fork_count_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kForkThreads, 1) paged_kv_fork_count_kernel(const ForkParams p) {
   __shared__ int warp_sums[32];
   griddep_wait();
   griddep_launch_dependents();
@@ -449,6 +522,20 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
     total = __reduce_add_sync(0xffffffffu, n);
     rank += __reduce_add_sync(0xffffffffu, tid % 32 < cta ? n : 0);
   }
+  // Every CTA has read the lengths and the free count by now, except those of a long run,
+  // which reads the lengths once more.  No CTA may exit before its count is read.
+  auto write_lengths = [&] {
+    for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
+      const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
+      p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
+    }
+    if (cta == 0 && tid == 0)
+      *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
+  };
+  if (once) {
+    cluster_arrive();
+    write_lengths();
+  }
   each_batch([&] {
     // (looked up again, a block's other entries see the winner's key or the zero written over
     // it: not theirs)
@@ -464,13 +551,9 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
       if (p.block_refs != nullptr) p.block_refs[block[u]] = 0;
     }
   });
-  cluster.sync();  // every length, count and sum is read
-  for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
-    const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
-    p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
-  }
-  if (cta == 0 && tid == 0)
-    *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
+  if (!once) cluster_arrive();
+  cluster_wait();
+  if (!once) write_lengths();
 }
 
 cudaLaunchAttribute dependent_launch() {  // may be scheduled while the kernel before it ends
@@ -498,21 +581,30 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_fork(const ForkParams& p, int sms, cudaStream_t stream) {
-  // parts of a fork: a power of two, until the CTAs are about four an SM
-  int parts = 1;
-  while (parts < 2 * p.cache.H_kv && (long long)p.num_forks * parts * 2 <= 4LL * sms) parts *= 2;
-  const long long units = (long long)p.num_forks * parts, most = 8LL * sms;
+  static std::atomic<bool> limit_raised[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !limit_raised[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(paged_kv_fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)kForkSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) limit_raised[dev].store(true, std::memory_order_release);
+  }
+  const int runs = 2 * p.num_forks * p.cache.H_kv, share = runs < sms ? 1 : (runs + sms - 1) / sms;
   const int apart = p.free_count_out == p.free_count;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units < 1 ? 1 : units < most ? units : most));
+  cfg.gridDim = dim3((unsigned)(runs < 1 ? 1 : (runs + share - 1) / share));
   cfg.blockDim = dim3(kForkThreads);
+  cfg.dynamicSmemBytes = kForkSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1] = {dependent_launch()};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, paged_kv_fork_kernel, p, parts, apart);
+  e = cudaLaunchKernelEx(&cfg, paged_kv_fork_kernel, p, share, apart);
   if (e != cudaSuccess || !apart) return e;
   cfg.gridDim = dim3(1);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_kv_fork_count_kernel, p);
 }
 

@@ -163,7 +163,9 @@ int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
   int rc = cache_sizes(k_scale, v_scale, H_kv, head_dim, max_blocks_per_seq, block_size,
                        num_blocks);
   if (rc != PAGED_ATTN_OK) return rc;
-  if (num_forks < 0 || num_rows < 0 || free_capacity < 0) return PAGED_ATTN_ERR_SIZES;
+  if (num_forks < 0 || num_rows < 0 || free_capacity < 0 ||
+      2LL * num_forks * H_kv > 0x3fffffffLL)
+    return PAGED_ATTN_ERR_SIZES;
   if (!aligned4(free_count) || !aligned4(free_count_out) ||
       (refused != nullptr && !aligned4(refused)))
     return PAGED_ATTN_ERR_POINTER;
