@@ -556,8 +556,9 @@ PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int to
  *
  * Cache rows that no row sees, those of padding nodes too, may hold anything, NaN
  * included; a row that only some of a sequence's rows see must be finite for the others'
- * sake.  Everything else, workspace and its size too, as paged_attn_decode_multi_mods.
- * Returns PAGED_ATTN_ERR_SIZES for mask_words out of range.
+ * sake.  Everything else as paged_attn_decode_multi_mods; workspace: as there,
+ * paged_attn_tree_workspace_bytes(...) bytes.  Returns PAGED_ATTN_ERR_SIZES for mask_words
+ * out of range.
  */
 PAGED_ATTN_API int paged_attn_decode_tree(
     const void* q, const void* k_cache, const void* v_cache, void* out,
@@ -566,6 +567,10 @@ PAGED_ATTN_API int paged_attn_decode_tree(
     int H_kv, int head_dim, int max_blocks_per_seq, int block_size, float scale, float softcap,
     const float* alibi_slopes, int window, const int32_t* prefix_lens, void* workspace,
     size_t workspace_bytes, void* stream);
+
+PAGED_ATTN_API size_t paged_attn_tree_workspace_bytes(int num_seqs, int total_q, int H_q,
+                                                      int H_kv, int head_dim,
+                                                      int max_blocks_per_seq, int block_size);
 
 /*
  * Decode of a batch whose sequences share long prefixes (system prompts, a

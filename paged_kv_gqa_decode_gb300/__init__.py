@@ -42,6 +42,7 @@ __all__ = [
     "paged_kv_assign",
     "paged_kv_append_slots",
     "paged_attn_decode_tree",
+    "paged_attn_tree_workspace_bytes",
     "paged_kv_rope_append_slots",
     "paged_kv_compact",
     "paged_kv_fork",
@@ -85,6 +86,7 @@ EXPORTED_SYMBOLS = (
     "paged_kv_assign",
     "paged_kv_append_slots",
     "paged_attn_decode_tree",
+    "paged_attn_tree_workspace_bytes",
     "paged_kv_rope_append_slots",
     "paged_kv_compact",
     "paged_kv_fork",
@@ -186,6 +188,8 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
         lib.paged_attn_decode_tree.argtypes = ([P] * 6 + [I, P, P] + [I] * 7 +
                                                [F, F, P, I, P, P, SZ, P])
         lib.paged_attn_decode_tree.restype = I
+        lib.paged_attn_tree_workspace_bytes.argtypes = [I] * 7
+        lib.paged_attn_tree_workspace_bytes.restype = SZ
         lib.paged_kv_rope_append_slots.argtypes = ([P, P, P, LL, LL, LL] + [P] * 7 + [I, P, P] +
                                                    [I, I, I, P, P, F] + [I] * 5 + [LL, P])
         lib.paged_kv_rope_append_slots.restype = I
@@ -887,10 +891,17 @@ def paged_attn_decode_tree(q, k_cache, v_cache, qo_indptr, tree_mask, block_tabl
     of word j // 32 of a row is set where it sees drafted token j of its sequence (a node
     of a tree: itself and its ancestors).  A row's position is the tokens before the tree
     plus the drafted ones it sees, less one; the other options as
-    paged_attn_decode_multi_mods (``workspace``: paged_attn_multi_mods_workspace_bytes)."""
+    paged_attn_decode_multi_mods (``workspace``: paged_attn_tree_workspace_bytes)."""
     return (_native or _load_native()).decode_tree(
         q, k_cache, v_cache, qo_indptr, tree_mask, block_tables, seq_lens, scale, softcap,
         alibi_slopes, window, prefix_lens, out, workspace, stream)
+
+
+def paged_attn_tree_workspace_bytes(num_seqs: int, total_q: int, H_q: int, H_kv: int,
+                                    head_dim: int, max_blocks_per_seq: int,
+                                    block_size: int) -> int:
+    return int(load().paged_attn_tree_workspace_bytes(num_seqs, total_q, H_q, H_kv, head_dim,
+                                                      max_blocks_per_seq, block_size))
 
 
 def paged_kv_rope_append_slots(q, k_new, v_new, k_cache, v_cache, slot_map, positions, cos_sin,

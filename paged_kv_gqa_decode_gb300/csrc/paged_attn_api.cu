@@ -842,6 +842,36 @@ int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,
   return s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
+// The same for trees, whose sequences have nearly the same number of rows, so that the pieces
+// can be counted (a tile of rows for each started 128 or 256 of the mean), and often the
+// same length.  Near 1.75 CTAs a place it takes the number of parts that fills the
+// last round of CTAs best (trees over four contexts of 100000 tokens, head_dim 256, 32 pieces
+// on 152 places, 5 / 7 / 9 / 10 / 12 / 14 / 19 parts 584 / 439 / 371 / 473 / 427 / 408 / 459
+// us).  No more than the block tables have pairs of token tiles: with one part there is no
+// merge (two chats of up to 112 tokens 11.9 -> 8.9 us).
+int tree_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int maxb, int BS, int sms) {
+  const long long rows = (long long)total_q * (H_q / H_kv);
+  const int teams = tile_teams(D, rows, num_seqs, H_kv, sms), tile = 128 * teams;
+  const long long places = (D < 256 && teams == 1 ? 2 : 1) * (long long)sms;
+  const long long mean = (rows + num_seqs - 1) / num_seqs;
+  const long long pieces = (mean + tile - 1) / tile * num_seqs * H_kv;
+  const int BN = teams == 2 ? 128 : 64;  // tokens of a tile
+  long long most = ((long long)maxb * BS + BN - 1) / BN / 2;
+  if (most > kMaxSplits) most = kMaxSplits;
+  if (pieces >= places || most <= 1) return 1;
+  const long long near = (7 * places / 4 + pieces / 2) / pieces;
+  long long best = near, best_waves = 0;
+  for (long long s = near * 3 / 4 > 1 ? near * 3 / 4 : 1; s <= near + near / 3; ++s) {
+    // rounds of CTAs a part: waves(s) / s, compared as fractions
+    const long long waves = (pieces * s + places - 1) / places;
+    if (best_waves == 0 || waves * best < best_waves * s) {
+      best = s;
+      best_waves = waves;
+    }
+  }
+  return (int)(best < most ? best : most);
+}
+
 // Workspace of the partial states: (m, l) of every part and row, then their o.
 size_t tile_part_bytes(int D, int total_q, int H_q, int splits) {
   const size_t rows = (size_t)splits * total_q * H_q;
@@ -915,11 +945,10 @@ void set_parts(TileParams* t, uint8_t* base) {
   t->part_o = reinterpret_cast<float*>(base + round_up(rows * 8, kWsAlign));
 }
 
-// A row-tile launch of whole sequences (everything of `t` set but its parts and status
-// word), and the merge where the token ranges are split.
+// A row-tile launch of whole sequences (everything of `t` set but its status word and its
+// parts' places), and the merge where the token ranges are split.
 int run_row_tiles(int D, const DeviceInfo& di, TileParams& t, const void* k_cache,
                   const void* v_cache, void* workspace, size_t workspace_bytes, cudaStream_t st) {
-  t.splits = tile_splits(D, t.total_q, t.num_seqs, t.H_q, t.H_kv, di.sms);
   t.single = t.splits == 1 ? 1 : 0;
   const size_t parts = t.single ? 0 : tile_part_bytes(D, t.total_q, t.H_q, t.splits);
   void* ws = nullptr;
@@ -1390,8 +1419,23 @@ int paged_attn_decode_multi_mods(const void* q, const void* k_cache, const void*
   t.window = window;
   t.prefix_lens = prefix_lens;
   t.doc_starts = doc_starts;
+  t.splits = tile_splits(head_dim, total_q, num_seqs, H_q, H_kv, di.sms);
   return run_row_tiles(head_dim, di, t, k_cache, v_cache, workspace, workspace_bytes,
                        static_cast<cudaStream_t>(stream));
+}
+
+size_t paged_attn_tree_workspace_bytes(int num_seqs, int total_q, int H_q, int H_kv,
+                                       int head_dim, int max_blocks_per_seq, int block_size) {
+  if (validate_sizes(num_seqs, H_q, H_kv, head_dim, max_blocks_per_seq, block_size) !=
+          PAGED_ATTN_OK ||
+      total_q < 0 || !tile_sizes_ok(total_q, num_seqs, H_q, H_kv, head_dim))
+    return 0;
+  DeviceInfo di;
+  if (device_info(&di) != PAGED_ATTN_OK) return 0;
+  if (num_seqs == 0 || total_q == 0) return counters_end(di);
+  const int splits =
+      tree_splits(head_dim, total_q, num_seqs, H_q, H_kv, max_blocks_per_seq, block_size, di.sms);
+  return counters_end(di) + (splits > 1 ? tile_part_bytes(head_dim, total_q, H_q, splits) : 0);
 }
 
 int paged_attn_decode_tree(const void* q, const void* k_cache, const void* v_cache, void* out,
@@ -1422,6 +1466,8 @@ int paged_attn_decode_tree(const void* q, const void* k_cache, const void* v_cac
   t.prefix_lens = prefix_lens;
   t.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
   t.mask_words = mask_words;
+  t.splits = tree_splits(head_dim, total_q, num_seqs, H_q, H_kv, max_blocks_per_seq, block_size,
+                         di.sms);
   return run_row_tiles(head_dim, di, t, k_cache, v_cache, workspace, workspace_bytes,
                        static_cast<cudaStream_t>(stream));
 }

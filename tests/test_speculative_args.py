@@ -213,3 +213,9 @@ def test_the_binding_refuses_other_releases(kw, name):
                 free_count=torch.zeros(1, dtype=I32), block_size=16)
     with pytest.raises(ValueError, match=name):
         pa.paged_kv_release(**dict(good, **kw))
+
+
+@pytest.mark.parametrize("args", [(4, -1, 8, 2, 128, 8, 16), (4, 5, 8, 2, 128, 8, 8), (4, 5, 6, 4, 128, 8, 16),
+                                  (-1, 5, 8, 2, 128, 8, 16)])
+def test_the_workspace_query_rejects_bad_sizes(lib, args):
+    assert lib.paged_attn_tree_workspace_bytes(*args) == 0

@@ -162,7 +162,7 @@ def test_other_scales(scale):
 
 
 def test_a_chain_equals_the_causal_call():
-    lens, ql = [300, 65, 40], [33, 64, 1]
+    lens, ql = [300 + s for s in range(200)], [33 if s % 2 else 64 for s in range(200)]  # (neither is split)
     w, q, qo, mask, bt = make(lens, ql, 8, 2, 128, 16, 15, kind="chain")
     a = pa.paged_attn_decode_tree(q, w.k_cache, w.v_cache, i32(qo), i32(mask), w.block_tables, w.seq_lens, w.scale)
     b = pa.paged_attn_decode_multi_mods(q, w.k_cache, w.v_cache, i32(qo), w.block_tables, w.seq_lens, w.scale)
@@ -182,7 +182,7 @@ def test_rows_outside_the_offsets_are_left():
 
 def test_captured_replayed_on_another_stream_with_new_trees():
     w, q, qo, mask, bt = make([200, 90], [20, 31], 8, 2, 128, 16, 17)
-    need = pa.paged_attn_multi_mods_workspace_bytes(2, q.shape[0], 8, 2, 128, w.block_tables.shape[1], 16)
+    need = pa.paged_attn_tree_workspace_bytes(2, q.shape[0], 8, 2, 128, w.block_tables.shape[1], 16)
     ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
     d_mask, d_qo, out = i32(mask), i32(qo), torch.empty_like(q)
     st = torch.cuda.Stream()
