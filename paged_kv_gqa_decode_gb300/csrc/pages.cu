@@ -383,6 +383,10 @@ __global__ void __launch_bounds__(kForkThreads, 1) paged_kv_fork_count_kernel(co
 //   3. entries with refs[b] == INT_MIN + e are counted, the counts summed
 //   4. those write their block to the stack at their rank and refs[b] = 0
 //
+// When every entry finds a count of zero in step 1 (nothing released is shared: all blocks are
+// distinct), each one places its block, its rank is its place among the entries, and steps 2
+// and 3 fall away.
+//
 // The grid is one thread-block cluster, whose barrier separates the steps (and all reads
 // of lengths and the free count from their writes in place).  A thread has a run of
 // consecutive entries, so ranks need one scan.
@@ -393,11 +397,11 @@ constexpr int kReleaseBatch = 8;  // entries of a thread in flight
 __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const ReleaseParams p) {
   __shared__ int before[kReleaseThreads];  // entries ahead of each thread's sequences
   __shared__ int warp_sums[32];
-  __shared__ int sm_count;
+  __shared__ int sm_count, sm_plain;
   griddep_wait();
   griddep_launch_dependents();  // (after the wait: what is ahead of this launch is complete)
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, N = p.num_seqs;
+  const int tid = threadIdx.x, lane = tid & 31, N = p.num_seqs;
   const int ctas = (int)gridDim.x, cta = (int)blockIdx.x;
   const int free_count = min(max(*p.free_count, 0), p.free_capacity);
   const int per = (N + kReleaseThreads - 1) / kReleaseThreads;
@@ -449,7 +453,7 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   // The entries of a batch: keys (-1: none) and blocks.  A run of one batch, the usual one, is
   // looked up once; a longer one in every step.
   int key[kReleaseBatch], block[kReleaseBatch];
-  int s = start_s, page = start_p, left = start_left;
+  int s = start_s, page = start_p, left = start_left, e_at = 0;  // (e_at: first of the batch)
   auto look_up = [&](int e) {
 #pragma unroll
     for (int u = 0; u < kReleaseBatch; ++u) {
@@ -478,8 +482,8 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
     s = start_s;
     page = start_p;
     left = start_left;
-    for (int e = e0; e < e1; e += kReleaseBatch) {
-      if (!once) look_up(e);
+    for (e_at = e0; e_at < e1; e_at += kReleaseBatch) {
+      if (!once) look_up(e_at);
       f();
     }
   };
@@ -492,21 +496,78 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   auto places = [&](int u) -> bool {
     return key[u] >= 0 && (p.block_refs == nullptr || refs[u] == INT_MIN + key[u]);
   };
-  if (p.block_refs != nullptr) {
+  // A value of each CTA's shared memory: lane c of a warp gets CTA c's.
+  auto of_cta = [&](int* x, int none) -> int {
+    return lane < ctas ? *cluster.map_shared_rank(x, lane) : none;
+  };
+  // ---- 1.
+  int old[kReleaseBatch];  // counts before, of a run of one batch
+  bool plain = true;
+  each_batch([&] {
+    int was[kReleaseBatch];
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u)
+      was[u] = key[u] >= 0 && p.block_refs != nullptr ? atomicSub(p.block_refs + block[u], 1) : 0;
+#pragma unroll
+    for (int u = 0; u < kReleaseBatch; ++u) {
+      old[u] = was[u];
+      // (an entry that is none would leave a gap in the ranks)
+      if (was[u] != 0 || (key[u] < 0 && e_at + u < e1)) plain = false;
+    }
+  });
+  plain = __syncthreads_and(plain) != 0;
+  if (tid == 0) sm_plain = plain;
+  cluster.sync();
+  // (the same in all CTAs, whatever the caller does to the lengths meanwhile: they all read
+  // the same words)
+  plain = __all_sync(0xffffffffu, of_cta(&sm_plain, 1) != 0) != 0;
+  // What all paths end with: every CTA has read the lengths and the free count by now, except
+  // those of a long run, which reads the lengths once more.
+  auto write_lengths = [&](int total) {
+    for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
+      const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
+      p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
+    }
+    if (cta == 0 && tid == 0)
+      *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
+  };
+  auto place = [&](int u, int rank) {
+    const long long to = (long long)free_count + rank;
+    if (to < p.free_capacity)
+      p.free_blocks[to] = block[u];
+    else
+      report(p.status, kBadLength);
+    if (p.block_refs != nullptr) p.block_refs[block[u]] = 0;
+  };
+  if (plain) {
+    if (once) {
+      cluster_arrive();
+      write_lengths(all);
+    }
     each_batch([&] {
 #pragma unroll
       for (int u = 0; u < kReleaseBatch; ++u)
-        if (key[u] >= 0) atomicSub(p.block_refs + block[u], 1);
+        if (key[u] >= 0) place(u, e_at + u);
     });
-    cluster.sync();
+    if (!once) cluster_arrive();
+    cluster_wait();  // (no CTA exits before its word is read)
+    if (!once) write_lengths(all);
+    return;
+  }
+  // ---- 2.
+  if (p.block_refs != nullptr) {
     each_batch([&] {
-      counts();
+      // (a count that was zero or less before is below zero now)
+#pragma unroll
+      for (int u = 0; u < kReleaseBatch; ++u)
+        refs[u] = key[u] < 0 ? 0 : once && old[u] <= 0 ? -1 : __ldcg(p.block_refs + block[u]);
 #pragma unroll
       for (int u = 0; u < kReleaseBatch; ++u)
         if (refs[u] < 0) atomicMin(p.block_refs + block[u], INT_MIN + key[u]);
     });
     cluster.sync();
   }
+  // ---- 3.
   int freed = 0, in_cta;
   each_batch([&] {
     counts();
@@ -516,44 +577,26 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   int rank = block_exclusive<kReleaseThreads>(freed, warp_sums, &in_cta);
   if (tid == 0) sm_count = in_cta;
   cluster.sync();
-  int total = 0;
-  {
-    const int n = tid % 32 < ctas ? *cluster.map_shared_rank(&sm_count, tid % 32) : 0;
-    total = __reduce_add_sync(0xffffffffu, n);
-    rank += __reduce_add_sync(0xffffffffu, tid % 32 < cta ? n : 0);
-  }
-  // Every CTA has read the lengths and the free count by now, except those of a long run,
-  // which reads the lengths once more.  No CTA may exit before its count is read.
-  auto write_lengths = [&] {
-    for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
-      const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
-      p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
-    }
-    if (cta == 0 && tid == 0)
-      *p.free_count_out = (int)min((long long)free_count + total, (long long)p.free_capacity);
-  };
+  const int in_it = of_cta(&sm_count, 0);
+  const int total = __reduce_add_sync(0xffffffffu, in_it);
+  rank += __reduce_add_sync(0xffffffffu, lane < cta ? in_it : 0);
   if (once) {
     cluster_arrive();
-    write_lengths();
+    write_lengths(total);
   }
+  // ---- 4.
   each_batch([&] {
     // (looked up again, a block's other entries see the winner's key or the zero written over
     // it: not theirs)
     if (!once) counts();
 #pragma unroll
     for (int u = 0; u < kReleaseBatch; ++u) {
-      if (!places(u)) continue;
-      const long long to = (long long)free_count + rank++;
-      if (to < p.free_capacity)
-        p.free_blocks[to] = block[u];
-      else
-        report(p.status, kBadLength);
-      if (p.block_refs != nullptr) p.block_refs[block[u]] = 0;
+      if (places(u)) place(u, rank++);
     }
   });
   if (!once) cluster_arrive();
   cluster_wait();
-  if (!once) write_lengths();
+  if (!once) write_lengths(total);
 }
 
 cudaLaunchAttribute dependent_launch() {  // may be scheduled while the kernel before it ends
