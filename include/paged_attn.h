@@ -720,7 +720,8 @@ PAGED_ATTN_API int paged_kv_append_slots(const void* k_new, const void* v_new,
  * cos_sin may be null then).  PAGED_ATTN_ERR_ROPE for other values, for num_axes or
  * max_positions below 1 and for an eps that is negative or not finite.  The slots of a
  * call must be distinct.  With paged_attn_set_checks on, a slot past the pool sets bit 0 of
- * the status word and a position outside the table bit 1.  Strides, other sizes and
+ * the status word, a position outside the table bit 1 (and bit 2 reports a copy that did not
+ * come, a library fault, never expected).  Strides, other sizes and
  * errors as paged_kv_append_slots.  One launch; asynchronous; allocates nothing.
  */
 PAGED_ATTN_API int paged_kv_rope_append_slots(
@@ -773,7 +774,8 @@ PAGED_ATTN_API int paged_kv_compact(void* k_cache, void* v_cache, float* k_scale
  *   block_tables  [num_rows, max_blocks_per_seq]  int32: the children's entries are written
  *   seq_lens      [num_rows]  int32: the children's are written
  *   parents, children  [num_forks]  int32.  The children of a call are distinct and none is
- *                 a parent of it; a parent may have any number of them
+ *                 a parent of it; a parent may have any number of them.  A child's old pages
+ *                 are not given back: it has ended before (paged_kv_release)
  *   block_refs    [num_blocks]  int32: the table rows that hold a block, less one (zero for
  *                 blocks fresh from paged_kv_assign and for free ones); paged_kv_release
  *                 counts it down
@@ -783,7 +785,8 @@ PAGED_ATTN_API int paged_kv_compact(void* k_cache, void* v_cache, float* k_scale
  *
  * A fork is refused, its child left empty, when its block is not in the free stack or
  * a row is outside [0, num_rows).  With checks on, a block id outside [0, num_blocks) sets
- * bit 0 of the status word (it is handed on, not copied), an invalid row or length bit 1.
+ * bit 0 of the status word (it is handed on, not copied), an invalid row or length bit 1, a
+ * copy that did not come bit 2.  PAGED_ATTN_ERR_SIZES for 2 num_forks H_kv past 2^30.
  * k_scale, v_scale, sizes and errors as paged_kv_compact.  Asynchronous; allocates nothing.
  */
 PAGED_ATTN_API int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,

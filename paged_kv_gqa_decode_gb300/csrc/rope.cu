@@ -14,7 +14,7 @@
 // lanes (a group) a head.  The coefficients of a row are made once for several heads: with
 // the norm's weights folded in, z = r (x[a] (w[a] c) - x[b] (w[b] s)), r the root's reciprocal.
 //
-// Two kernels.  With few rows (a decode step) a group reads kHeads heads of one row
+// Two kernels.  With few bf16 rows (a decode step) a group reads kHeads heads of one row
 // straight into its registers.  With many, registers are what limits the bytes in flight
 // (8192 rows of 32 + 2 x 8 heads of 128: 50 us however the heads and CTAs were set), so
 // there each warp streams units of 4 KB through a ring of its own in shared memory by bulk
@@ -34,10 +34,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kHeads = 4;  // heads of one row that a group of lanes takes (few rows)
-// The rows are many from this many input bytes an SM on, if units hold half of their 4 KB on
-// average (32 + 2 x 8 heads of 128, few / many: 512 rows 4.3 / 4.5 us, 1024 6.7 / 6.1, 8192 40.9 /
-// 38.2; 24 + 2 x 4 of 256, FP8, 512 6.4 / 7.0, 8192 77 / 52; but 8 + 2 x 1 heads of 128, whose
-// units are mostly short, 8192 16.2 / 20.0).
+// bf16 rows are many from this many input bytes an SM on, if units hold half of their 4 KB on
+// average (32 + 2 x 8 heads of 128, few / many: 512 rows 4.2 / 4.3 us, 1024 6.7 / 5.9, 8192 40.6 /
+// 37.4; but 4 + 2 x 2 heads of 64, whose units are short, 8192 8.0 / 15.4).  FP8 rows always
+// are: the quantization in four heads' copies is too long a code for a short kernel (8 + 2 x 2
+// heads of 128, few / many: 64 rows 4.9 / 3.5, 1024 5.1 / 5.5, 8192 23.2 / 22.6; 24 + 2 x 4 of
+// 256, 64 rows 5.5 / 4.0, 8192 77 / 47).
 constexpr long long kManyBytes = 64 << 10;
 constexpr float kE4m3Max = 448.f;
 constexpr int kBadSlot = 1, kBadPosition = 2, kTimeout = 4;
@@ -261,7 +263,7 @@ __device__ __forceinline__ void head(const RopeParams& p, const Place<INTER>& at
       to[at.c0] = kind == 1 ? pack(z[0]) : raw0;
       to[at.c1] = kind == 1 ? pack(z[1]) : raw1;
     }
-  } else if (__any_sync(0xffffffffu, kind != 0)) {
+  } else if (kind != 0) {  // (the whole warp's: FP8 caches are written by the kernel for many rows)
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -271,7 +273,7 @@ __device__ __forceinline__ void head(const RopeParams& p, const Place<INTER>& at
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1)
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (kind != 0 && write && at_row >= 0) {
+    if (write && at_row >= 0) {
       const float f = top > 0.f ? top / kE4m3Max : 1.f;
       const long long to = at_row + (long long)h * p.BS;
       uint2* dst = reinterpret_cast<uint2*>(
@@ -319,7 +321,7 @@ __device__ __forceinline__ const float* norm_of(const RopeParams& p, int kind) {
   return kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
 }
 
-template <int D, bool FP8, bool INTER>
+template <int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) paged_kv_rope_few_kernel(const RopeParams p) {
   constexpr int kLanes = D / 16, kGroups = 32 / kLanes;
   griddep_wait();
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_kv_rope_few_kernel(const Ro
     const Coefficients k = coefficients(p, at, axes, pos, x.row, norm, rotate, some);
 #pragma unroll
     for (int u = 0; u < kHeads; ++u)
-      head<D, FP8, INTER>(p, at, k, raw[u][0], raw[u][1], norm != nullptr, rotate, x.kind, x.row,
+      head<D, false, INTER>(p, at, k, raw[u][0], raw[u][1], norm != nullptr, rotate, x.kind, x.row,
                           x.h0 + u, at_row, some && u < x.heads);
   }
 }
@@ -479,7 +481,7 @@ cudaError_t launch_kernel(const RopeParams& p, int sms, cudaStream_t stream) {
   const long long row_bytes = (long long)(p.H_q + 2 * p.H_kv) * D * 2;
   constexpr int kUnitHeads = kUnitBytes / (2 * D);
   const int units = (p.H_q + kUnitHeads - 1) / kUnitHeads + 2 * ((p.H_kv + kUnitHeads - 1) / kUnitHeads);
-  if (p.rows * row_bytes >= kManyBytes * sms && row_bytes >= units * (kUnitBytes / 2)) {
+  if (FP8 || (p.rows * row_bytes >= kManyBytes * sms && row_bytes >= units * (kUnitBytes / 2))) {
     static std::atomic<bool> limit_raised[64];
     auto kernel = paged_kv_rope_many_kernel<D, FP8, INTER>;
     int dev = 0;
@@ -496,12 +498,15 @@ cudaError_t launch_kernel(const RopeParams& p, int sms, cudaStream_t stream) {
     cfg.dynamicSmemBytes = kStreamSmem;
     return cudaLaunchKernelEx(&cfg, kernel, p);
   }
-  const int parts = (p.H_q + kHeads - 1) / kHeads + 2 * ((p.H_kv + kHeads - 1) / kHeads);
-  const long long lanes = (long long)p.rows * parts * (D / 16);
-  const long long want = (lanes + kThreads - 1) / kThreads, most = (long long)sms * 8;
-  cfg.gridDim = dim3((unsigned)(want < most ? want : most));
-  cfg.blockDim = dim3(kThreads);
-  return cudaLaunchKernelEx(&cfg, paged_kv_rope_few_kernel<D, FP8, INTER>, p);
+  if constexpr (!FP8) {
+    const int parts = (p.H_q + kHeads - 1) / kHeads + 2 * ((p.H_kv + kHeads - 1) / kHeads);
+    const long long lanes = (long long)p.rows * parts * (D / 16);
+    const long long want = (lanes + kThreads - 1) / kThreads, most = (long long)sms * 8;
+    cfg.gridDim = dim3((unsigned)(want < most ? want : most));
+    cfg.blockDim = dim3(kThreads);
+    return cudaLaunchKernelEx(&cfg, paged_kv_rope_few_kernel<D, INTER>, p);
+  }
+  return cudaErrorInvalidValue;  // (not reached)
 }
 
 template <int D>

@@ -239,6 +239,16 @@ def test_release_of_shared_blocks(BS, n, most, share, in_place):
     check_release(bt, lens, keep, refs, stack, 2, BS, in_place)
 
 
+@pytest.mark.parametrize("share", [1, 3, None])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_release_of_very_many_blocks(share, in_place):
+    """More entries than the threads hold at once."""
+    bt, lens, keep, refs, nb = random_release(700, 13000, 16, share or 1, 4, 0)
+    keep = np.where(np.arange(700) % 50 == 7, lens // 2, 0)
+    assert (-(-lens // 16) - -(-np.minimum(keep, lens) // 16)).sum() > 16 * 1024 * 8
+    check_release(bt, lens, keep, refs if share else None, np.full(nb, -1), 0, 16, in_place)
+
+
 @pytest.mark.parametrize("n,most", [(1, 40), (100, 500), (2000, 100)])
 def test_release_without_counts(n, most):
     bt, lens, keep, _, nb = random_release(n, most, 16, 1, n, 30)

@@ -9,7 +9,7 @@ from paged_kv_gqa_decode_gb300 import build as pbuild
 BF, I32 = torch.bfloat16, torch.int32
 
 
-@pytest.fixture(scope="module")
+@pytest.fixture(scope="module", autouse=True)
 def lib():
     pbuild.build()
     return pa.load()

@@ -156,6 +156,16 @@ def test_two_teams_and_split_ranges(D):
     run_case([5000], [5], 4, 1, D, 32, 13, softcap=20.0, window=3000, prefix=[100])
 
 
+@pytest.mark.parametrize("D,H_q,H_kv", [(64, 16, 4), (128, 32, 8), (128, 8, 8), (256, 12, 4)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=20.0, window=900), dict(alibi=True, prefix=[300, 5])])
+def test_long_sequences_among_many_short_ones(D, H_q, H_kv, kw):
+    """Pieces for every SM, a few of them much longer; the same bits every time."""
+    lens = [100 + s for s in range(70)]
+    lens[3], lens[40], lens[41], lens[69] = 3000, 2111, 900, 1500
+    outs = [run_case(lens, [40 - s % 23 for s in range(70)], H_q, H_kv, D, 16, 21, kind=KINDS, **kw) for _ in range(3)]
+    assert all(torch.equal(outs[0], o) for o in outs)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1])
 def test_other_scales(scale):
     run_case([200], [30], 4, 2, 128, 16, 14, scale=scale)
