@@ -84,23 +84,29 @@ struct TileShape {
   static constexpr int kHalves = D / 64;                  // 128-byte column halves of a row
   static constexpr int kQTileBytes = 128 * D * 2;         // one 128-row query tile
   static constexpr int kSlotBytes = BN * D * 2;           // one K or V tile
-  static constexpr int kSlots = D == 256 ? 5 : D == 64 ? 8 : 4;
+  // Trees of head_dim 256 hold the query rows in tensor memory (128 of its columns): their
+  // 64 KB are two more K/V tiles on the way, and the score product reads one operand less
+  // from shared memory, whose bandwidth 64-token tiles otherwise exceed.  (A tile took 1800
+  // cycles, 430 of them waiting for tiles and 1200 issuing products, now 1500, 260 and 1060;
+  // four contexts of 100000 tokens 356 -> 324 us.)
+  static constexpr bool kQTmem = TREE && D == 256;
+  static constexpr int kSlots = D == 256 ? (kQTmem ? 7 : 5) : D == 64 ? 8 : 4;
   // The teams' warps, then the producers and the product warp.  A warp's tensor
   // copies are issued one after the other, about 54 cycles each and 214 for a group,
   // whatever their size (measured on 2, 4 and 8 KB boxes), and warps side by side:
   // one producer brings 2 KB boxes at 18 to 30 bytes a cycle, two at 35, four at 70.
   // Slot s of the ring belongs to producer s % kProducers, which so waits for its
   // phases strictly in order (a parity wait cannot tell phase k from k - 2).
-  static constexpr int kProducers = D == 256 ? 5 : 2;
+  static constexpr int kProducers = D == 256 ? kSlots : 2;
   static_assert(kSlots % kProducers == 0, "a slot belongs to one producer");
   static constexpr int kThreads = kTeams * 256 + 32 + kProducers * 32;
-  // tensor memory: the teams' score buffers, then the accumulators
-  static constexpr int kOCol = kTeams * kBufs * BN;
+  // tensor memory: the teams' score buffers, then the accumulators (and the query rows)
+  static constexpr int kOCol = kTeams * kBufs * BN, kQCol = kOCol + kTeams * D;
   static constexpr int kTmemColumns = kCtas == 2 ? 256 : 512;
-  static_assert(kOCol + kTeams * D <= kTmemColumns, "tensor memory");
+  static_assert(kQCol + (kQTmem ? D / 2 : 0) <= kTmemColumns, "tensor memory");
   // shared memory: query tiles, the K/V ring, barriers (384 bytes) and scalars, the
   // row maxima the two threads of a row exchange, [team][kBufs][half][row]
-  static constexpr int kRingOff = kTeams * kQTileBytes;
+  static constexpr int kRingOff = kQTmem ? 0 : kTeams * kQTileBytes;
   static constexpr int kBarOff = kRingOff + kSlots * kSlotBytes;
   static constexpr int kMaxOff = kBarOff + 512;
   // (trees) depths of the drafted tokens, 16 bits each
@@ -153,7 +159,8 @@ __device__ __forceinline__ float cap_score(float s, float c, float cap_log2) {
 }
 
 template <int D, int TEAMS, int MOD, bool TREE>
-__global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TEAMS>::kCtas)
+__global__ void __launch_bounds__(TileShape<D, TEAMS, TREE>::kThreads,
+                                  TileShape<D, TEAMS, TREE>::kCtas)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const TileParams p) {
   using T = TileShape<D, TEAMS, TREE>;
@@ -239,7 +246,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     fence_barrier_init();
   }
   if (N <= kRankedSeqs) {
-    int2* rank = reinterpret_cast<int2*>(smem);  // (tokens, tiles) of each sequence
+    // (tokens, tiles) of each sequence, where no copy lands
+    int2* rank = reinterpret_cast<int2*>(smem + (T::kQTmem ? T::kMaxOff : 0));
     int tokens = 0, tiles = 0;
     if (tid < N) {
       // what the sequence's last row sees, which is near what each of its pieces walks
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
   // ---- the query rows, swizzled for the products (128-byte rows, 16-byte chunk c
   // of row r at c ^ (r % 8)); the threads of a row (four with one row tile for two
   // teams) share the work
-  if (softmax_thread) {
+  if (softmax_thread && !T::kQTmem) {
     const int sharers = both ? 2 : 2 * kTeams, chunks = D / 8 / sharers;
     const int c0 = (both ? half : 2 * team + half) * chunks;
     uint8_t* tile = sm_q + (both ? team * T::kQTileBytes : 0);
@@ -583,6 +591,7 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
       const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
       constexpr uint32_t kDescS = instr_desc(128, BN, false), kDescO = instr_desc(128, D, true);
       bool ok = mbar_wait(q_full, 0);
+      if (T::kQTmem) tc_fence_after();
       const uint32_t q_desc = desc_lo(smem_addr(smem), 16);
       const uint32_t v_lead = ((uint32_t)(BN * 128 - 16) >> 4) << 16;  // K-major to MN-major lead
       // The next K tile's and the next V tile's place in the ring: both advance
@@ -611,10 +620,14 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
         const uint32_t qd = q_desc + (two && t == 1 ? T::kQTileBytes >> 4 : 0);
         const uint32_t kd = q_desc + (slot_off(k_slot) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(lead, tm + buf_of(t, i) * BN,
-                 qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4),
-                 kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4), kDescS, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t k_part = kd + (((kk >> 2) * (BN * 128) + (kk & 3) * 32) >> 4);
+          if constexpr (T::kQTmem)
+            mma_ts(lead, tm + buf_of(t, i) * BN, tm + T::kQCol + kk * 8, k_part, kDescS, kk > 0);
+          else
+            mma_ss(lead, tm + buf_of(t, i) * BN,
+                   qd + (((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4), k_part, kDescS, kk > 0);
+        }
         mma_commit(lead, &s_full[buf_of(t, i)]);
         if (!two || t == 1) mma_commit(lead, &empty[k_slot]);
       };
@@ -667,6 +680,29 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS>::kThreads, TileShape<D, TE
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t o_addr =
         tmem + lane_base + T::kOCol + (kTeams == 2 ? team * D : 0) + half * (D / 2);
+    if constexpr (T::kQTmem) {
+      // the query rows: each thread half of its row, 32-bit words of two elements a column
+      static_assert(!T::kQTmem || kTeams == 1, "one row tile");
+#pragma unroll 1
+      for (int c = 0; c < D / 4; c += 16) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 v = valid ? __ldg(reinterpret_cast<const uint4*>(p.q + q_row * D) +
+                                        half * (D / 16) + c / 4 + i)
+                                : make_uint4(0u, 0u, 0u, 0u);
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+        tmem_st(tmem + lane_base + T::kQCol + half * (D / 4) + c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
     float* sm_max = reinterpret_cast<float*>(smem + T::kMaxOff) + team * kBufs * 256;
     const uint32_t pair_bar = 1 + team * 4 + (warp & 3);  // the two warps of 32 rows
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
