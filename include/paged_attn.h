@@ -701,7 +701,7 @@ PAGED_ATTN_API int paged_kv_append_slots(const void* k_new, const void* v_new,
  *   quantized as paged_kv_append_fp8 does (z from its float32 values)
  *
  *   q, k_new, v_new  rows at their strides as paged_kv_append_slots (slices of one fused
- *                 projection need no copy)
+ *                 projection need no copy); device memory
  *   q_out         [rows, H_q, head_dim]  bf16 (written); may be q where q_stride = H_q *
  *                 head_dim, else apart from all inputs
  *   k_scale, v_scale  [num_blocks, H_kv, block_size]  float32 (written), or both null; with
@@ -778,7 +778,7 @@ PAGED_ATTN_API int paged_kv_compact(void* k_cache, void* v_cache, float* k_scale
  *                 are not given back: it has ended before (paged_kv_release)
  *   block_refs    [num_blocks]  int32: the table rows that hold a block, less one (zero for
  *                 blocks fresh from paged_kv_assign and for free ones); paged_kv_release
- *                 counts it down
+ *                 counts it down.  Device memory
  *   free_blocks, free_count, free_count_out  as paged_kv_assign (free_count_out may be free_count,
  *                 at the cost of a second launch)
  *   refused       [1]  int32, or null: forks refused

@@ -94,6 +94,12 @@ class Call {
     return t.data_ptr();
   }
   void* at(const Tensor* t) { return t ? at(*t) : nullptr; }
+  // What tensor copies and atomics reach lies in device memory.
+  void* on_device(const Tensor& t, const char* name) {
+    void* x = at(t);
+    if (!t.is_cuda()) refuse(std::string(name) + " must be in device memory");
+    return x;
+  }
   template <typename T>
   T* as(const Tensor& t) {
     return static_cast<T*>(at(t));
@@ -242,7 +248,7 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
   if (prefix) c.need(*prefix, "prefix_lens", kI32, {seqs});
   if (ws && !ws->is_contiguous()) refuse("workspace must be contiguous");
   Output made(c, a[12], "out", ScalarType::BFloat16, q.sizes());
-  const void *pq = c.at(q), *pk = c.at(k), *pv = c.at(v);
+  const void *pq = c.at(q), *pk = c.on_device(k, "k_cache"), *pv = c.on_device(v, "v_cache");
   const Tensor& out = made.get(q, q.sizes());
   check(entry.tree(pq, pk, pv, c.at(out), c.as<int32_t>(qo), c.as<int32_t>(mask),
                    int32_size(mask.size(1), "tree_mask's words"), c.as<int32_t>(bt),
@@ -285,10 +291,11 @@ PyObject* rope_append_slots(PyObject* const* a, Py_ssize_t n) {
   if (qw) c.need(*qw, "q_norm", ScalarType::Float, {D});
   if (kw) c.need(*kw, "k_norm", ScalarType::Float, {D});
   Output made(c, a[15], "out", ScalarType::BFloat16, q.sizes());
-  const void *pq = c.at(q), *pk = c.at(kn), *pv = c.at(vn);
+  const void *pq = c.on_device(q, "q"), *pk = c.on_device(kn, "k_new"),
+             *pv = c.on_device(vn, "v_new");
   const Tensor& out = made.get(q, q.sizes());
-  check(entry.rope(pq, pk, pv, qs, ks, vs, c.at(out), c.at(cache.k), c.at(cache.v),
-                   c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int64_t>(slots),
+  check(entry.rope(pq, pk, pv, qs, ks, vs, c.at(out), c.on_device(cache.k, "k_cache"),
+                   c.on_device(cache.v, "v_cache"), c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int64_t>(slots),
                    c.as<int32_t>(pos), int32_size(axes, "axes"), c.as<int32_t>(axis),
                    c.as<float>(cs), int32_size(cs.size(0), "max_positions"),
                    int32_size(cs.size(1), "rotary_dim"), interleaved, c.as<float>(qw),
@@ -314,7 +321,8 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[8], "seq_lens_out", kI32, {seqs});
   int32_t* plens = c.as<int32_t>(lens);
   const Tensor& out = made.get(lens, {seqs});
-  check(entry.compact(c.at(cache.k), c.at(cache.v), c.as<float>(cache.k_scale),
+  check(entry.compact(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
+                      c.as<float>(cache.k_scale),
                       c.as<float>(cache.v_scale), c.as<int32_t>(qo), c.as<int32_t>(acc),
                       c.as<int32_t>(bt), plens, c.as<int32_t>(out), int32_size(seqs, "num_seqs"),
                       int32_size(acc.size(1), "max_accept"), cache.H, cache.D,
@@ -345,7 +353,9 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[11], "free_count_out", kI32, {1});
   int32_t* pcount = c.as<int32_t>(count);
   const Tensor& left = made.get(count, {1});
-  check(entry.fork(c.at(cache.k), c.at(cache.v), c.as<float>(cache.k_scale),
+  c.on_device(refs, "block_refs");
+  check(entry.fork(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
+                   c.as<float>(cache.k_scale),
                    c.as<float>(cache.v_scale), c.as<int32_t>(bt), c.as<int32_t>(lens),
                    c.as<int32_t>(parents), c.as<int32_t>(children), c.as<int32_t>(refs),
                    c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(left),
@@ -377,6 +387,7 @@ PyObject* release(PyObject* const* a, Py_ssize_t n) {
   int32_t *plens = c.as<int32_t>(lens), *pcount = c.as<int32_t>(count);
   const Tensor& out = made_lens.get(lens, {seqs});
   const Tensor& left = made_count.get(count, {1});
+  if (refs) c.on_device(*refs, "block_refs");
   check(entry.release(c.as<int32_t>(bt), plens, c.as<int32_t>(keep), c.as<int32_t>(refs),
                       refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount,
                       c.as<int32_t>(out), c.as<int32_t>(left), int32_size(seqs, "num_seqs"),

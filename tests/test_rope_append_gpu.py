@@ -220,3 +220,24 @@ def test_no_rows():
     out = pa.paged_kv_rope_append_slots(e, e, e, kc, kc.clone(), torch.zeros(0, dtype=torch.int64, device="cuda"),
                                         torch.zeros(0, dtype=torch.int32, device="cuda"), torch.zeros(4, 128, device="cuda"))
     assert out.shape == (0, 2, 128)
+
+
+def test_small_tensors_may_be_pinned_rows_and_caches_not():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(6, 12, 128, generator=g).to(torch.bfloat16)
+    q, k, v = (t.cuda() for t in (x[:, :8].contiguous(), x[:, 8:10].contiguous(), x[:, 10:].contiguous()))
+    slots, pos = torch.tensor([3, 40, 0, -1, 9, 17]), torch.arange(6, dtype=torch.int32)
+    cs = torch.tensor(table(8, 128))
+    want = None
+    for pinned in (False, True):
+        kc, vc = (torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        s, p, t = (y.pin_memory() if pinned else y.cuda() for y in (slots, pos, cs))
+        got = (pa.paged_kv_rope_append_slots(q, k, v, kc, vc, s, p, t), kc, vc)
+        torch.cuda.synchronize()
+        assert want is None or all(torch.equal(a, b) for a, b in zip(got, want))
+        want = got
+    host = torch.zeros(4, 2, 16, 128, dtype=torch.bfloat16).pin_memory()
+    for bad in ((q.cpu().pin_memory(), k, v, kc, vc), (q, k.cpu().pin_memory(), v, kc, vc), (q, k, v, host, vc),
+                (q, k, v, kc, host)):
+        with pytest.raises(ValueError, match="device memory"):
+            pa.paged_kv_rope_append_slots(*bad, slots.cuda(), pos.cuda(), cs.cuda())
