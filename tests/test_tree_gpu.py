@@ -172,7 +172,7 @@ def test_other_scales(scale):
 
 
 def test_a_chain_equals_the_causal_call():
-    lens, ql = [300 + s for s in range(200)], [33 if s % 2 else 64 for s in range(200)]  # (neither is split)
+    lens, ql = [300 + s for s in range(200)], [32 - s % 9 for s in range(200)]  # (the same pieces, not split)
     w, q, qo, mask, bt = make(lens, ql, 8, 2, 128, 16, 15, kind="chain")
     a = pa.paged_attn_decode_tree(q, w.k_cache, w.v_cache, i32(qo), i32(mask), w.block_tables, w.seq_lens, w.scale)
     b = pa.paged_attn_decode_multi_mods(q, w.k_cache, w.v_cache, i32(qo), w.block_tables, w.seq_lens, w.scale)
