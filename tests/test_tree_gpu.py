@@ -166,6 +166,41 @@ def test_long_sequences_among_many_short_ones(D, H_q, H_kv, kw):
     assert all(torch.equal(outs[0], o) for o in outs)
 
 
+@pytest.mark.parametrize("D,H_q,H_kv", [(64, 8, 1), (128, 4, 2), (256, 6, 1)])
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=9.0, window=12, prefix=[3])])
+def test_more_sequences_than_are_ranked(D, H_q, H_kv, kw):
+    n = 150
+    run_case([(7 * s) % 61 for s in range(n)], [min((7 * s) % 61, (5 * s) % 23) for s in range(n)], H_q, H_kv, D, 16, 22,
+             kind=KINDS, **kw)
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Captured apart, replayed in any order, with the parts of one larger than the other's."""
+    calls = []
+    for lens, ql, seed in (([900], [20], 31), ([400, 70], [40, 3], 32)):
+        w, q, qo, mask, bt = make(lens, ql, 8, 2, 128, 16, seed)
+        calls.append((q, w.k_cache, w.v_cache, i32(qo), i32(mask), w.block_tables, w.seq_lens, w.scale))
+    need = max(pa.paged_attn_tree_workspace_bytes(len(c[6]), c[0].shape[0], 8, 2, 128, c[5].shape[1], 16) for c in calls)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    want = [pa.paged_attn_decode_tree(*c) for c in calls]
+    outs = [torch.empty_like(x) for x in want]
+    torch.cuda.synchronize()
+    graphs = []
+    for c, out in zip(calls, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.paged_attn_decode_tree(*c, out=out, workspace=ws)
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (1, 1), (0, 0)):
+        for out in outs:
+            out.zero_()
+        for k in order:
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        for k in set(order):
+            assert torch.equal(outs[k], want[k])
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.1])
 def test_other_scales(scale):
     run_case([200], [30], 4, 2, 128, 16, 14, scale=scale)
