@@ -7,6 +7,10 @@ CUDA kernels.  There is no fallback: if the compiled library is missing the
 calls raise.  The entry points of speculative and parallel decoding (trees, rotation
 with the append, compaction, forks, release) are marshalled by a native module
 (``csrc/binding.cpp``), as an engine's step waits for the host in them.
+
+An output that one of those makes under ``stream=`` is that stream's memory, as if made under
+``torch.cuda.stream(stream)``: another stream that uses it waits for that one, and
+holds it with ``record_stream``.
 """
 from __future__ import annotations
 

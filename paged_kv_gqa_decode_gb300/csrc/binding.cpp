@@ -16,6 +16,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -59,9 +60,19 @@ std::string shape_text(IntArrayRef s) {
   return x + (s.size() == 1 ? ",)" : ")");
 }
 
-// The tensors of a call: each checked once, all on the current device or pinned.
+// The tensors of a call: each checked once, all on the current device or pinned; and its stream,
+// the one given or the device's current one.
 class Call {
  public:
+  explicit Call(PyObject* s) {
+    if (s == Py_None) return;
+    PyObject* h = PyObject_GetAttrString(s, "cuda_stream");
+    if (!h) throw Raised();
+    stream_ = static_cast<cudaStream_t>(PyLong_AsVoidPtr(h));
+    Py_DECREF(h);
+    if (!stream_ && PyErr_Occurred()) throw Raised();
+    given_ = true;
+  }
   const Tensor& tensor(PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
     return THPVariable_Unpack(o);
@@ -108,20 +119,26 @@ class Call {
   T* as(const Tensor* t) {
     return static_cast<T*>(at(t));
   }
-  // The stream's handle: the one given, or the device's current one.
-  void* stream(PyObject* s) {
-    if (s == Py_None)
-      return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device_)).stream();
-    PyObject* h = PyObject_GetAttrString(s, "cuda_stream");
-    if (!h) throw Raised();
-    void* p = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (!p && PyErr_Occurred()) throw Raised();
-    return p;
+  void* stream() const {
+    return given_ ? stream_
+                  : c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device_)).stream();
+  }
+  // An output of the call (its inputs have been seen).  With a stream given it is that stream's memory: the
+  // allocator may give a block of the current stream's whose last use there is still to come, and
+  // may give it away again before the call's kernels have run.
+  Tensor make(const Tensor& like, IntArrayRef shape) {
+    const auto device = static_cast<c10::DeviceIndex>(device_);
+    if (!given_ || c10::cuda::getCurrentCUDAStream(device).stream() == stream_)
+      return at::empty(shape, like.options());
+    c10::cuda::CUDAStreamGuard guard(
+        c10::cuda::getStreamFromExternal(stream_, device < 0 ? c10::cuda::current_device() : device));
+    return at::empty(shape, like.options());
   }
 
  private:
   int device_ = -1;  // the current one, once a CUDA tensor has been seen
+  cudaStream_t stream_ = nullptr;
+  bool given_ = false;
 };
 
 int int32_of(PyObject* o, const char* name) {
@@ -202,9 +219,9 @@ struct Output {
       : object(o), given(c.optional(o, name)) {
     if (given) c.need(*given, name, dtype, shape);
   }
-  const Tensor& get(const Tensor& like, IntArrayRef shape) {
+  const Tensor& get(Call& c, const Tensor& like, IntArrayRef shape) {
     if (given) return *given;
-    made = at::empty(shape, like.options());
+    made = c.make(like, shape);
     return made;
   }
   PyObject* result() const {  // a new reference
@@ -224,7 +241,7 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
   expect(n, 15);
   const float scale = float_of(a[7]), softcap = softcap_of(a[8]);
   const int window = int32_of(a[10], "window");
-  Call c;
+  Call c(a[14]);
   const Tensor &q = c.tensor(a[0], "q"), &k = c.tensor(a[1], "k_cache"),
                &v = c.tensor(a[2], "v_cache"), &qo = c.tensor(a[3], "qo_indptr"),
                &mask = c.tensor(a[4], "tree_mask"), &bt = c.tensor(a[5], "block_tables"),
@@ -249,7 +266,7 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
   if (ws && !ws->is_contiguous()) refuse("workspace must be contiguous");
   Output made(c, a[12], "out", ScalarType::BFloat16, q.sizes());
   const void *pq = c.at(q), *pk = c.on_device(k, "k_cache"), *pv = c.on_device(v, "v_cache");
-  const Tensor& out = made.get(q, q.sizes());
+  const Tensor& out = made.get(c, q, q.sizes());
   check(entry.tree(pq, pk, pv, c.at(out), c.as<int32_t>(qo), c.as<int32_t>(mask),
                    int32_size(mask.size(1), "tree_mask's words"), c.as<int32_t>(bt),
                    c.as<int32_t>(lens), int32_size(seqs, "num_seqs"), int32_size(rows, "total_q"),
@@ -257,13 +274,13 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
                    int32_size(q.size(2), "head_dim"), int32_size(bt.size(1), "max_blocks"),
                    int32_size(k.size(2), "block_size"), scale, softcap, c.as<float>(slopes),
                    window, c.as<int32_t>(prefix), c.at(ws), ws ? ws->nbytes() : 0,
-                   c.stream(a[14])));
+                   c.stream()));
   return made.result();
 }
 
 PyObject* rope_append_slots(PyObject* const* a, Py_ssize_t n) {
   expect(n, 17);
-  Call c;
+  Call c(a[16]);
   const Caches cache(c, a[3], a[4], a[13], a[14]);
   const Tensor &q = c.tensor(a[0], "q"), &kn = c.tensor(a[1], "k_new"),
                &vn = c.tensor(a[2], "v_new"), &slots = c.tensor(a[5], "slot_map"),
@@ -293,20 +310,20 @@ PyObject* rope_append_slots(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[15], "out", ScalarType::BFloat16, q.sizes());
   const void *pq = c.on_device(q, "q"), *pk = c.on_device(kn, "k_new"),
              *pv = c.on_device(vn, "v_new");
-  const Tensor& out = made.get(q, q.sizes());
+  const Tensor& out = made.get(c, q, q.sizes());
   check(entry.rope(pq, pk, pv, qs, ks, vs, c.at(out), c.on_device(cache.k, "k_cache"),
                    c.on_device(cache.v, "v_cache"), c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int64_t>(slots),
                    c.as<int32_t>(pos), int32_size(axes, "axes"), c.as<int32_t>(axis),
                    c.as<float>(cs), int32_size(cs.size(0), "max_positions"),
                    int32_size(cs.size(1), "rotary_dim"), interleaved, c.as<float>(qw),
                    c.as<float>(kw), eps, int32_size(rows, "rows"), int32_size(H, "H_q"), cache.H,
-                   cache.D, cache.BS, cache.nb, c.stream(a[16])));
+                   cache.D, cache.BS, cache.nb, c.stream()));
   return made.result();
 }
 
 PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   expect(n, 10);
-  Call c;
+  Call c(a[9]);
   const Caches cache(c, a[0], a[1], a[6], a[7]);
   const Tensor &qo = c.tensor(a[2], "qo_indptr"), &acc = c.tensor(a[3], "accepted"),
                &bt = c.tensor(a[4], "block_tables"), &lens = c.tensor(a[5], "seq_lens");
@@ -320,19 +337,19 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   c.need(bt, "block_tables", kI32, {seqs, bt.size(1)});
   Output made(c, a[8], "seq_lens_out", kI32, {seqs});
   int32_t* plens = c.as<int32_t>(lens);
-  const Tensor& out = made.get(lens, {seqs});
+  const Tensor& out = made.get(c, lens, {seqs});
   check(entry.compact(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
                       c.as<float>(cache.k_scale),
                       c.as<float>(cache.v_scale), c.as<int32_t>(qo), c.as<int32_t>(acc),
                       c.as<int32_t>(bt), plens, c.as<int32_t>(out), int32_size(seqs, "num_seqs"),
                       int32_size(acc.size(1), "max_accept"), cache.H, cache.D,
-                      int32_size(bt.size(1), "max_blocks"), cache.BS, cache.nb, c.stream(a[9])));
+                      int32_size(bt.size(1), "max_blocks"), cache.BS, cache.nb, c.stream()));
   return made.result();
 }
 
 PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   expect(n, 14);
-  Call c;
+  Call c(a[13]);
   const Caches cache(c, a[0], a[1], a[9], a[10]);
   const Tensor &bt = c.tensor(a[2], "block_tables"), &lens = c.tensor(a[3], "seq_lens"),
                &parents = c.tensor(a[4], "parents"), &children = c.tensor(a[5], "children"),
@@ -352,7 +369,7 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   if (refused) c.need(*refused, "refused", kI32, {1});
   Output made(c, a[11], "free_count_out", kI32, {1});
   int32_t* pcount = c.as<int32_t>(count);
-  const Tensor& left = made.get(count, {1});
+  const Tensor& left = made.get(c, count, {1});
   c.on_device(refs, "block_refs");
   check(entry.fork(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
                    c.as<float>(cache.k_scale),
@@ -361,14 +378,14 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
                    c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(left),
                    c.as<int32_t>(refused), int32_size(forks, "forks"), int32_size(rows, "rows"),
                    cache.H, cache.D, int32_size(bt.size(1), "max_blocks"), cache.BS,
-                   int32_size(n_free, "free_blocks' length"), cache.nb, c.stream(a[13])));
+                   int32_size(n_free, "free_blocks' length"), cache.nb, c.stream()));
   return made.result();
 }
 
 PyObject* release(PyObject* const* a, Py_ssize_t n) {
   expect(n, 10);
   const int BS = int32_of(a[5], "block_size");
-  Call c;
+  Call c(a[9]);
   const Tensor &bt = c.tensor(a[0], "block_tables"), &lens = c.tensor(a[1], "seq_lens"),
                &keep = c.tensor(a[2], "keep_lens"), &free_blocks = c.tensor(a[3], "free_blocks"),
                &count = c.tensor(a[4], "free_count");
@@ -385,14 +402,14 @@ PyObject* release(PyObject* const* a, Py_ssize_t n) {
   Output made_lens(c, a[7], "seq_lens_out", kI32, {seqs});
   Output made_count(c, a[8], "free_count_out", kI32, {1});
   int32_t *plens = c.as<int32_t>(lens), *pcount = c.as<int32_t>(count);
-  const Tensor& out = made_lens.get(lens, {seqs});
-  const Tensor& left = made_count.get(count, {1});
+  const Tensor& out = made_lens.get(c, lens, {seqs});
+  const Tensor& left = made_count.get(c, count, {1});
   if (refs) c.on_device(*refs, "block_refs");
   check(entry.release(c.as<int32_t>(bt), plens, c.as<int32_t>(keep), c.as<int32_t>(refs),
                       refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount,
                       c.as<int32_t>(out), c.as<int32_t>(left), int32_size(seqs, "num_seqs"),
                       int32_size(bt.size(1), "max_blocks"), BS,
-                      int32_size(n_free, "free_blocks' length"), c.stream(a[9])));
+                      int32_size(n_free, "free_blocks' length"), c.stream()));
   PyObject* x = made_lens.result();
   if (!x) return nullptr;
   PyObject* y = made_count.result();
