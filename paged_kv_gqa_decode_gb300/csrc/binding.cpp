@@ -5,7 +5,9 @@
 //
 // The entry points' addresses come from the library that the package has loaded, so this
 // module links to torch alone.  Every failure is a Python exception; nothing is kept
-// between calls but the addresses.
+// between calls but the addresses.  Other Python threads run while a call is in the library or the
+// allocator: either may wait for the GPU (a full launch queue, a workspace that grows), and
+// the GPU may be waiting for a host function that needs the interpreter.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -43,6 +45,12 @@ struct Raised {};
   PyErr_SetString(PyExc_ValueError, why.c_str());
   throw Raised();
 }
+
+// The interpreter's lock, let go of in a scope that touches no Python object.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
 
 std::string dtype_name(ScalarType t) {
   switch (t) {
@@ -128,6 +136,7 @@ class Call {
   // may give it away again before the call's kernels have run.
   Tensor make(const Tensor& like, IntArrayRef shape) {
     const auto device = static_cast<c10::DeviceIndex>(device_);
+    const Unlocked others;
     if (!given_ || c10::cuda::getCurrentCUDAStream(device).stream() == stream_)
       return at::empty(shape, like.options());
     c10::cuda::CUDAStreamGuard guard(
@@ -173,7 +182,14 @@ bool truth(PyObject* o) {
   if (v < 0) throw Raised();
   return v != 0;
 }
-void check(int status) {
+// A call into the library, and its status as an exception.
+template <typename... P, typename... A>
+void run(int (*f)(P...), A... a) {
+  int status;
+  {
+    const Unlocked others;
+    status = f(a...);
+  }
   if (status == 0) return;
   PyObject* r = PyObject_CallFunction(on_error, "i", status);
   Py_XDECREF(r);
@@ -267,14 +283,12 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[12], "out", ScalarType::BFloat16, q.sizes());
   const void *pq = c.at(q), *pk = c.on_device(k, "k_cache"), *pv = c.on_device(v, "v_cache");
   const Tensor& out = made.get(c, q, q.sizes());
-  check(entry.tree(pq, pk, pv, c.at(out), c.as<int32_t>(qo), c.as<int32_t>(mask),
-                   int32_size(mask.size(1), "tree_mask's words"), c.as<int32_t>(bt),
-                   c.as<int32_t>(lens), int32_size(seqs, "num_seqs"), int32_size(rows, "total_q"),
-                   int32_size(H, "H_q"), int32_size(k.size(1), "H_kv"),
-                   int32_size(q.size(2), "head_dim"), int32_size(bt.size(1), "max_blocks"),
-                   int32_size(k.size(2), "block_size"), scale, softcap, c.as<float>(slopes),
-                   window, c.as<int32_t>(prefix), c.at(ws), ws ? ws->nbytes() : 0,
-                   c.stream()));
+  run(entry.tree, pq, pk, pv, c.at(out), c.as<int32_t>(qo), c.as<int32_t>(mask),
+      int32_size(mask.size(1), "tree_mask's words"), c.as<int32_t>(bt), c.as<int32_t>(lens),
+      int32_size(seqs, "num_seqs"), int32_size(rows, "total_q"), int32_size(H, "H_q"),
+      int32_size(k.size(1), "H_kv"), int32_size(q.size(2), "head_dim"),
+      int32_size(bt.size(1), "max_blocks"), int32_size(k.size(2), "block_size"), scale, softcap,
+      c.as<float>(slopes), window, c.as<int32_t>(prefix), c.at(ws), ws ? ws->nbytes() : 0, c.stream());
   return made.result();
 }
 
@@ -311,13 +325,12 @@ PyObject* rope_append_slots(PyObject* const* a, Py_ssize_t n) {
   const void *pq = c.on_device(q, "q"), *pk = c.on_device(kn, "k_new"),
              *pv = c.on_device(vn, "v_new");
   const Tensor& out = made.get(c, q, q.sizes());
-  check(entry.rope(pq, pk, pv, qs, ks, vs, c.at(out), c.on_device(cache.k, "k_cache"),
-                   c.on_device(cache.v, "v_cache"), c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int64_t>(slots),
-                   c.as<int32_t>(pos), int32_size(axes, "axes"), c.as<int32_t>(axis),
-                   c.as<float>(cs), int32_size(cs.size(0), "max_positions"),
-                   int32_size(cs.size(1), "rotary_dim"), interleaved, c.as<float>(qw),
-                   c.as<float>(kw), eps, int32_size(rows, "rows"), int32_size(H, "H_q"), cache.H,
-                   cache.D, cache.BS, cache.nb, c.stream()));
+  run(entry.rope, pq, pk, pv, qs, ks, vs, c.at(out), c.on_device(cache.k, "k_cache"),
+      c.on_device(cache.v, "v_cache"), c.as<float>(cache.k_scale), c.as<float>(cache.v_scale),
+      c.as<int64_t>(slots), c.as<int32_t>(pos), int32_size(axes, "axes"), c.as<int32_t>(axis),
+      c.as<float>(cs), int32_size(cs.size(0), "max_positions"),
+      int32_size(cs.size(1), "rotary_dim"), interleaved, c.as<float>(qw), c.as<float>(kw), eps,
+      int32_size(rows, "rows"), int32_size(H, "H_q"), cache.H, cache.D, cache.BS, cache.nb, c.stream());
   return made.result();
 }
 
@@ -338,12 +351,11 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[8], "seq_lens_out", kI32, {seqs});
   int32_t* plens = c.as<int32_t>(lens);
   const Tensor& out = made.get(c, lens, {seqs});
-  check(entry.compact(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
-                      c.as<float>(cache.k_scale),
-                      c.as<float>(cache.v_scale), c.as<int32_t>(qo), c.as<int32_t>(acc),
-                      c.as<int32_t>(bt), plens, c.as<int32_t>(out), int32_size(seqs, "num_seqs"),
-                      int32_size(acc.size(1), "max_accept"), cache.H, cache.D,
-                      int32_size(bt.size(1), "max_blocks"), cache.BS, cache.nb, c.stream()));
+  run(entry.compact, c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
+      c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int32_t>(qo),
+      c.as<int32_t>(acc), c.as<int32_t>(bt), plens, c.as<int32_t>(out),
+      int32_size(seqs, "num_seqs"), int32_size(acc.size(1), "max_accept"), cache.H, cache.D,
+      int32_size(bt.size(1), "max_blocks"), cache.BS, cache.nb, c.stream());
   return made.result();
 }
 
@@ -371,14 +383,13 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   int32_t* pcount = c.as<int32_t>(count);
   const Tensor& left = made.get(c, count, {1});
   c.on_device(refs, "block_refs");
-  check(entry.fork(c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
-                   c.as<float>(cache.k_scale),
-                   c.as<float>(cache.v_scale), c.as<int32_t>(bt), c.as<int32_t>(lens),
-                   c.as<int32_t>(parents), c.as<int32_t>(children), c.as<int32_t>(refs),
-                   c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(left),
-                   c.as<int32_t>(refused), int32_size(forks, "forks"), int32_size(rows, "rows"),
-                   cache.H, cache.D, int32_size(bt.size(1), "max_blocks"), cache.BS,
-                   int32_size(n_free, "free_blocks' length"), cache.nb, c.stream()));
+  run(entry.fork, c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
+      c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int32_t>(bt),
+      c.as<int32_t>(lens), c.as<int32_t>(parents), c.as<int32_t>(children), c.as<int32_t>(refs),
+      c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(left), c.as<int32_t>(refused),
+      int32_size(forks, "forks"), int32_size(rows, "rows"), cache.H, cache.D,
+      int32_size(bt.size(1), "max_blocks"), cache.BS, int32_size(n_free, "free_blocks' length"),
+      cache.nb, c.stream());
   return made.result();
 }
 
@@ -405,11 +416,10 @@ PyObject* release(PyObject* const* a, Py_ssize_t n) {
   const Tensor& out = made_lens.get(c, lens, {seqs});
   const Tensor& left = made_count.get(c, count, {1});
   if (refs) c.on_device(*refs, "block_refs");
-  check(entry.release(c.as<int32_t>(bt), plens, c.as<int32_t>(keep), c.as<int32_t>(refs),
-                      refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount,
-                      c.as<int32_t>(out), c.as<int32_t>(left), int32_size(seqs, "num_seqs"),
-                      int32_size(bt.size(1), "max_blocks"), BS,
-                      int32_size(n_free, "free_blocks' length"), c.stream()));
+  run(entry.release, c.as<int32_t>(bt), plens, c.as<int32_t>(keep), c.as<int32_t>(refs),
+      refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(out),
+      c.as<int32_t>(left), int32_size(seqs, "num_seqs"), int32_size(bt.size(1), "max_blocks"), BS,
+      int32_size(n_free, "free_blocks' length"), c.stream());
   PyObject* x = made_lens.result();
   if (!x) return nullptr;
   PyObject* y = made_count.result();

@@ -1,5 +1,13 @@
 """The native marshalling beside other streams, other threads and host memory: who may use the memory
 of an output that the call makes, and when."""
+import ctypes
+import importlib.machinery
+import importlib.util
+import shutil
+import subprocess
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -118,3 +126,80 @@ def test_a_dropped_output_is_not_given_to_the_current_stream_at_once(call):
     torch.cuda.synchronize()
     assert all(bool((x == 0x55).all()) for x in mine)
     del held
+
+
+# ------------------------------------------------------------------ other Python threads
+
+@pytest.fixture
+def slow(tmp_path, monkeypatch):
+    """A second copy of the marshalling module whose entry points sleep on the host for 0.3 seconds, and then
+    return the status that the fixture's function is given."""
+    src, lib = tmp_path / "slow.c", tmp_path / "slow.so"
+    src.write_text("#include <unistd.h>\nint status;\nint slow(void) { usleep(300000); return status; }\n")
+    subprocess.run([shutil.which("gcc") or "gcc", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    stub = ctypes.CDLL(str(lib))
+    path = shutil.copy(pa.NATIVE_PATH, tmp_path / "_paged_native.so")
+    loader = importlib.machinery.ExtensionFileLoader("_paged_native", str(path))
+    mod = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_paged_native", str(path),
+                                                                                 loader=loader))
+    loader.exec_module(mod)
+    mod.init(pa._check, *[ctypes.cast(stub.slow, ctypes.c_void_p).value] * 5)
+    monkeypatch.setattr(pa, "_native", mod)
+
+    def returns(status):
+        ctypes.c_int.in_dll(stub, "status").value = status
+
+    return returns
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_other_threads_run_while_a_call_is_in_the_library(slow, call):
+    p = Problem()
+    torch.cuda.synchronize()
+    ticks, done = [], threading.Event()
+
+    def count():
+        while not done.is_set():
+            ticks.append(time.perf_counter())
+            time.sleep(0.005)
+
+    other = threading.Thread(target=count)
+    other.start()
+    try:
+        start = time.perf_counter()
+        getattr(p, call)()
+        end = time.perf_counter()
+        slow(-5)
+        with pytest.raises(pa.PagedAttnError) as e:
+            getattr(p, call)()
+    finally:
+        done.set()
+        other.join()
+    assert e.value.status == -5
+    assert end - start > 0.2 and sum(start < t < end for t in ticks) >= 5
+
+
+def test_calls_of_several_threads_at_once():
+    """Each on a stream of its own, with outputs that the calls make."""
+    want = {c: getattr(Problem(), c)() for c in CALLS}
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            for c in CALLS:
+                with torch.cuda.stream(s):
+                    p = Problem()
+                s.synchronize()
+                got = getattr(p, c)(stream=s)
+                s.synchronize()
+                if not all(torch.equal(x, y) for x, y in zip(got, want[c])):
+                    wrong.append(c)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
