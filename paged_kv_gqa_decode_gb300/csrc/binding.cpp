@@ -131,17 +131,19 @@ class Call {
     return given_ ? stream_
                   : c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device_)).stream();
   }
-  // An output of the call (its inputs have been seen).  With a stream given it is that stream's memory: the
-  // allocator may give a block of the current stream's whose last use there is still to come, and
-  // may give it away again before the call's kernels have run.
+  // An output of the call (its inputs have been seen), in device memory even where it is made like a
+  // pinned tensor.  With a stream given it is that stream's memory: the allocator may give a
+  // block of the current stream's whose last use there is still to come, and may give it
+  // away again before the call's kernels have run.
   Tensor make(const Tensor& like, IntArrayRef shape) {
+    if (device_ < 0) device_ = c10::cuda::current_device();
     const auto device = static_cast<c10::DeviceIndex>(device_);
+    const auto options = like.options().device(c10::Device(c10::DeviceType::CUDA, device));
     const Unlocked others;
     if (!given_ || c10::cuda::getCurrentCUDAStream(device).stream() == stream_)
-      return at::empty(shape, like.options());
-    c10::cuda::CUDAStreamGuard guard(
-        c10::cuda::getStreamFromExternal(stream_, device < 0 ? c10::cuda::current_device() : device));
-    return at::empty(shape, like.options());
+      return at::empty(shape, options);
+    c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream_, device));
+    return at::empty(shape, options);
   }
 
  private:

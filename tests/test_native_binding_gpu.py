@@ -128,6 +128,17 @@ def test_a_dropped_output_is_not_given_to_the_current_stream_at_once(call):
     del held
 
 
+@pytest.mark.parametrize("call", ["tree", "compact", "fork", "release"])
+def test_outputs_made_beside_pinned_inputs_are_device_memory(call):
+    want = getattr(Problem(), call)()
+    p = Problem()
+    p.q, p.lens, p.count = (t.cpu().pin_memory() for t in (p.q, p.lens, p.count))
+    got = getattr(p, call)()
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert x.is_cuda and torch.equal(x, y)
+
+
 # ------------------------------------------------------------------ other Python threads
 
 @pytest.fixture
