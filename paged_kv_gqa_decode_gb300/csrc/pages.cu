@@ -425,13 +425,14 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   // ---- this thread's run of entries [e0, e1) of all the released ones
   const int run = (int)(((long long)all + ctas * kReleaseThreads - 1) / (ctas * kReleaseThreads));
   const long long at = ((long long)cta * kReleaseThreads + tid) * run;
-  const int e0 = (int)min((long long)all, at), e1 = (int)min((long long)all, at + run);
+  // (unsigned, as a batch behind the last one may begin past an int)
+  const uint32_t e0 = (uint32_t)min((long long)all, at), e1 = (uint32_t)min((long long)all, at + run);
   int start_s = 0, start_p = 0, start_left = 0;  // sequence, page and pages left at e0
   if (e0 < e1) {
     int lo = 0, hi = kReleaseThreads - 1;  // the last group of sequences starting at or before e0
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (before[mid] <= e0)
+      if (before[mid] <= (int)e0)
         lo = mid;
       else
         hi = mid - 1;
@@ -441,9 +442,9 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
     for (;;) {
       int first;
       const int n = span(start_s, first);
-      if (e0 < ahead + n || start_s + 1 >= N) {
-        start_p = first + (e0 - ahead);
-        start_left = ahead + n - e0;
+      if ((int)e0 < ahead + n || start_s + 1 >= N) {
+        start_p = first + ((int)e0 - ahead);
+        start_left = ahead + n - (int)e0;
         break;
       }
       ahead += n;
@@ -453,8 +454,9 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   // The entries of a batch: keys (-1: none) and blocks.  A run of one batch, the usual one, is
   // looked up once; a longer one in every step.
   int key[kReleaseBatch], block[kReleaseBatch];
-  int s = start_s, page = start_p, left = start_left, e_at = 0;  // (e_at: first of the batch)
-  auto look_up = [&](int e) {
+  int s = start_s, page = start_p, left = start_left;
+  uint32_t e_at = 0;  // first of the batch
+  auto look_up = [&](uint32_t e) {
 #pragma unroll
     for (int u = 0; u < kReleaseBatch; ++u) {
       key[u] = -1;
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
   // What all paths end with: every CTA has read the lengths and the free count by now, except
   // those of a long run, which reads the lengths once more.
   auto write_lengths = [&](int total) {
-    for (int i = cta * kReleaseThreads + tid; i < N; i += ctas * kReleaseThreads) {
+    for (uint32_t i = cta * kReleaseThreads + tid; i < (uint32_t)N; i += ctas * kReleaseThreads) {
       const int len = clamped_length(p.seq_lens[i], p.maxb, p.BS, nullptr);
       p.seq_lens_out[i] = min(max(p.keep_lens[i], 0), len);
     }
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kReleaseThreads) paged_kv_release_kernel(const
     each_batch([&] {
 #pragma unroll
       for (int u = 0; u < kReleaseBatch; ++u)
-        if (key[u] >= 0) place(u, e_at + u);
+        if (key[u] >= 0) place(u, (int)(e_at + u));
     });
     if (!once) cluster_arrive();
     cluster_wait();  // (no CTA exits before its word is read)
