@@ -32,12 +32,14 @@ __device__ __forceinline__ int clamped_length(int L, int maxb, int BS, int32_t* 
   return (int)min(max((long long)L, 0LL), cap);
 }
 
-// The two halves of the cluster's barrier.
+// The two halves of the cluster's barrier.  (Not the aligned forms: the loops ahead of them end
+// earlier for some threads of a warp than for others, and nothing says that the warp is
+// together again.)
 __device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Exclusive sum over the block's threads; the block's total in every thread.  `warp_sums`
