@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(kForkThreads, 1)
   const int pieces = max(1, (int)page / kForkPiece);  // of a run at most: 1, 2 or 4
   const int shift = pieces == 4 ? 2 : pieces - 1;
   uint32_t phase = 0;
+  bool lost = false;  // a copy did not come (never expected): this warp's barrier is not used again
   for (int f0 = first / pairs; (long long)f0 * pairs < last; f0 += kForkThreads) {
     const int r0 = max(first, f0 * pairs);  // this batch's runs
     const int r1 = (int)min((long long)last, ((long long)f0 + kForkThreads) * pairs);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(kForkThreads, 1)
     };
     const long long most = (long long)(r1 - r0) * pieces;
     auto find = [&](long long& q, Piece& x) -> bool {  // this warp's next one from place q on
-      for (; q < most; q += kForkWarps) {
+      for (; !lost && q < most; q += kForkWarps) {
         // (pieces is a power of two, at most four)
         const int r = r0 + (int)(q >> shift), piece = (int)q & (pieces - 1);
         const int k = (int)((uint32_t)r / (uint32_t)pairs) - f0, pair = r - (k + f0) * pairs;
@@ -306,6 +307,9 @@ __global__ void __launch_bounds__(kForkThreads, 1)
     auto load = [&](const Piece& x) {
       if (lane == 0) {
         mbar_arrive_expect_tx(full_bar, (uint32_t)x.bytes);
+#ifdef PAGED_ATTN_WAIT_TEST
+        if (x.at == 0 && x.to == p.test_skip_page) return;  // (armed and never filled)
+#endif
         bulk_load(place, x.cache + x.from * page + x.at, (uint32_t)x.bytes, full_bar);
       }
       if (x.floats != nullptr && x.at == 0 && lane < x.tail)
@@ -337,15 +341,18 @@ __global__ void __launch_bounds__(kForkThreads, 1)
       }
     }
     while (some) {
+      bool landed = true;
       if (lane == 0) {
-        if (mbar_wait(full_bar, phase)) {
+        landed = mbar_wait(full_bar, phase);
+        if (landed) {
           bulk_store(x.cache + x.to * page + x.at, place, (uint32_t)x.bytes);
-        } else {  // never expected: a copy that may still land
+        } else {
           report(p.status, kTimeout);
-          mbar_wait(full_bar, phase);
+          mbar_wait(full_bar, phase);  // (no copy may be in flight when the CTA exits)
         }
         bulk_store_read();  // the place is free again
       }
+      lost = !__shfl_sync(0xffffffffu, landed, 0);
       phase ^= 1u;
       __syncwarp();
       q += kForkWarps;

@@ -41,6 +41,11 @@ struct ForkParams {
   int32_t* refused;             // [1] or null
   int num_forks, num_rows, maxb, free_capacity;
   int32_t* status;
+#ifdef PAGED_ATTN_WAIT_TEST
+  // Test build only: the copy of the K or V rows to this KV head page (block * H_kv + head) is
+  // waited for and never issued.  -1: off.
+  long long test_skip_page;
+#endif
 };
 
 struct ReleaseParams {

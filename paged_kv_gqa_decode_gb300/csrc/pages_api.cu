@@ -55,10 +55,23 @@ CacheRows cache_rows(void* k_cache, void* v_cache, float* k_scale, float* v_scal
   return c;
 }
 
+#ifdef PAGED_ATTN_WAIT_TEST
+thread_local long long g_test_skip_page = -1;
+#endif
+
 }  // namespace
 }  // namespace pagedattn
 
 using namespace pagedattn;
+
+#ifdef PAGED_ATTN_WAIT_TEST
+// Test build only (not in include/paged_attn.h): the next forks of this thread wait for copies to KV
+// head page `page` that they do not issue (-1: off).
+extern "C" PAGED_ATTN_API int paged_attn_test_set_fork_fault(long long page) {
+  g_test_skip_page = page;
+  return PAGED_ATTN_OK;
+}
+#endif
 
 int paged_kv_rope_append_slots(const void* q, const void* k_new, const void* v_new,
                                long long q_stride, long long k_stride, long long v_stride,
@@ -192,6 +205,9 @@ int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
   p.maxb = max_blocks_per_seq;
   p.free_capacity = free_capacity;
   p.status = api_check_status();
+#ifdef PAGED_ATTN_WAIT_TEST
+  p.test_skip_page = g_test_skip_page;
+#endif
   return done(launch_fork(p, sms, static_cast<cudaStream_t>(stream)));
 }
 
