@@ -703,7 +703,8 @@ PAGED_ATTN_API int paged_kv_append_slots(const void* k_new, const void* v_new,
  *   q, k_new, v_new  rows at their strides as paged_kv_append_slots (slices of one fused
  *                 projection need no copy); device memory
  *   q_out         [rows, H_q, head_dim]  bf16 (written); may be q where q_stride = H_q *
- *                 head_dim, else apart from all inputs
+ *                 head_dim, else apart from all inputs (PAGED_ATTN_ERR_POINTER where it
+ *                 meets a row of q, k_new or v_new)
  *   k_scale, v_scale  [num_blocks, H_kv, block_size]  float32 (written), or both null; with
  *                 them head_dim is 128 or 256
  *   slot_map      [rows]  int64.  A slot outside [0, num_blocks * block_size) writes no K

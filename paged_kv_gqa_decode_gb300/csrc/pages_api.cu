@@ -41,6 +41,16 @@ bool cache_pointers(const void* k_cache, const void* v_cache, const float* k_sca
   return aligned16(k_scale) && aligned16(v_scale);
 }
 
+// Whether bytes [out, out + size) meet one of the rows of `row` bytes, `stride` apart.
+bool meets_rows(const void* out, long long size, const void* src, long long row, long long stride,
+                int rows) {
+  const long long from = (long long)(reinterpret_cast<uintptr_t>(out) -
+                                     reinterpret_cast<uintptr_t>(src));  // out's place behind src
+  // the first row that ends past `from`
+  const long long r = from < row ? 0 : (from - row) / stride + 1;
+  return r < rows && r * stride < from + size;
+}
+
 CacheRows cache_rows(void* k_cache, void* v_cache, float* k_scale, float* v_scale, int H_kv,
                      int head_dim, int block_size, long long num_blocks) {
   CacheRows c;
@@ -101,7 +111,15 @@ int paged_kv_rope_append_slots(const void* q, const void* k_new, const void* v_n
   if (rotary_dim > 0 && (!aligned4(positions) || !aligned16(cos_sin) ||
                          (freq_axis != nullptr && !aligned16(freq_axis))))
     return PAGED_ATTN_ERR_POINTER;
-  if (q_out == q && q_stride != q_row) return PAGED_ATTN_ERR_POINTER;  // rows over one another
+  // q_out is q, row by row, or apart from what is read: a row written over another one is
+  // written before or after that one is read
+  const long long out_bytes = 2 * q_row * rows;
+  if ((q_out != q || q_stride != q_row) &&
+      meets_rows(q_out, out_bytes, q, 2 * q_row, 2 * q_stride, rows))
+    return PAGED_ATTN_ERR_POINTER;
+  if (meets_rows(q_out, out_bytes, k_new, 2 * kv_row, 2 * k_stride, rows) ||
+      meets_rows(q_out, out_bytes, v_new, 2 * kv_row, 2 * v_stride, rows))
+    return PAGED_ATTN_ERR_POINTER;
   int sms = 0;
   if ((rc = api_sms(&sms)) != PAGED_ATTN_OK) return rc;
   RopeParams p;

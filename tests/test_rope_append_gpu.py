@@ -172,6 +172,36 @@ def test_strides_and_queries_in_place():
     run_case(1, 8, 2, 64, 16, 64, in_place=True)
 
 
+@pytest.mark.parametrize("at", ["before", "behind", "between"])
+def test_queries_out_next_to_the_inputs(at):
+    """Directly before, behind and between the rows of a projection that lie far apart."""
+    rows, H_q, H_kv, D = 3, 2, 1, 64
+    width, size = (H_q + 2 * H_kv) * D, rows * H_q * D
+    stride = width + size if at == "between" else width + 8
+    x = torch.randn(2 * size + rows * stride, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    fused = x[size:size + rows * stride].view(rows, stride)
+    last = size + (rows - 1) * stride + width
+    at = {"before": 0, "behind": last, "between": size + width}[at]
+    out = x[at:at + size].view(rows, H_q, D)
+    a, b = H_q * D, (H_q + H_kv) * D
+    q, k, v = (t.unflatten(1, (-1, D)) for t in (fused[:, :a], fused[:, a:b], fused[:, b:width]))
+    slots, pos = torch.arange(rows, device="cuda"), torch.arange(rows, dtype=torch.int32, device="cuda")
+    cs = torch.tensor(table(8, D)).cuda()
+    want = None
+    for o in (None, out):
+        kc, vc = (torch.zeros(1, H_kv, 16, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        got = (pa.paged_kv_rope_append_slots(q, k, v, kc, vc, slots, pos, cs, out=o), kc, vc)
+        assert want is None or all(torch.equal(s, t) for s, t in zip(got, want))
+        want = got
+    with pytest.raises(pa.PagedAttnError):
+        pa.paged_kv_rope_append_slots(q, k, v, kc, vc, slots, pos, cs, out=x[size + 8:][:size].view(rows, H_q, D))
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(4, 1), (8, 2), (3, 3)])
+def test_few_heads_in_many_rows_of_fp8_caches(H_q, H_kv):
+    run_case(2500, H_q, H_kv, 128, 16, 96, seed=H_q, fp8=True)
+
+
 def test_small_and_large_values():
     run_case(20, 4, 2, 128, 16, 128, scale=1e-18, eps=0.0)
     run_case(20, 4, 2, 128, 16, 128, scale=1e15)

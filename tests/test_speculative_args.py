@@ -51,6 +51,19 @@ def test_rope_append_refuses(lib, kw, code):
     assert lib.paged_kv_rope_append_slots(*dict(ROPE, **kw).values()) == code
 
 
+# q at 2^20, three rows of 2048 bytes 8192 apart; k and v far from it, rows of 512 bytes 1024 apart
+APART = dict(ROPE, q=2 ** 20, qs=4096, k=2 ** 24, ks=512, v=2 ** 25, vs=512, pos=2 ** 10, slots=2 ** 10)
+
+
+@pytest.mark.parametrize("out", [
+    2 ** 20 - 6144 + 16, 2 ** 20, 2 ** 20 + 16, 2 ** 20 + 2032, 2 ** 20 + 2064, 2 ** 20 + 2 * 8192 + 2032,
+    2 ** 24 - 6144 + 16, 2 ** 24, 2 ** 24 + 2 * 1024 + 496, 2 ** 25 - 16, 2 ** 25 + 512, 2 ** 25 + 2 * 1024 + 496,
+])
+def test_rope_append_refuses_queries_out_over_its_inputs(lib, out):
+    """3 rows of 2048 bytes in one: from the last place before an input to the last one in it."""
+    assert lib.paged_kv_rope_append_slots(*dict(APART, out=out).values()) == -1
+
+
 COMPACT = dict(kc=16, vc=16, kf=None, vf=None, qo=16, acc=16, bt=16, sl=16, out=32, n=2, most=4,
                H_kv=2, D=128, maxb=4, BS=16, nb=5, stream=None)
 
