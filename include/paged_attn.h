@@ -786,8 +786,9 @@ PAGED_ATTN_API int paged_kv_compact(void* k_cache, void* v_cache, float* k_scale
  *
  * A fork is refused, its child left empty, when its block is not in the free stack or
  * a row is outside [0, num_rows).  With checks on, a block id outside [0, num_blocks) sets
- * bit 0 of the status word (it is handed on, not copied), an invalid row or length bit 1, a
- * copy that did not come bit 2.  PAGED_ATTN_ERR_SIZES for 2 num_forks H_kv past 2^30.
+ * bit 0 of the status word (it is handed on, not copied), an invalid row or length bit 1, as
+ * does, in a call of up to 65536 forks, a child that is a parent or twice a child; a copy
+ * that did not come sets bit 2.  PAGED_ATTN_ERR_SIZES for 2 num_forks H_kv past 2^30.
  * k_scale, v_scale, sizes and errors as paged_kv_compact.  Asynchronous; allocates nothing.
  */
 PAGED_ATTN_API int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, float* v_scale,

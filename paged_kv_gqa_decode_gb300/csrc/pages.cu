@@ -176,6 +176,9 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
 // first run does its table row and the counts of its blocks.
 constexpr int kForkThreads = 512, kForkWarps = kForkThreads / 32;
 constexpr int kForkPiece = 4096;
+// Calls of up to so many forks are looked through for children that are parents or children of
+// other forks (with checks on): all pairs.
+constexpr int kForkChecked = 65536;
 constexpr size_t kForkSmem = (size_t)kForkWarps * (kForkPiece + 8);
 
 struct Fork {
@@ -266,6 +269,12 @@ __global__ void __launch_bounds__(kForkThreads, 1)
         }
         if (f.child >= 0 && f.child < p.num_rows && f.child != f.parent)
           p.seq_lens[f.child] = given ? f.len : 0;
+        if (p.status != nullptr && n <= kForkChecked && f.valid) {
+          bool other = false;
+          for (int j = 0; j < n; ++j)
+            other |= p.parents[j] == f.child || (j != i && p.children[j] == f.child);
+          if (other) report(p.status, kBadLength);
+        }
       }
       if (given && f.need &&
           (from < 0 || from >= p.cache.num_blocks || to < 0 || to >= p.cache.num_blocks)) {

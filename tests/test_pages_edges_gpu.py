@@ -41,3 +41,23 @@ def test_release_of_a_table_that_just_fits_its_keys(bad):
     assert torch.equal(stack[:at], flat[:at])
     if bad:
         assert torch.equal(stack[at:-1], flat[at + 1:]) and int(stack[-1]) == -2
+
+
+@pytest.mark.parametrize("parents,children,want", [
+    ([0, 0, 1], [2, 3, 4], 0), ([0, 2], [2, 3], 2), ([2, 0], [3, 2], 2), ([0, 1], [3, 3], 2),
+    ([0] * 600 + [599], list(range(1, 601)) + [601], 2), ([0] * 600, list(range(1, 601)), 0),
+    ([0] * 600, list(range(1, 600)) + [1], 2), ([0, 7], [3, -1], 2),
+])
+def test_children_that_are_parents_or_twice_children_are_reported(parents, children, want):
+    """All rows hold the same token counts and pages of the pool, whichever is read first."""
+    rows = 602
+    k, v = (torch.zeros(640, 1, 16, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bt, lens = i32([[0, 1]] * rows), i32([20] * rows)
+    refs, free, status = i32([0] * 640), i32(range(2, 640)), i32([0])
+    try:
+        pa.paged_attn_set_checks(640, status)
+        pa.paged_kv_fork(k, v, bt, lens, i32(parents), i32(children), refs, free, i32([638]))
+        torch.cuda.synchronize()
+    finally:
+        pa.paged_attn_set_checks(0, None)
+    assert int(status) == want
