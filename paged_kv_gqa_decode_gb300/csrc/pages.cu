@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
 constexpr int kForkThreads = 512, kForkWarps = kForkThreads / 32;
 constexpr int kForkPiece = 4096;
 // Calls of up to so many forks are looked through for children that are parents or children of
-// other forks (with checks on): all pairs.
+// other forks (with checks on): all pairs, 65536 forks 0.15 -> 6.1 ms.
 constexpr int kForkChecked = 65536;
 constexpr size_t kForkSmem = (size_t)kForkWarps * (kForkPiece + 8);
 
