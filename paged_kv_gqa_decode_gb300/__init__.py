@@ -8,12 +8,13 @@ calls raise.  The entry points of speculative and parallel decoding (trees, rota
 with the append, compaction, forks, release) are marshalled by a native module
 (``csrc/binding.cpp``), as an engine's step waits for the host in them.
 
-An output that one of those makes under ``stream=`` is that stream's memory, as if made under
+An output that a call makes under ``stream=`` is that stream's memory, as if made under
 ``torch.cuda.stream(stream)``: another stream that uses it waits for that one, and
 holds it with ``record_stream``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -295,6 +296,30 @@ def _stream(stream) -> int:
     return int(s.cuda_stream)
 
 
+def _owned_by(stream, like):
+    """The context in which an output of a call on ``stream`` (None: the current one) is made: it is that
+    stream's memory, as a block of the current stream's may still be in use there, or be
+    given away again before the call's kernels have run."""
+    if stream is None or not like.is_cuda:
+        return contextlib.nullcontext()
+    import torch
+
+    if not isinstance(stream, torch.cuda.Stream):  # anything with a handle
+        handle = int(stream.cuda_stream)
+        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle
+                  else torch.cuda.default_stream(like.device))
+    return torch.cuda.stream(stream)
+
+
+def _empty_like(like, stream):
+    import torch
+
+    if stream is None:
+        return torch.empty_like(like)
+    with _owned_by(stream, like):
+        return torch.empty_like(like)
+
+
 def _sizes(q, k_cache, block_tables):
     num_seqs, H_q, D = (int(x) for x in q.shape)
     _, H_kv, BS, Dk = (int(x) for x in k_cache.shape)
@@ -317,10 +342,8 @@ def _args(q, k_cache, v_cache, out, block_tables, seq_lens, scale):
 def paged_attn_decode(q, k_cache, v_cache, block_tables, seq_lens, scale: float, out=None,
                       stream=None):
     """out[s, h] = softmax(scale * q[s, h] . K^T) . V over the paged cache (see paged_attn.h)."""
-    import torch
-
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check(load().paged_attn_decode(*_args(q, k_cache, v_cache, out, block_tables, seq_lens,
                                            scale), _stream(stream)))
     return out
@@ -335,10 +358,8 @@ def paged_attn_workspace_bytes(num_seqs: int, H_q: int, H_kv: int, head_dim: int
 def paged_attn_decode_ws(q, k_cache, v_cache, block_tables, seq_lens, scale: float, workspace,
                          out=None, stream=None):
     """As paged_attn_decode, with a caller-owned zero-initialised uint8 device workspace."""
-    import torch
-
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check(load().paged_attn_decode_ws(*_args(q, k_cache, v_cache, out, block_tables, seq_lens,
                                               scale), _ptr(workspace),
                                        int(workspace.numel() * workspace.element_size()),
@@ -350,10 +371,8 @@ def paged_attn_decode_checked(q, k_cache, v_cache, block_tables, seq_lens, scale
                               status, out=None, stream=None, num_blocks: Optional[int] = None):
     """As paged_attn_decode, validating block ids and lengths on the device into ``status``
     (an int32 device tensor of one element that the caller zero-fills)."""
-    import torch
-
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     nb = int(k_cache.shape[0]) if num_blocks is None else int(num_blocks)
     _check(load().paged_attn_decode_checked(*_args(q, k_cache, v_cache, out, block_tables,
                                                    seq_lens, scale), nb, _ptr(status),
@@ -367,10 +386,8 @@ def paged_attn_decode_static(q, k_cache, v_cache, block_tables, seq_lens, scale:
     library's fixed 4 MiB scratch array stands in for the workspace (see paged_attn.h;
     calls that overlap on the GPU race on that array).  ``out`` should be passed in by
     such callers, since creating it here would allocate."""
-    import torch
-
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check(load().paged_attn_decode_static(*_args(q, k_cache, v_cache, out, block_tables,
                                                   seq_lens, scale), _stream(stream)))
     return out
@@ -380,8 +397,6 @@ def paged_attn_decode_xpacked(q, kx, vt, block_tables, seq_lens, scale: float, o
                               stream=None):
     """Decode over x-packed bf16 caches (see paged_attn.h): kx [num_blocks, H_kv,
     head_dim / 8, block_size, 8], vt [num_blocks, H_kv, head_dim, block_size]."""
-    import torch
-
     for name, t in (("q", q), ("kx", kx), ("vt", vt), ("block_tables", block_tables),
                     ("seq_lens", seq_lens)):
         if not t.is_contiguous():
@@ -393,7 +408,7 @@ def paged_attn_decode_xpacked(q, kx, vt, block_tables, seq_lens, scale: float, o
     if x != 8 or dx * 8 != D or tuple(vt.shape) != (nb, H_kv, D, BS):
         raise ValueError("kx / vt shapes do not match q's head_dim")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     if not out.is_contiguous():
         raise ValueError("out must be contiguous")
     maxb = int(block_tables.shape[1]) if block_tables.dim() == 2 else 0
@@ -426,14 +441,12 @@ def paged_attn_decode_multi(q, k_cache, v_cache, qo_indptr, block_tables, seq_le
     """Multi-token decode (see paged_attn.h): q [total_q, H_q, D], sequence s owning
     rows qo_indptr[s] .. qo_indptr[s+1] - 1 (its last tokens); causal, or every
     row attending all of the sequence's tokens with ``causal=False``."""
-    import torch
-
     num_seqs, total_q, H_q, H_kv, D, maxb, BS = _multi_sizes(
         q, k_cache, qo_indptr, block_tables, seq_lens,
         dict(q=q, k_cache=k_cache, v_cache=v_cache, qo_indptr=qo_indptr,
              block_tables=block_tables, seq_lens=seq_lens))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check(load().paged_attn_decode_multi_ex(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out),
                                              _ptr(qo_indptr), _ptr(block_tables),
                                              _ptr(seq_lens), num_seqs, total_q, int(max_q_len),
@@ -460,15 +473,13 @@ def paged_attn_append_decode_multi(q, k_new, v_new, k_cache, v_cache, qo_indptr,
                                    seq_lens, scale: float, max_q_len: int, out=None,
                                    stream=None, causal: bool = True):
     """paged_kv_append_multi then paged_attn_decode_multi (see paged_attn.h)."""
-    import torch
-
     _check_rows(k_new, v_new, q, k_cache)
     num_seqs, total_q, H_q, H_kv, D, maxb, BS = _multi_sizes(
         q, k_cache, qo_indptr, block_tables, seq_lens,
         dict(q=q, k_cache=k_cache, v_cache=v_cache, qo_indptr=qo_indptr,
              block_tables=block_tables, seq_lens=seq_lens))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     _check(load().paged_attn_append_decode_multi(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(out),
         _ptr(qo_indptr), _ptr(block_tables), _ptr(seq_lens), num_seqs, total_q, int(max_q_len),
@@ -501,11 +512,9 @@ def paged_kv_append(k_new, v_new, k_cache, v_cache, block_tables, seq_lens, stre
 def paged_attn_append_decode(q, k_new, v_new, k_cache, v_cache, block_tables, seq_lens,
                              scale: float, out=None, stream=None):
     """paged_kv_append then paged_attn_decode, fused into one launch (see paged_attn.h)."""
-    import torch
-
     _check_rows(k_new, v_new, q, k_cache)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     a = _args(q, k_cache, v_cache, out, block_tables, seq_lens, scale)
     # (q, k_new, v_new, k_cache, v_cache, out, tables, lens, sizes..., scale)
     _check(load().paged_attn_append_decode(a[0], _ptr(k_new), _ptr(v_new), a[1], a[2], a[3],
@@ -529,7 +538,7 @@ def paged_attn_decode_fp8(q, k8, v8, k_scale, v_scale, block_tables, seq_lens, s
             tuple(k_scale.shape) != tuple(k8.shape[:3]) or k_scale.shape != v_scale.shape:
         raise ValueError("k_scale / v_scale must be float32 [num_blocks, H_kv, block_size]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     a = _args(q, k8, v8, out, block_tables, seq_lens, scale)
     # (q, k8, v8, k_scale, v_scale, out, tables, lens, sizes..., scale)
     _check(load().paged_attn_decode_fp8(a[0], a[1], a[2], _ptr(k_scale), _ptr(v_scale), a[3],
@@ -568,12 +577,10 @@ def paged_kv_append_fp8(k_new, v_new, k8, v8, k_scale, v_scale, block_tables, se
 def paged_attn_append_decode_fp8(q, k_new, v_new, k8, v8, k_scale, v_scale, block_tables,
                                  seq_lens, scale: float, out=None, stream=None):
     """paged_kv_append_fp8 then paged_attn_decode_fp8 (see paged_attn.h)."""
-    import torch
-
     _check_fp8_cache(k8, v8, k_scale, v_scale)
     _check_rows(k_new, v_new, q, k8)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     a = _args(q, k8, v8, out, block_tables, seq_lens, scale)
     # (q, k_new, v_new, k8, v8, k_scale, v_scale, out, tables, lens, sizes..., scale)
     _check(load().paged_attn_append_decode_fp8(a[0], _ptr(k_new), _ptr(v_new), a[1], a[2],
@@ -635,7 +642,7 @@ def _raw_stream(stream, device) -> int:
 
 
 def _mods_problem(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens,
-                  doc_starts, workspace, cache_dtype, rows=None):
+                  doc_starts, workspace, cache_dtype, stream, rows=None):
     """Checks the tensors of a decode call with score options; returns the sizes, out and
     the device."""
     import torch
@@ -666,7 +673,7 @@ def _mods_problem(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty_like(q, stream)
     else:
         _need("out", out, torch.bfloat16, qs)
     device = _same_device(q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes,
@@ -694,7 +701,7 @@ def paged_attn_decode_mods(q, k_cache, v_cache, block_tables, seq_lens, scale: f
     softcap, window = _softcap(softcap), _int32("window", window)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
-        workspace, torch.bfloat16)
+        workspace, torch.bfloat16, stream)
     _check((_lib or load()).paged_attn_decode_mods(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(),
         block_tables.data_ptr(), seq_lens.data_ptr(), n, H_q, H_kv, D, maxb, BS, float(scale),
@@ -713,7 +720,7 @@ def paged_attn_decode_fp8_mods(q, k8, v8, k_scale, v_scale, block_tables, seq_le
     softcap, window = _softcap(softcap), _int32("window", window)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k8, v8, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts, workspace,
-        torch.uint8)
+        torch.uint8, stream)
     _need("k_scale", k_scale, torch.float32, k8.shape[:3])
     _need("v_scale", v_scale, torch.float32, k8.shape[:3])
     _same_device(k_scale, v_scale)
@@ -746,7 +753,7 @@ def paged_attn_decode_multi_mods(q, k_cache, v_cache, qo_indptr, block_tables, s
     softcap, window = _softcap(softcap), _int32("window", window)
     total_q, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, prefix_lens, doc_starts,
-        workspace, torch.bfloat16, rows="many")
+        workspace, torch.bfloat16, stream, rows="many")
     _need("qo_indptr", qo_indptr, torch.int32, (n + 1,))
     _same_device(qo_indptr)
     _check((_lib or load()).paged_attn_decode_multi_mods(
@@ -779,7 +786,7 @@ def paged_attn_decode_shared(q, k_cache, v_cache, group_indptr, prefix_tables, p
     softcap = _softcap(softcap)
     _, n, H_q, H_kv, D, maxb, BS, out, dev = _mods_problem(
         q, k_cache, v_cache, block_tables, seq_lens, out, alibi_slopes, None, None, workspace,
-        torch.bfloat16)
+        torch.bfloat16, stream)
     if prefix_tables.dim() != 2:
         raise ValueError("prefix_tables must be [num_groups, prefix_max_blocks]")
     groups, pmax = prefix_tables.shape
@@ -829,19 +836,21 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
     _need("free_count", free_count, i32, (1,))
     where = seq_lens.device
     if seq_lens_out is None:
-        seq_lens_out = torch.empty_like(seq_lens)
+        seq_lens_out = _empty_like(seq_lens, stream)
     else:
         _need("seq_lens_out", seq_lens_out, i32, (n,))
     if qo_indptr is None:
-        qo_indptr = torch.empty(n + 1, dtype=i32, device=where)
+        with _owned_by(stream, seq_lens):
+            qo_indptr = torch.empty(n + 1, dtype=i32, device=where)
     else:
         _need("qo_indptr", qo_indptr, i32, (n + 1,))
     if slot_map is None:
-        slot_map = torch.empty(max_new, dtype=torch.int64, device=where)
+        with _owned_by(stream, seq_lens):
+            slot_map = torch.empty(max_new, dtype=torch.int64, device=where)
     else:
         _need("slot_map", slot_map, torch.int64, (max_new,))
     if free_count_out is None:
-        free_count_out = torch.empty_like(free_count)
+        free_count_out = _empty_like(free_count, stream)
     else:
         _need("free_count_out", free_count_out, i32, (1,))
     if refused is not None:

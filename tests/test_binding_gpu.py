@@ -1,5 +1,5 @@
-"""The native marshalling beside other streams, other threads and host memory: who may use the memory
-of an output that the call makes, and when."""
+"""The calls beside other streams, other threads and host memory: who may use the memory of an output that
+a call makes, and when."""
 import ctypes
 import importlib.machinery
 import importlib.util
@@ -56,6 +56,8 @@ class Problem:
         self.free, self.count, self.refs = i32([2, 4, 0, 0, 0, 0, 0, 0]), i32([2]), i32([0] * 8)
         self.row_lens = i32([40, 23, 0])
         self.accepted, self.keep = i32([[0, 3, 5], [2, -1, -1]]), i32([17, 0])
+        self.new = i32([3, 6])
+        self.kx = self.k.view(8, 2, 16, 16, 8).transpose(2, 3).contiguous()
         self.parents, self.children = i32([0]), i32([2])
         self.ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
 
@@ -77,8 +79,35 @@ class Problem:
     def release(self, **kw):
         return list(pa.paged_kv_release(self.bt[:2], self.lens, self.keep, self.free, self.count, 16, **kw))
 
+    # those that are marshalled in Python
+    def decode(self, **kw):
+        return [pa.paged_attn_decode(self.q[:2], self.k, self.v, self.bt[:2], self.lens, 0.1, **kw)]
+
+    def xpacked(self, **kw):
+        return [pa.paged_attn_decode_xpacked(self.q[:2], self.kx, self.k.view(8, 2, 128, 16), self.bt[:2],
+                                             self.lens, 0.1, **kw)]
+
+    def multi(self, **kw):
+        return [pa.paged_attn_decode_multi(self.q, self.k, self.v, self.qo, self.bt[:2], self.lens, 0.1, 6, **kw)]
+
+    def append_decode(self, **kw):
+        return [pa.paged_attn_append_decode(self.q[:2], self.kn[:2], self.vn[:2], self.k, self.v, self.bt[:2],
+                                            self.lens, 0.1, **kw)]
+
+    def mods(self, **kw):
+        return [pa.paged_attn_decode_mods(self.q[:2], self.k, self.v, self.bt[:2], self.lens, 0.1, softcap=20.0,
+                                          workspace=self.ws, **kw)]
+
+    def multi_mods(self, **kw):
+        return [pa.paged_attn_decode_multi_mods(self.q, self.k, self.v, self.qo, self.bt[:2], self.lens, 0.1,
+                                                window=30, workspace=self.ws, **kw)]
+
+    def assign(self, **kw):
+        return list(pa.paged_kv_assign(self.lens, self.new, self.bt[:2], self.free, self.count, 16, 9, **kw))
+
 
 CALLS = ["tree", "rope", "compact", "fork", "release"]
+PYTHON = ["decode", "xpacked", "multi", "append_decode", "mods", "multi_mods", "assign"]
 
 
 def crowd(sizes):
@@ -86,7 +115,7 @@ def crowd(sizes):
     return [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(5000 if n < 512 else 200)]
 
 
-@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("call", CALLS + PYTHON)
 def test_made_outputs_are_the_given_streams_memory(call):
     """Blocks freed on the current stream with a write still to come do not become the outputs of a call on
     another stream."""
@@ -110,7 +139,7 @@ def test_made_outputs_are_the_given_streams_memory(call):
     del held
 
 
-@pytest.mark.parametrize("call", CALLS)
+@pytest.mark.parametrize("call", CALLS + PYTHON)
 def test_a_dropped_output_is_not_given_to_the_current_stream_at_once(call):
     want = getattr(Problem(), call)()
     s = torch.cuda.Stream()
