@@ -135,15 +135,14 @@ class Call {
   // pinned tensor.  With a stream given it is that stream's memory: the allocator may give a
   // block of the current stream's whose last use there is still to come, and may give it
   // away again before the call's kernels have run.
-  Tensor make(const Tensor& like, IntArrayRef shape) {
+  Tensor make(const Tensor& like) {
     if (device_ < 0) device_ = c10::cuda::current_device();
     const auto device = static_cast<c10::DeviceIndex>(device_);
     const auto options = like.options().device(c10::Device(c10::DeviceType::CUDA, device));
-    const Unlocked others;
     if (!given_ || c10::cuda::getCurrentCUDAStream(device).stream() == stream_)
-      return at::empty(shape, options);
+      return at::empty(like.sizes(), options);
     c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(stream_, device));
-    return at::empty(shape, options);
+    return at::empty(like.sizes(), options);
   }
 
  private:
@@ -184,7 +183,7 @@ bool truth(PyObject* o) {
   if (v < 0) throw Raised();
   return v != 0;
 }
-// A call into the library, and its status as an exception.
+// A call into the library, with the outputs that it makes, and its status as an exception.
 template <typename... P, typename... A>
 void run(int (*f)(P...), A... a) {
   int status;
@@ -228,7 +227,7 @@ struct Caches {
 
 constexpr ScalarType kI32 = ScalarType::Int;
 
-// An output: the tensor given, checked, or one that is made once the inputs' device is.
+// An output: the tensor given, checked, or one like an input that is made when the library is called.
 struct Output {
   PyObject* object;
   const Tensor* given;
@@ -237,10 +236,20 @@ struct Output {
       : object(o), given(c.optional(o, name)) {
     if (given) c.need(*given, name, dtype, shape);
   }
-  const Tensor& get(Call& c, const Tensor& like, IntArrayRef shape) {
-    if (given) return *given;
-    made = c.make(like, shape);
-    return made;
+  // An argument of `run`, which turns it into the pointer.
+  struct Pointer {
+    Output& output;
+    Call& call;
+    const Tensor& like;
+    void* known;
+    template <typename T>
+    operator T*() const {
+      if (!output.given) output.made = call.make(like);
+      return static_cast<T*>(output.given ? known : output.made.data_ptr());
+    }
+  };
+  Pointer at(Call& c, const Tensor& like) {
+    return {*this, c, like, given ? c.at(*given) : nullptr};
   }
   PyObject* result() const {  // a new reference
     if (!given) return THPVariable_Wrap(made);
@@ -284,8 +293,7 @@ PyObject* decode_tree(PyObject* const* a, Py_ssize_t n) {
   if (ws && !ws->is_contiguous()) refuse("workspace must be contiguous");
   Output made(c, a[12], "out", ScalarType::BFloat16, q.sizes());
   const void *pq = c.at(q), *pk = c.on_device(k, "k_cache"), *pv = c.on_device(v, "v_cache");
-  const Tensor& out = made.get(c, q, q.sizes());
-  run(entry.tree, pq, pk, pv, c.at(out), c.as<int32_t>(qo), c.as<int32_t>(mask),
+  run(entry.tree, pq, pk, pv, made.at(c, q), c.as<int32_t>(qo), c.as<int32_t>(mask),
       int32_size(mask.size(1), "tree_mask's words"), c.as<int32_t>(bt), c.as<int32_t>(lens),
       int32_size(seqs, "num_seqs"), int32_size(rows, "total_q"), int32_size(H, "H_q"),
       int32_size(k.size(1), "H_kv"), int32_size(q.size(2), "head_dim"),
@@ -326,8 +334,7 @@ PyObject* rope_append_slots(PyObject* const* a, Py_ssize_t n) {
   Output made(c, a[15], "out", ScalarType::BFloat16, q.sizes());
   const void *pq = c.on_device(q, "q"), *pk = c.on_device(kn, "k_new"),
              *pv = c.on_device(vn, "v_new");
-  const Tensor& out = made.get(c, q, q.sizes());
-  run(entry.rope, pq, pk, pv, qs, ks, vs, c.at(out), c.on_device(cache.k, "k_cache"),
+  run(entry.rope, pq, pk, pv, qs, ks, vs, made.at(c, q), c.on_device(cache.k, "k_cache"),
       c.on_device(cache.v, "v_cache"), c.as<float>(cache.k_scale), c.as<float>(cache.v_scale),
       c.as<int64_t>(slots), c.as<int32_t>(pos), int32_size(axes, "axes"), c.as<int32_t>(axis),
       c.as<float>(cs), int32_size(cs.size(0), "max_positions"),
@@ -352,10 +359,9 @@ PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   c.need(bt, "block_tables", kI32, {seqs, bt.size(1)});
   Output made(c, a[8], "seq_lens_out", kI32, {seqs});
   int32_t* plens = c.as<int32_t>(lens);
-  const Tensor& out = made.get(c, lens, {seqs});
   run(entry.compact, c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
       c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int32_t>(qo),
-      c.as<int32_t>(acc), c.as<int32_t>(bt), plens, c.as<int32_t>(out),
+      c.as<int32_t>(acc), c.as<int32_t>(bt), plens, made.at(c, lens),
       int32_size(seqs, "num_seqs"), int32_size(acc.size(1), "max_accept"), cache.H, cache.D,
       int32_size(bt.size(1), "max_blocks"), cache.BS, cache.nb, c.stream());
   return made.result();
@@ -383,12 +389,11 @@ PyObject* fork(PyObject* const* a, Py_ssize_t n) {
   if (refused) c.need(*refused, "refused", kI32, {1});
   Output made(c, a[11], "free_count_out", kI32, {1});
   int32_t* pcount = c.as<int32_t>(count);
-  const Tensor& left = made.get(c, count, {1});
   c.on_device(refs, "block_refs");
   run(entry.fork, c.on_device(cache.k, "k_cache"), c.on_device(cache.v, "v_cache"),
       c.as<float>(cache.k_scale), c.as<float>(cache.v_scale), c.as<int32_t>(bt),
       c.as<int32_t>(lens), c.as<int32_t>(parents), c.as<int32_t>(children), c.as<int32_t>(refs),
-      c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(left), c.as<int32_t>(refused),
+      c.as<int32_t>(free_blocks), pcount, made.at(c, count), c.as<int32_t>(refused),
       int32_size(forks, "forks"), int32_size(rows, "rows"), cache.H, cache.D,
       int32_size(bt.size(1), "max_blocks"), cache.BS, int32_size(n_free, "free_blocks' length"),
       cache.nb, c.stream());
@@ -415,12 +420,10 @@ PyObject* release(PyObject* const* a, Py_ssize_t n) {
   Output made_lens(c, a[7], "seq_lens_out", kI32, {seqs});
   Output made_count(c, a[8], "free_count_out", kI32, {1});
   int32_t *plens = c.as<int32_t>(lens), *pcount = c.as<int32_t>(count);
-  const Tensor& out = made_lens.get(c, lens, {seqs});
-  const Tensor& left = made_count.get(c, count, {1});
   if (refs) c.on_device(*refs, "block_refs");
   run(entry.release, c.as<int32_t>(bt), plens, c.as<int32_t>(keep), c.as<int32_t>(refs),
-      refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount, c.as<int32_t>(out),
-      c.as<int32_t>(left), int32_size(seqs, "num_seqs"), int32_size(bt.size(1), "max_blocks"), BS,
+      refs ? refs->numel() : 0, c.as<int32_t>(free_blocks), pcount, made_lens.at(c, lens),
+      made_count.at(c, count), int32_size(seqs, "num_seqs"), int32_size(bt.size(1), "max_blocks"), BS,
       int32_size(n_free, "free_blocks' length"), c.stream());
   PyObject* x = made_lens.result();
   if (!x) return nullptr;
