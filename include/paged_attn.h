@@ -549,6 +549,12 @@ PAGED_ATTN_API size_t paged_attn_multi_mods_workspace_bytes(int num_seqs, int to
  * the difference of the two rows' positions for a drafted one.  A mask without bits
  * leaves the cached tokens (a padding node; pos = ctx - 1); a row that sees nothing is zero.
  *
+ * The window bounds cached tokens alone: a row sees each drafted token that it has a bit for,
+ * however far above it the node stands.  So the call is right for a layer whose window is at
+ * least as long as its trees are deep, and only there a chain is what
+ * paged_attn_decode_multi_mods makes of it.  (Bits taken out for far ancestors move the
+ * row's position, and with it the window over cached tokens and the bias.)
+ *
  *   tree_mask   [total_q, mask_words]  int32 (read; 16-byte aligned): any bits, those
  *               from q_len on are not used
  *   mask_words  1 .. 8: a drafted token from 32 * mask_words on has no bit and is seen by no
@@ -818,6 +824,10 @@ PAGED_ATTN_API int paged_kv_fork(void* k_cache, void* v_cache, float* k_scale, f
  *                 pool is enough; a block that finds none is lost (bit 1 of the status word)
  *   free_count    [1] int32; free_count_out [1] int32 may be free_count
  *   seq_lens_out  [num_seqs]  may be seq_lens or keep_lens
+ *
+ * A kept last page that is only partly kept and that other rows hold too stays shared: tokens
+ * appended to it would be theirs as well.  (Cut back into such a page, a sequence goes on
+ * in a spare row: paged_kv_fork of it copies the page.)
  *
  * The table entries keep their values.  Entries outside [0, num_blocks) (without
  * block_refs: below 0) are passed over (bit 0 with checks on).  The result does not depend

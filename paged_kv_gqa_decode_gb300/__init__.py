@@ -904,7 +904,8 @@ def paged_attn_decode_tree(q, k_cache, v_cache, qo_indptr, tree_mask, block_tabl
     of word j // 32 of a row is set where it sees drafted token j of its sequence (a node
     of a tree: itself and its ancestors).  A row's position is the tokens before the tree
     plus the drafted ones it sees, less one; the other options as
-    paged_attn_decode_multi_mods (``workspace``: paged_attn_tree_workspace_bytes)."""
+    paged_attn_decode_multi_mods (``workspace``: paged_attn_tree_workspace_bytes), but
+    ``window`` bounds the cached tokens alone: it is to be as long as the trees are deep."""
     return (_native or _load_native()).decode_tree(
         q, k_cache, v_cache, qo_indptr, tree_mask, block_tables, seq_lens, scale, softcap,
         alibi_slopes, window, prefix_lens, out, workspace, stream)
@@ -957,8 +958,8 @@ def paged_kv_fork(k_cache, v_cache, block_tables, seq_lens, parents, children, b
     filled last page copied to a block from the top of the free stack.  block_tables,
     seq_lens and block_refs are updated in place.  The children are distinct and none is
     a parent.  Returns the free count (``free_count_out``, which may be free_count);
-    ``refused``: an int32 tensor of one element that receives the number of forks for
-    which there was no block."""
+    ``refused``: an int32 tensor of one element that receives the number of forks that
+    had no block or named no row."""
     return (_native or _load_native()).fork(
         k_cache, v_cache, block_tables, seq_lens, parents, children, block_refs, free_blocks,
         free_count, k_scale, v_scale, free_count_out, refused, stream)

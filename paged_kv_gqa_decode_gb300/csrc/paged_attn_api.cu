@@ -846,8 +846,8 @@ int tile_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int sms,
 // can be counted (a tile of rows for each started 128 or 256 of the mean), and often the
 // same length.  Near 1.75 CTAs a place it takes the number of parts that fills the
 // last round of CTAs best (trees over four contexts of 100000 tokens, head_dim 256, 32 pieces
-// on 152 places, 4 / 5 / 7 / 9 / 10 / 12 / 14 / 19 parts 341 / 505 / 386 / 342 / 431 / 424 / 468
-// / 481 us).  No more than the block tables have pairs of token tiles: with one part there is no
+// on 152 places, 4 / 5 / 7 / 9 / 10 / 12 / 14 / 19 parts 358 / 505 / 391 / 363 / 426 / 421 / 456
+// / 477 us in a loop, the fast ones at the power cap).  No more than the block tables have pairs of token tiles: with one part there is no
 // merge (two chats of up to 112 tokens 11.9 -> 8.9 us).
 int tree_splits(int D, int total_q, int num_seqs, int H_q, int H_kv, int maxb, int BS, int sms) {
   const long long rows = (long long)total_q * (H_q / H_kv);

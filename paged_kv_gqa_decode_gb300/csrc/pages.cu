@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kCompactThreads) paged_kv_compact_kernel(const
   const int g = pair < H ? pair : pair - H;
   uint8_t* cache = pair < H ? p.cache.k : p.cache.v;
   float* floats = pair < H ? p.cache.k_scale : p.cache.v_scale;
-  const int chunks = p.cache.row_bytes / 16;  // 4 .. 32, a power of two
+  const int chunks = p.cache.row_bytes / 16;  // 8 .. 32, a power of two
   const int rows = 32 / chunks, lane = tid & 31, c = lane % chunks, r = lane / chunks;
   for (int base = 0; base < n; base += kCompactThreads) {
     const int m = min(kCompactThreads, n - base);

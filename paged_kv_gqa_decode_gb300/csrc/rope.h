@@ -27,7 +27,8 @@ struct RopeParams {
   float eps;
   int rows, axes, max_positions, R, interleaved, H_q, H_kv, D, BS;
   long long num_blocks;
-  int32_t* status;             // null, or: bit 0 a slot past the pool, bit 1 a position outside
+  int32_t* status;             // null, or: bit 0 a slot past the pool, bit 1 a position outside,
+                               // bit 2 a copy that did not come
 };
 
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream);

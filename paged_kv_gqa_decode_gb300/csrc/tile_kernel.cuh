@@ -47,9 +47,9 @@
 //
 // Trees (TREE; kernels of their own, so that the others stay as they are): a row is a
 // drafted token, sees the cached tokens before the tree as above and of the tree's tokens
-// those its mask has a bit for.  Only the one or two token tiles with drafted tokens look at
-// the bits, shifted to the tile's columns; there V rows without a bit in any row of the
-// piece (padding nodes) are zeroed too.
+// those its mask has a bit for.  Only the token tiles with drafted tokens (one or two for small trees,
+// up to 256 / BN + 1) look at the bits, shifted to the tile's columns; there V rows without a
+// bit in any row of the piece (padding nodes) are zeroed too.
 #pragma once
 
 #include <atomic>
@@ -87,8 +87,9 @@ struct TileShape {
   // Trees of head_dim 256 hold the query rows in tensor memory (128 of its columns): their
   // 64 KB are two more K/V tiles on the way, and the score product reads one operand less
   // from shared memory, whose bandwidth 64-token tiles otherwise exceed.  (A tile took 1800
-  // cycles, 430 of them waiting for tiles and 1200 issuing products, now 1500, 260 and 1060;
-  // four contexts of 100000 tokens 356 -> 324 us.)
+  // cycles, 430 of them waiting for tiles and 1200 issuing products, now 1500, 260 and 1060.
+  // Four contexts of 100000 tokens, both in turn on one GPU: 354 -> 323 us a pass after idle,
+  // 386 -> 362 in a loop, which the power cap holds at 1.6 to 1.8 GHz.)
   static constexpr bool kQTmem = TREE && D == 256;
   static constexpr int kSlots = D == 256 ? (kQTmem ? 7 : 5) : D == 64 ? 8 : 4;
   // The teams' warps, then the producers and the product warp.  A warp's tensor
@@ -183,7 +184,8 @@ __global__ void __launch_bounds__(TileShape<D, TEAMS, TREE>::kThreads,
   // [5] max lo, [6] min hi, [7] a row sees nothing: there may be tokens between min lo
   // and max hi that no row sees,
   // [8..32) warp sums of the tile search; then [8..16) a bit per query of the piece, set when
-  // a row sees its token (used with [7] only)
+  // a row sees its token (used with [7] only), in trees a bit per drafted token of the
+  // sequence, set when a row of the piece sees it
   uint32_t* sm_tmem = reinterpret_cast<uint32_t*>(sm_i);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
