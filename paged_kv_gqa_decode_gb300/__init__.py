@@ -300,24 +300,33 @@ def _owned_by(stream, like):
     """The context in which an output of a call on ``stream`` (None: the current one) is made: it is that
     stream's memory, as a block of the current stream's may still be in use there, or be
     given away again before the call's kernels have run."""
-    if stream is None or not like.is_cuda:
+    if stream is None or _where(like).type != "cuda":
         return contextlib.nullcontext()
     import torch
 
     if not isinstance(stream, torch.cuda.Stream):  # anything with a handle
         handle = int(stream.cuda_stream)
-        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle
-                  else torch.cuda.default_stream(like.device))
+        stream = (torch.cuda.ExternalStream(handle, device=_where(like)) if handle
+                  else torch.cuda.default_stream(_where(like)))
     return torch.cuda.stream(stream)
+
+
+def _where(like):
+    """The device of an output like ``like``: device memory beside a pinned input."""
+    import torch
+
+    if like.is_cuda or not like.is_pinned():
+        return like.device
+    return torch.device("cuda", torch.cuda.current_device())
 
 
 def _empty_like(like, stream):
     import torch
 
     if stream is None:
-        return torch.empty_like(like)
+        return torch.empty_like(like, device=_where(like))
     with _owned_by(stream, like):
-        return torch.empty_like(like)
+        return torch.empty_like(like, device=_where(like))
 
 
 def _sizes(q, k_cache, block_tables):
@@ -834,7 +843,7 @@ def paged_kv_assign(seq_lens, new_lens, block_tables, free_blocks, free_count, b
     _need("block_tables", block_tables, i32, (n, block_tables.shape[1]))
     _need("free_blocks", free_blocks, i32, (free_blocks.numel(),))
     _need("free_count", free_count, i32, (1,))
-    where = seq_lens.device
+    where = _where(seq_lens)
     if seq_lens_out is None:
         seq_lens_out = _empty_like(seq_lens, stream)
     else:

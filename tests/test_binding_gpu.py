@@ -157,7 +157,7 @@ def test_a_dropped_output_is_not_given_to_the_current_stream_at_once(call):
     del held
 
 
-@pytest.mark.parametrize("call", ["tree", "compact", "fork", "release"])
+@pytest.mark.parametrize("call", ["tree", "compact", "fork", "release", "assign", "mods", "multi_mods"])
 def test_outputs_made_beside_pinned_inputs_are_device_memory(call):
     want = getattr(Problem(), call)()
     p = Problem()
