@@ -66,7 +66,7 @@ CacheRows cache_rows(void* k_cache, void* v_cache, float* k_scale, float* v_scal
 }
 
 #ifdef PAGED_ATTN_WAIT_TEST
-thread_local long long g_test_skip_page = -1;
+thread_local long long g_test_skip_page = -1, g_test_skip_row = -1;
 #endif
 
 }  // namespace
@@ -79,6 +79,11 @@ using namespace pagedattn;
 // head page `page` that they do not issue (-1: off).
 extern "C" PAGED_ATTN_API int paged_attn_test_set_fork_fault(long long page) {
   g_test_skip_page = page;
+  return PAGED_ATTN_OK;
+}
+// The same for the copies of the queries of row `row` that the rotation streams.
+extern "C" PAGED_ATTN_API int paged_attn_test_set_rope_fault(long long row) {
+  g_test_skip_row = row;
   return PAGED_ATTN_OK;
 }
 #endif
@@ -152,6 +157,9 @@ int paged_kv_rope_append_slots(const void* q, const void* k_new, const void* v_n
   p.BS = block_size;
   p.num_blocks = num_blocks;
   p.status = api_check_status();
+#ifdef PAGED_ATTN_WAIT_TEST
+  p.test_skip_row = g_test_skip_row;
+#endif
   return done(launch_rope_append(p, sms, static_cast<cudaStream_t>(stream)));
 }
 

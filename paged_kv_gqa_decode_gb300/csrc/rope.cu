@@ -407,6 +407,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     if (lane == 0) {
       const uint32_t bytes = (uint32_t)x.heads * D * 2;
       mbar_arrive_expect_tx(&full[stage], bytes);
+#ifdef PAGED_ATTN_WAIT_TEST
+      if (x.kind == 0 && x.row == p.test_skip_row) return;  // (armed and never filled)
+#endif
       bulk_load(ring + stage * kUnitBytes, source(p, x), bytes, &full[stage]);
     }
   };
@@ -432,8 +435,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1)
     const Item next = behind(x);
     if (next.row != x.row && i + 1 < n) pos = positions_of(p, at, axes, next.row, true);
     if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
-      // never expected: no copy may be in flight when the CTA exits
-      for (int j = 1; j < kStages && i + j < n; ++j)
+      // never expected: no copy may be in flight when the CTA exits, the one that is late included
+      for (int j = 0; j < kStages && i + j < n; ++j)
         mbar_wait(&full[(stage + j) % kStages], stage + j >= kStages ? phase ^ 1u : phase);
       if (p.status != nullptr && lane == 0) atomicOr(p.status, kTimeout);
       return;

@@ -29,6 +29,10 @@ struct RopeParams {
   long long num_blocks;
   int32_t* status;             // null, or: bit 0 a slot past the pool, bit 1 a position outside,
                                // bit 2 a copy that did not come
+#ifdef PAGED_ATTN_WAIT_TEST
+  // Test build only: the copies of this row's queries are waited for and never issued.  -1: off.
+  long long test_skip_row;
+#endif
 };
 
 cudaError_t launch_rope_append(const RopeParams& p, int sms, cudaStream_t stream);
